@@ -6,6 +6,7 @@
  *   pa_cache_write  writes each new token's K and V into its paged slot;
  *   pa_forward      runs attention for every new token over its request's
  *                   KV, read through the request's block table.
+ * Beside them, pa_cache_read reads slots of a cache back.
  *
  * Sources (page title, section):
  *   "Inside vLLM: Anatomy of a High-Throughput LLM Inference System",
@@ -32,7 +33,8 @@
  *   - Shapes:  q, out        [num_tokens][num_q_heads][head_size]
  *              k, v          [num_tokens][num_kv_heads][head_size]
  *              k_cache, v_cache [num_blocks][block_size][num_kv_heads][head_size]
- *     Element type is layout->dtype, except the caches: layout->cache_dtype.
+ *     Element type is layout->dtype, except the caches: layout->cache_dtype
+ *     (a PA_INT4 cache has pages of its own, see pa_layout).
  *   - Return value: PA_OK, or an error code with a message for
  *     pa_last_error().  Argument errors are found on the host before anything
  *     is launched.  Values that live in device memory (slots, block ids,
@@ -57,7 +59,7 @@ typedef enum {
   PA_ERR_CUDA = 3          /* a CUDA runtime call or launch failed */
 } pa_status;
 
-typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
 
 /* Bits the kernels OR into the optional device status word. */
 #define PA_DEV_SLOT_RANGE 1   /* slot >= num_blocks*block_size: that token's write skipped */
@@ -71,13 +73,33 @@ typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
  * or 128; num_q_heads / num_kv_heads in {1, 2, 4, 8}.
  *   dtype        element type of q, out and the new k, v: PA_F32 or PA_BF16.
  *   cache_dtype  element type of k_cache / v_cache: equal to dtype, or
- *                PA_FP8_E4M3 with dtype PA_BF16 (8-bit KV; "Serving models at
+ *                PA_INT4 or PA_FP8_E4M3 with dtype PA_BF16 (8-bit KV; "Serving models at
  *                scale with vLLM", section Your model is too big: KV data can
  *                be kept at 8-bit precision).  An FP8 element holds
  *                code = E4M3(x / scale) (float32 division, round to nearest
  *                even, saturating at +-448) and stands for code * scale.
- *   k_scale, v_scale  the per-tensor scales of an FP8 cache (finite, > 0);
- *                ignored otherwise. */
+ *   k_scale, v_scale  the per-tensor scales of an FP8 or a 4-bit cache (finite,
+ *                > 0); ignored otherwise.
+ *
+ * A PA_INT4 cache holds 4-bit codes with an f16 scale s and zero z for every
+ * token, kv head and group of 32 head dims; code c stands for
+ * (c * s + z) * k_scale (v_scale for V).  For a group x_0 .. x_31 the write takes,
+ * in float32 with ties to even,
+ *   y = x / k_scale, saturated at +-PA_INT4_LIMIT (infinities too);
+ *   z = f16(min y);  s = f16((max y - min y) / 15);
+ *   c = (y - z) / s rounded to an integer and clamped to 0 .. 15; 0 where s is 0;
+ * and a group that holds a NaN reads back as NaN throughout.
+ * k_cache and v_cache are then [num_blocks][num_kv_heads][10 * head_size] bytes:
+ * a page per block and head, 8 * head_size bytes of codes and 2 * head_size of
+ * parameters.  With D = head_size and token t of the block:
+ *   K page: dim 32 g + 8 c + i in byte t D/2 + c D/8 + 4 g + i/2, nibble i % 2
+ *           (0: the low one); s of group g at 8 D + t D/8 + 2 g, z D/16 bytes on;
+ *   V page: dim e D/8 + i in byte (t/8) 4 D + e D/2 + ((t%8)/2) D/8 + 4 (i/4) + 2 (t%2)
+ *           + (i%4)/2, nibble i % 2;
+ *           s of group g at 8 D + 64 g + 16 ((t%8)/2) + 4 (t/8) + 2 (t%2), z 8 bytes on.
+ * Over a quantised cache (FP8 or 4-bit) attention takes q in f16: chunks of 16
+ * and more tokens want |q| <= 65504, and below 2^-14 it is rounded to a multiple
+ * of 2^-24; shorter queries over a 4-bit cache are scaled by a power of two first. */
 typedef struct {
   int num_q_heads;
   int num_kv_heads;
@@ -105,9 +127,25 @@ typedef struct {
  *   stream        cudaStream_t
  * num_tokens == 0 is a no-op.
  */
+#define PA_INT4_LIMIT 16384
 int pa_cache_write(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
                    void* k_cache, void* v_cache, const pa_layout* layout, int32_t* status,
                    void* stream);
+
+/*
+ * The reverse: for every t < num_tokens with s = slot_mapping[t] >= 0, k[t] and
+ * v[t] receive the values of slot s: the cache's bits where its type is
+ * layout->dtype, the value a code stands for rounded to bf16 otherwise.  For
+ * handing a request's KV to another instance or tier, or to a cache of another
+ * type (the pages name KV transfer between instances but give no interface).
+ * Rows of tokens with s < 0 are left as they were; so are those with
+ * s >= num_blocks*block_size, which set PA_DEV_SLOT_RANGE.  A slot may be named
+ * any number of times.  Alignment as for pa_cache_write; k and v must not
+ * overlap the caches.
+ */
+int pa_cache_read(const void* k_cache, const void* v_cache, const int64_t* slot_mapping,
+                  int num_tokens, void* k, void* v, const pa_layout* layout, int32_t* status,
+                  void* stream);
 
 /*
  * Bytes of device workspace pa_forward needs for a step with at most

@@ -14,7 +14,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpa.so")
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA = 0, 1, 2, 3
-PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
+PA_F32, PA_BF16, PA_FP8_E4M3, PA_INT4 = 0, 1, 2, 3
+PA_INT4_LIMIT = 16384  # |x / scale| saturates here in a 4-bit cache
 PA_DEV_SLOT_RANGE, PA_DEV_BLOCK_RANGE, PA_DEV_QSL, PA_DEV_LENGTHS, PA_DEV_CAPACITY = 1, 2, 4, 8, 16
 PA_DEV_TIMEOUT = 32
 
@@ -50,6 +51,8 @@ def lib() -> ctypes.CDLL:
         lp = ctypes.POINTER(pa_layout)
         L.pa_cache_write.argtypes = [vp, vp, vp, i32, vp, vp, lp, vp, vp]
         L.pa_cache_write.restype = i32
+        L.pa_cache_read.argtypes = [vp, vp, vp, i32, vp, vp, lp, vp, vp]
+        L.pa_cache_read.restype = i32
         L.pa_forward_workspace_size.argtypes = [lp, i32, i32, i32]
         L.pa_forward_workspace_size.restype = sz
         L.pa_forward.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float,
@@ -102,6 +105,17 @@ def _on_one_device(**tensors) -> None:
             raise PaError(PA_ERR_INVALID, f"{name} is on {t.device}, expected {dev}")
 
 
+def _int4_pages(layout: pa_layout, *caches) -> None:
+    """The caches of a 4-bit layout must have its pages (their size is not the
+    rows' size that the other types share)."""
+    if layout.cache_dtype != PA_INT4:
+        return
+    shape = cache_shape(layout)
+    for c in caches:
+        if c.dtype != torch.uint8 or tuple(c.shape) != shape:
+            raise PaError(PA_ERR_INVALID, f"a 4-bit cache is uint8 {shape}, got {c.dtype} {tuple(c.shape)}")
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -113,7 +127,8 @@ def _stream(stream) -> int | None:
 def make_layout(num_q_heads: int, num_kv_heads: int, head_size: int, num_blocks: int,
                 dtype, block_size: int = 16, cache_dtype=None, k_scale: float = 1.0,
                 v_scale: float = 1.0) -> pa_layout:
-    """Layout of a step; cache_dtype defaults to dtype (PA_FP8_E4M3 for an 8-bit cache)."""
+    """Layout of a step; cache_dtype defaults to dtype (PA_FP8_E4M3 for an 8-bit cache,
+    PA_INT4 for a 4-bit one)."""
     code = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
     if cache_dtype is None:
         ccode = code
@@ -128,8 +143,15 @@ def make_layout(num_q_heads: int, num_kv_heads: int, head_size: int, num_blocks:
 def layout_of(k_cache: torch.Tensor, num_q_heads: int, dtype=None, k_scale: float = 1.0,
               v_scale: float = 1.0) -> pa_layout:
     """Layout of a cache tensor [num_blocks][block_size][num_kv_heads][head_size].  A
-    uint8 cache holds FP8 (E4M3) codes; then `dtype` (of q/out, default bf16) and the
-    scales apply."""
+    uint8 cache of that shape holds FP8 (E4M3) codes, one of shape
+    [num_blocks][num_kv_heads][10 * head_size] the pages of a 4-bit cache; then
+    `dtype` (of q/out, default bf16) and the scales apply."""
+    if k_cache.dtype == torch.uint8 and k_cache.dim() == 3:
+        nb, hkv, page = k_cache.shape
+        if page % 10:
+            raise PaError(PA_ERR_INVALID, f"a 4-bit page of {page} bytes is not 10 * head_size")
+        return make_layout(num_q_heads, hkv, page // 10, nb, dtype or torch.bfloat16, 16, PA_INT4,
+                           k_scale, v_scale)
     nb, bs, hkv, d = k_cache.shape
     if k_cache.dtype == torch.uint8:
         return make_layout(num_q_heads, hkv, d, nb, dtype or torch.bfloat16, bs, PA_FP8_E4M3,
@@ -142,9 +164,37 @@ def pa_cache_write(k, v, slot_mapping, k_cache, v_cache, layout: pa_layout,
     """Write k[t], v[t] into slot slot_mapping[t] of the caches (in place)."""
     _on_one_device(k=k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache,
                    status=status)
+    _int4_pages(layout, k_cache, v_cache)
     _check(lib().pa_cache_write(_ptr(k), _ptr(v), _ptr(slot_mapping), int(k.shape[0]),
                                 _ptr(k_cache), _ptr(v_cache), ctypes.byref(layout),
                                 _ptr(status), _stream(stream)))
+
+
+def cache_shape(layout: pa_layout) -> tuple:
+    """Shape of the k_cache / v_cache tensors of a layout (uint8 for FP8 and 4-bit caches)."""
+    if layout.cache_dtype == PA_INT4:
+        return (layout.num_blocks, layout.num_kv_heads, 10 * layout.head_size)
+    return (layout.num_blocks, layout.block_size, layout.num_kv_heads, layout.head_size)
+
+
+def pa_cache_read(k_cache, v_cache, slot_mapping, k, v, layout: pa_layout,
+                  status: torch.Tensor | None = None, stream=None) -> None:
+    """Read slot slot_mapping[t] of the caches into k[t], v[t] (in place); the
+    values of a quantised cache come rounded to layout.dtype."""
+    _on_one_device(k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, k=k, v=v,
+                   status=status)
+    _int4_pages(layout, k_cache, v_cache)
+    n = int(slot_mapping.shape[0])
+    row = layout.num_kv_heads * layout.head_size
+    if slot_mapping.dtype != torch.int64:
+        raise PaError(PA_ERR_INVALID, f"slot_mapping is {slot_mapping.dtype}, expected torch.int64")
+    for name, t in (("k", k), ("v", v)):
+        if t.numel() != n * row or _DTYPES.get(t.dtype) != layout.dtype:
+            raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, expected {n} rows of "
+                                          f"{row} elements of the layout's dtype")
+    _check(lib().pa_cache_read(_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+                               n, _ptr(k), _ptr(v), ctypes.byref(layout),
+                               _ptr(status), _stream(stream)))
 
 
 def pa_forward_workspace_size(layout: pa_layout, num_seqs: int, num_tokens: int,
@@ -163,6 +213,7 @@ def pa_forward(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
     _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
                    seq_lens=seq_lens, query_start_loc=query_start_loc, out=out,
                    workspace=workspace, status=status)
+    _int4_pages(layout, k_cache, v_cache)
     _check(lib().pa_forward(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                             int(block_tables.shape[1]), _ptr(seq_lens), _ptr(query_start_loc),
                             int(seq_lens.shape[0]), int(q.shape[0]), int(max_query_len),
@@ -178,6 +229,7 @@ def pa_forward_noalloc(q, k_cache, v_cache, block_tables, seq_lens, query_start_
     caller workspace (for callers that cannot allocate device memory)."""
     _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
                    seq_lens=seq_lens, query_start_loc=query_start_loc, out=out, status=status)
+    _int4_pages(layout, k_cache, v_cache)
     _check(lib().pa_forward_noalloc(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                     int(block_tables.shape[1]), _ptr(seq_lens),
                                     _ptr(query_start_loc), int(seq_lens.shape[0]), int(q.shape[0]),

@@ -48,9 +48,11 @@ int fail_cuda(cudaError_t e, const char* what) {
   return fail(PA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-int elem_bytes(pa_dtype t) { return t == PA_FP8_E4M3 ? 1 : (t == PA_BF16 ? 2 : 4); }
+int elem_bytes(pa_dtype t) { return t == PA_BF16 ? 2 : 4; }  // of q, k, v, out
 
 bool fp8_cache(const pa_layout* L) { return L->cache_dtype == PA_FP8_E4M3; }
+bool int4_cache(const pa_layout* L) { return L->cache_dtype == PA_INT4; }
+bool quantised(const pa_layout* L) { return L->cache_dtype != L->dtype; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -61,14 +63,15 @@ int check_layout(const pa_layout* L) {
   if (L->dtype != PA_F32 && L->dtype != PA_BF16)
     return fail(PA_ERR_INVALID, "dtype %d is not PA_F32 or PA_BF16", static_cast<int>(L->dtype));
   if (L->cache_dtype != L->dtype) {
-    if (L->cache_dtype != PA_FP8_E4M3)
-      return fail(PA_ERR_INVALID, "cache_dtype %d must equal dtype or be PA_FP8_E4M3",
+    if (L->cache_dtype != PA_FP8_E4M3 && L->cache_dtype != PA_INT4)
+      return fail(PA_ERR_INVALID, "cache_dtype %d must equal dtype or be PA_FP8_E4M3 or PA_INT4",
                   static_cast<int>(L->cache_dtype));
     if (L->dtype != PA_BF16)
-      return fail(PA_ERR_UNSUPPORTED, "an FP8 cache is built for bf16 q/k/v only");
+      return fail(PA_ERR_UNSUPPORTED, "an %s cache is built for bf16 q/k/v only",
+                  L->cache_dtype == PA_INT4 ? "INT4" : "FP8");
     if (!(std::isfinite(L->k_scale) && L->k_scale > 0.f && std::isfinite(L->v_scale) &&
           L->v_scale > 0.f))
-      return fail(PA_ERR_INVALID, "FP8 cache scales must be finite and positive");
+      return fail(PA_ERR_INVALID, "FP8 and INT4 cache scales must be finite and positive");
   }
   if (L->num_q_heads <= 0 || L->num_kv_heads <= 0 || L->head_size <= 0 || L->num_blocks <= 0)
     return fail(PA_ERR_INVALID, "heads, head_size and num_blocks must be positive");
@@ -85,6 +88,30 @@ int check_layout(const pa_layout* L) {
   if (static_cast<long long>(L->num_blocks) * kBlockSize > (1LL << 40))
     return fail(PA_ERR_INVALID, "num_blocks %d too large", L->num_blocks);
   return PA_OK;
+}
+
+// The tensor arguments of a slot write or read-back.
+int check_slot_call(const void* k, const void* v, const int64_t* slot_mapping, const void* k_cache,
+                    const void* v_cache, const int32_t* status) {
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache)
+    return fail(PA_ERR_INVALID, "null tensor pointer");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return fail(PA_ERR_INVALID, "k, v, k_cache and v_cache must be 16-byte aligned");
+  if (!aligned(slot_mapping, 8)) return fail(PA_ERR_INVALID, "slot_mapping must be 8-byte aligned");
+  if (status && !aligned(status, 4)) return fail(PA_ERR_INVALID, "status must be 4-byte aligned");
+  return PA_OK;
+}
+
+// The decode (positions 1) or few-token attention kernel of the cache's type.
+cudaError_t launch_attn(const AttnParams& p, const pa_layout* L, int positions, bool keys_as_m,
+                        int num_sms, cudaStream_t stream, int* grid_only = nullptr) {
+  const int group = L->num_q_heads / L->num_kv_heads;
+  if (int4_cache(L))
+    return launch_attn_int4(p, L->head_size, group, positions, num_sms, stream, grid_only);
+  if (fp8_cache(L))
+    return launch_attn_fp8(p, L->head_size, group, positions, num_sms, stream, grid_only);
+  return launch_attn_by_dtype(p, L->dtype, L->head_size, group, positions, keys_as_m, num_sms, stream,
+                              grid_only);
 }
 
 #ifndef PA_SPLIT_BLOCKS
@@ -253,15 +280,15 @@ int pa_cache_write(const void* k, const void* v, const int64_t* slot_mapping, in
   if (int rc = check_layout(layout)) return rc;
   if (num_tokens < 0) return fail(PA_ERR_INVALID, "num_tokens %d < 0", num_tokens);
   if (num_tokens == 0) return PA_OK;
-  if (!k || !v || !slot_mapping || !k_cache || !v_cache)
-    return fail(PA_ERR_INVALID, "null tensor pointer");
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
-    return fail(PA_ERR_INVALID, "k, v, k_cache and v_cache must be 16-byte aligned");
-  if (!aligned(slot_mapping, 8)) return fail(PA_ERR_INVALID, "slot_mapping must be 8-byte aligned");
-  if (status && !aligned(status, 4)) return fail(PA_ERR_INVALID, "status must be 4-byte aligned");
+  if (int rc = check_slot_call(k, v, slot_mapping, k_cache, v_cache, status)) return rc;
   const int row_bytes = layout->num_kv_heads * layout->head_size * elem_bytes(layout->dtype);
   const long long num_slots = static_cast<long long>(layout->num_blocks) * kBlockSize;
-  if (fp8_cache(layout) && !aligned(k_cache, 8)) return fail(PA_ERR_INVALID, "cache alignment");
+  if (int4_cache(layout)) {
+    const cudaError_t e4 = launch_cache_write_int4(
+        k, v, slot_mapping, num_tokens, k_cache, v_cache, layout->num_kv_heads, layout->head_size,
+        num_slots, layout->k_scale, layout->v_scale, status, static_cast<cudaStream_t>(stream));
+    return e4 == cudaSuccess ? static_cast<int>(PA_OK) : fail_cuda(e4, "cache write launch");
+  }
   cudaError_t e = fp8_cache(layout)
                       ? launch_cache_write_fp8(k, v, slot_mapping, num_tokens, k_cache, v_cache,
                                                row_bytes, num_slots, layout->k_scale,
@@ -272,6 +299,30 @@ int pa_cache_write(const void* k, const void* v, const int64_t* slot_mapping, in
                                            static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, "cache write launch");
   return PA_OK;
+}
+
+int pa_cache_read(const void* k_cache, const void* v_cache, const int64_t* slot_mapping,
+                  int num_tokens, void* k, void* v, const pa_layout* layout, int32_t* status,
+                  void* stream) {
+  g_last_error.clear();
+  if (int rc = check_layout(layout)) return rc;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID, "num_tokens %d < 0", num_tokens);
+  if (num_tokens == 0) return PA_OK;
+  if (int rc = check_slot_call(k, v, slot_mapping, k_cache, v_cache, status)) return rc;
+  const int row_bytes = layout->num_kv_heads * layout->head_size * elem_bytes(layout->dtype);
+  const long long num_slots = static_cast<long long>(layout->num_blocks) * kBlockSize;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      int4_cache(layout)
+          ? launch_cache_read_int4(k_cache, v_cache, slot_mapping, num_tokens, k, v,
+                                   layout->num_kv_heads, layout->head_size, num_slots,
+                                   layout->k_scale, layout->v_scale, status, st)
+      : fp8_cache(layout)
+          ? launch_cache_read_fp8(k_cache, v_cache, slot_mapping, num_tokens, k, v, row_bytes,
+                                  num_slots, layout->k_scale, layout->v_scale, status, st)
+          : launch_cache_read(k_cache, v_cache, slot_mapping, num_tokens, k, v, row_bytes, num_slots,
+                              status, st);
+  return e == cudaSuccess ? static_cast<int>(PA_OK) : fail_cuda(e, "cache read launch");
 }
 
 size_t pa_forward_workspace_size(const pa_layout* layout, int num_seqs, int num_tokens,
@@ -342,7 +393,7 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
   pp.max_blocks_per_seq = max_blocks_per_seq;
   pp.bps = blocks_per_split(layout);
   pp.num_sms = num_sms;
-  const bool tc_prefill = layout->dtype == PA_BF16;  // bf16 or FP8 cache
+  const bool tc_prefill = layout->dtype == PA_BF16;  // bf16, FP8 or 4-bit cache
   const bool run_prefill = tc_prefill && max_query_len >= kPrefillMinQlen;
   // bf16 decode tiles: keys as the MMA's M dimension when the step also runs
   // the tensor-core prefill kernel (the decode kernel then shares the GPU and
@@ -351,10 +402,7 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
   const bool keys_as_m = run_prefill;
   {
     AttnParams none{};
-    e = fp8_cache(layout)
-            ? launch_attn_fp8(none, layout->head_size, group, 1, num_sms, st, &pp.num_ctas)
-            : launch_attn_by_dtype(none, layout->dtype, layout->head_size, group, 1, keys_as_m,
-                                   num_sms, st, &pp.num_ctas);
+    e = launch_attn(none, layout, 1, keys_as_m, num_sms, st, &pp.num_ctas);
     if (e != cudaSuccess) return fail_cuda(e, "decode grid size");
   }
   pp.small_positions = small_positions(layout);
@@ -392,8 +440,8 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
   ap.num_kv_heads = layout->num_kv_heads;
   ap.num_blocks = layout->num_blocks;
   ap.num_tokens = num_tokens;
-  ap.scale_log2 = scale * 1.4426950408889634f * (fp8_cache(layout) ? layout->k_scale : 1.f);
-  ap.out_scale = fp8_cache(layout) ? layout->v_scale : 1.f;
+  ap.scale_log2 = scale * 1.4426950408889634f * (quantised(layout) ? layout->k_scale : 1.f);
+  ap.out_scale = quantised(layout) ? layout->v_scale : 1.f;
   ap.status = status;
 
   if (run_prefill) {
@@ -415,7 +463,7 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
       pst = side->stream;
     }
     if (g_pf_prof_start) cudaEventRecord(g_pf_prof_start, pst);
-    e = launch_prefill_tc(pf, layout->head_size, group, num_sms, fp8_cache(layout), pst);
+    e = launch_prefill_tc(pf, layout->head_size, group, num_sms, layout->cache_dtype, pst);
     if (e != cudaSuccess) return fail_cuda(e, "prefill attention launch");
     if (g_pf_prof_stop) cudaEventRecord(g_pf_prof_stop, pst);
     if (fork) {
@@ -436,10 +484,7 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
   ap.part_acc = reinterpret_cast<float*>(ws + lay.part_acc_d);
   ap.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_d);
   if (g_prof_start) cudaEventRecord(g_prof_start, st);
-  e = fp8_cache(layout)
-          ? launch_attn_fp8(ap, layout->head_size, group, 1, num_sms, st)
-          : launch_attn_by_dtype(ap, layout->dtype, layout->head_size, group, 1, keys_as_m, num_sms,
-                                 st);
+  e = launch_attn(ap, layout, 1, keys_as_m, num_sms, st);
   if (e != cudaSuccess) return fail_cuda(e, "decode attention launch");
   if (g_prof_stop) cudaEventRecord(g_prof_stop, st);
 
@@ -454,10 +499,7 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
     ap.merge_cnt = reinterpret_cast<int*>(ws + lay.cnt_s);
     ap.part_acc = reinterpret_cast<float*>(ws + lay.part_acc_s);
     ap.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_s);
-    e = fp8_cache(layout)
-            ? launch_attn_fp8(ap, layout->head_size, group, small_positions(layout), num_sms, st)
-            : launch_attn_by_dtype(ap, layout->dtype, layout->head_size, group,
-                                   small_positions(layout), false, num_sms, st);
+    e = launch_attn(ap, layout, small_positions(layout), false, num_sms, st);
     if (e != cudaSuccess) return fail_cuda(e, "small-q attention launch");
   }
   if (fork) {

@@ -16,6 +16,7 @@ constexpr int kPrefillRows = 128;     // query rows per tensor-core prefill tile
 constexpr int kPrefillMinQlen = 16;   // bf16 chunks at least this long use the tensor-core kernel
 constexpr int kSmallStepUnits = 2048; // extra decode units (items x kv heads) a workspace holds
                                       // for the finer splits of small steps
+constexpr int kInt4PageBytesPerDim = 10;  // bytes of a 4-bit page (block x kv head) per head dim
 constexpr int kPrefillKeys = 128;     // keys per KV tile of the tensor-core prefill kernel
 // Tensor-core prefill scheduling (see the plan kernel).  A unit is (query tile,
 // kv head); its KV tiles may be cut into pieces, each at least
@@ -121,8 +122,8 @@ struct AttnParams {
   void* out;
   int max_blocks_per_seq;
   int num_q_heads, num_kv_heads, num_blocks, num_tokens;
-  float scale_log2;      // softmax scale * log2(e) (times k_scale for an FP8 cache)
-  float out_scale;       // applied to the normalised output (v_scale for an FP8 cache)
+  float scale_log2;      // softmax scale * log2(e) (times k_scale for a quantised cache)
+  float out_scale;       // applied to the normalised output (v_scale for a quantised cache)
   const int* n_items;    // device count of work items (x num_kv_heads units)
   int after_plan;        // host side: launch with a programmatic dependency on the plan
   int* next;             // device work counter (zeroed by the plan kernel)
@@ -152,11 +153,30 @@ cudaError_t launch_cache_write_fp8(const void* k, const void* v, const int64_t* 
                                    int num_tokens, void* k_cache, void* v_cache, int row_bytes,
                                    long long num_slots, float k_scale, float v_scale,
                                    int32_t* status, cudaStream_t stream);
+// Quantising slot write into a 4-bit cache (pa_int4.cuh).
+cudaError_t launch_cache_write_int4(const void* k, const void* v, const int64_t* slot_mapping,
+                                    int num_tokens, void* k_cache, void* v_cache, int num_kv_heads,
+                                    int head_size, long long num_slots, float k_scale,
+                                    float v_scale, int32_t* status, cudaStream_t stream);
+// Read-back of slots: by copy (row_bytes a cache row), from an FP8 cache
+// (row_bytes the bf16 row) and from a 4-bit cache.
+cudaError_t launch_cache_read(const void* k_cache, const void* v_cache, const int64_t* slot_mapping,
+                              int num_tokens, void* k, void* v, int row_bytes, long long num_slots,
+                              int32_t* status, cudaStream_t stream);
+cudaError_t launch_cache_read_fp8(const void* k_cache, const void* v_cache,
+                                  const int64_t* slot_mapping, int num_tokens, void* k, void* v,
+                                  int row_bytes, long long num_slots, float k_scale, float v_scale,
+                                  int32_t* status, cudaStream_t stream);
+cudaError_t launch_cache_read_int4(const void* k_cache, const void* v_cache,
+                                   const int64_t* slot_mapping, int num_tokens, void* k, void* v,
+                                   int num_kv_heads, int head_size, long long num_slots,
+                                   float k_scale, float v_scale, int32_t* status,
+                                   cudaStream_t stream);
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 // Tensor-core (tcgen05) chunked-prefill attention over the prefill list
-// (bf16 q/out; a bf16 or an FP8 (E4M3) cache).
+// (bf16 q/out; a bf16, an FP8 (E4M3) or a 4-bit cache).
 cudaError_t launch_prefill_tc(const AttnParams& p, int head_size, int group, int num_sms,
-                              bool fp8_cache, cudaStream_t stream);
+                              pa_dtype cache_dtype, cudaStream_t stream);
 // Split-KV attention over the decode or few-token list, by element type:
 // bf16 runs the warp-level tensor-core (mma.sync) kernel, fp32 the CUDA-core
 // kernel.  positions: 1 (decode list) or the few-token tile height.
@@ -171,5 +191,8 @@ cudaError_t launch_attn_by_dtype(const AttnParams& p, pa_dtype dtype, int head_s
 // bf16 q/out over an FP8 (E4M3) cache (tensor-core decode and few-token tiles).
 cudaError_t launch_attn_fp8(const AttnParams& p, int head_size, int group, int positions,
                             int num_sms, cudaStream_t stream, int* grid_only = nullptr);
+// bf16 q/out over a 4-bit cache (decode and few-token tiles).
+cudaError_t launch_attn_int4(const AttnParams& p, int head_size, int group, int positions,
+                             int num_sms, cudaStream_t stream, int* grid_only = nullptr);
 
 }  // namespace pa

@@ -34,6 +34,11 @@
 // the V buffers themselves) and the softmax warps widen them to f16, one
 // 16-token block per warp, while they work on the tile before; the products
 // run as kind::f16.
+// A 4-bit cache (pa_int4.cuh) goes the same way: a block's page is one bulk copy,
+// and widening turns codes into values, v = fma(16 + c, s, z - 16 s) in f16 (16 + c:
+// the code in the top mantissa bits of 16.0).  Its head dims come out of the words
+// as 0, 4, 1, 5, 2, 6, 3, 7 of every eight; Q takes that order too, and the output's
+// columns are put back as they are written.
 // Hand-offs are mbarriers; every wait is bounded and a timeout makes the whole
 // CTA stop (status PA_DEV_TIMEOUT), drain its copies and MMAs, and free TMEM.
 #include <cuda.h>
@@ -44,6 +49,7 @@
 #include <mutex>
 
 #include "pa_device.cuh"
+#include "pa_int4.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
 
@@ -81,17 +87,22 @@ struct PfCfg {
   // ahead of its widening; V codes go into the upper half of each block's
   // region of the V buffer they are widened into (one warp widens a block in
   // place), so a V copy starts as soon as PV has read that buffer.
-  static constexpr int kCodeBytes = kTileN * D;
+  // A 4-bit cache: the same with pages of 10 D bytes, V pages at the end of
+  // each block's region.
   static constexpr int kKCodeOff = kVOff + 2 * kTileBytes;
-  static constexpr int kSmemBytesF8 = kKCodeOff + 2 * kCodeBytes + 1024;
+  static constexpr int code_block(pa_dtype kv) {  // bytes of a block's codes
+    return kv == PA_INT4 ? I4Page<D>::kBytes : kBlockSize * D;
+  }
+  static constexpr int code_tile(pa_dtype kv) { return kTileN / kBlockSize * code_block(kv); }
+  static constexpr int smem_bytes(pa_dtype kv) {
+    return kv == PA_BF16 ? kSmemBytes : kKCodeOff + 2 * code_tile(kv) + 1024;
+  }
   // S0, S1 (consecutive tiles) at 0 / 128, each tile's P (bf16 pairs) over the
   // first 64 columns of its S once read; O at 256
   static constexpr int kTmemCols = 512;
   static_assert(D == 64 || D == 128, "head size 64 or 128");
   static_assert(kTileN == kTileM, "K and V tiles share the Q tile geometry");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
-  // (4 KB: the kernel's static shared memory)
-  static_assert(kSmemBytesF8 + 4096 <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
 };
 
 // mbarriers.  [2] = one per buffer parity (tile t uses buffers t & 1 of S,
@@ -306,9 +317,105 @@ __device__ __forceinline__ void widen_blocks(uint32_t src, uint32_t src_stride, 
     }
 }
 
+// Values of nibble J of both halves of w as f16: (code s + z) of either half.
+template <int J>
+__device__ __forceinline__ uint32_t int4_values(uint32_t w, uint32_t s, uint32_t z16) {
+  constexpr int sh = 6 - 4 * J;  // the nibble goes to bits 6-9 of 16.0
+  const uint32_t x = sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh >= 0 ? 0 : -sh);
+  const uint32_t c = (x & 0x03c003c0u) | 0x4c004c00u;
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(c), "r"(s), "r"(z16));
+  return r;
+}
+// z - 16 s of an f16 pair
+__device__ __forceinline__ uint32_t int4_offset(uint32_t s, uint32_t z) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(s), "r"(0xcc00cc00u), "r"(z));
+  return r;
+}
+__device__ __forceinline__ void st_shared_int4(uint32_t addr, uint32_t w, uint32_t s, uint32_t z16) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(int4_values<0>(w, s, z16)),
+               "r"(int4_values<1>(w, s, z16)), "r"(int4_values<2>(w, s, z16)),
+               "r"(int4_values<3>(w, s, z16))
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+}
+
+// 4-bit: one page of K at src to f16 at dst, in the K layout above; one warp.
+// A lane takes one run (8 dims of every group) of tokens t and t + 8.  Rows t
+// and t ^ 5 share each quarter-warp: their loads (64 bytes a row) and their
+// stores (swizzled by row) then hit distinct banks.
+template <int D>
+__device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lane) {
+  using C = PfCfg<D>;
+  using Pg = I4Page<D>;
+  constexpr int NG = Pg::kGroups;
+  const int c = lane & 3;
+  const int t = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
+  uint32_t w[2][NG], q[2][NG];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    ld_shared_words<NG>(src + Pg::k_word(t + 8 * h, 0, c), w[h]);
+    ld_shared_words<NG>(src + Pg::k_scale(t + 8 * h, 0), q[h]);  // scales, then zeros
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const uint32_t sel = (g & 1) ? 0x3232u : 0x1010u;
+      const uint32_t s = __byte_perm(q[h][g / 2], 0, sel);
+      const uint32_t z16 = int4_offset(s, __byte_perm(q[h][NG / 2 + g / 2], 0, sel));
+      const int ch = 4 * g + c;  // 16-byte chunk of the row
+      st_shared_int4(dst + h * C::kKGroupBytes + (ch >> 3) * 1024 + t * 128 + (((ch & 7) ^ t) << 4),
+                     w[h][g], s, z16);
+    }
+}
+
+// 4-bit: one page of V at src (which may be the end of the block's own region)
+// to f16 at dst, in the V layout above; rows from `rows` on become zeros.  A lane
+// takes one run of each token pair (2c, 2c + 1) + 8 h.
+template <int D>
+__device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int rows, int lane) {
+  using Pg = I4Page<D>;
+  constexpr int NG = Pg::kGroups;
+  const int e = lane >> 2, c = lane & 3;
+  uint32_t w[2][NG], q[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    ld_shared_words<NG>(src + h * 4 * D + e * (D / 2) + c * Pg::kRun, w[h]);
+  ld_shared_words<4>(src + Pg::kCodeBytes + (e * Pg::kRun / 32) * 64 + c * 16, q);
+  __syncwarp();  // every load, before any store
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = 2 * c + 8 * h;
+    const uint32_t keep = rows >= t + 2 ? 0xffffffffu : (rows == t + 1 ? 0x0000ffffu : 0u);
+    const uint32_t s2 = q[h] & keep, z2 = int4_offset(s2, q[2 + h] & keep);
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int ch = e * (NG / 2) + i;
+        const uint32_t sel = b ? 0x3232u : 0x1010u;
+        st_shared_int4(dst + (ch >> 3) * (kBlockSize * 128) + (t + b) * 128 +
+                           (((ch & 7) ^ ((t + b) & 7)) << 4),
+                       __byte_perm(w[h][2 * i], w[h][2 * i + 1], b ? 0x7632u : 0x5410u),
+                       __byte_perm(s2, 0, sel), __byte_perm(z2, 0, sel));
+      }
+  }
+}
+
 }  // namespace
 
-// F8: the cache holds E4M3 codes.  K codes are copied by TMA into two
+// KV: the cache's type.  CODES: it holds FP8 or 4-bit codes.  K codes are copied into two
 // staging buffers, two tiles ahead, V codes into the V tile buffers they are
 // widened in; both are widened to f16 (exactly) in the K / V tile buffers, a
 // unit's first two K tiles by the K loader and every other tile by the
@@ -316,11 +423,14 @@ __device__ __forceinline__ void widen_blocks(uint32_t src, uint32_t src_stride, 
 // once per unit, and the two products run as kind::f16 with f16 operands (P
 // in f16).  The K scale is folded into the softmax scale and the V scale
 // into the normalisation.
-template <int D, int G, bool F8>
+template <int D, int G, pa_dtype KV>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_tc_kernel(const AttnParams p, const __grid_constant__ PfMaps maps) {
   using C = PfCfg<D>;
   constexpr int PM = kTileM / G;  // positions per unit
+  constexpr bool CODES = KV != PA_BF16, I4 = KV == PA_INT4;
+  constexpr int kCodeBlock = C::code_block(KV), kCodeTile = C::code_tile(KV);
+  constexpr int kVCodeOff = C::kVBlockBytes - kCodeBlock;  // V codes in their block's region
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ UnitInfo s_units[2];
@@ -339,7 +449,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), bar_count<F8>(i));
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), bar_count<CODES>(i));
     s_abort = 0;
     mbar_fence_init();
   }
@@ -349,10 +459,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
+  // KV block `lane` of tile t
+  auto lb_of = [&](int t) { return t * (kTileN / kBlockSize) + lane; };
   // Physical block of KV block `lane` (< 8) of tile t, -1 past the unit's
   // keys; checked where it is used, so the load's latency stays hidden.
   auto tile_phys = [&](const UnitInfo& u, int t) {
-    const int lb = t * (kTileN / kBlockSize) + lane;
+    const int lb = lb_of(t);
     if (lane < kTileN / kBlockSize && lb * kBlockSize < u.kv_end)
       return __ldg(p.block_tables + static_cast<long long>(u.r) * p.max_blocks_per_seq + lb);
     return -1;
@@ -367,15 +479,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       flag_error(p.status, PA_DEV_BLOCK_RANGE);
       ph = -1;
     }
-    if constexpr (F8) {
+    if constexpr (I4) {
+      // the pages, K into the staging buffer at dst, V to the ends of the blocks'
+      // regions; a bad table entry leaves a page of zeros (its scales and zeros
+      // too), a block past the unit's keys what was there (K is masked, V rows
+      // past the last key are zeroed as they are widened)
+      const bool have = lane < kTileN / kBlockSize && ph >= 0;
+      const bool bad = lane < kTileN / kBlockSize && lb_of(t) * kBlockSize < u.kv_end && !have;
+      const uint32_t d = dst + lane * (is_v ? C::kVBlockBytes : kCodeBlock) + (is_v ? kVCodeOff : 0);
+      if (bad) {
+        flag_error(p.status, PA_DEV_BLOCK_RANGE);
+        for (int i = 0; i < kCodeBlock / 16; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(d + i * 16), "r"(0u) : "memory");
+        fence_proxy_async_smem();  // before a later copy to this place
+      }
+      const int copies = __popc(__ballot_sync(0xffffffffu, have));
+      if (lane == 0) mbar_arrive_expect_tx(full, copies * kCodeBlock);
+      __syncwarp();
+      if (have)
+        bulk_load(d,
+                  static_cast<const unsigned char*>(is_v ? p.v_cache : p.k_cache) +
+                      (static_cast<long long>(ph) * p.num_kv_heads + u.g) * kCodeBlock,
+                  kCodeBlock, full);
+      return;
+    }
+    if constexpr (CODES) {
       // the codes, [16 rows][D bytes] per block: K into the staging buffer
       // at dst, V into the upper half of each block's region of the V
       // buffer at dst
-      if (lane == 0) mbar_arrive_expect_tx(full, C::kCodeBytes);
+      if (lane == 0) mbar_arrive_expect_tx(full, kCodeTile);
       __syncwarp();
       if (lane < kTileN / kBlockSize) {
         const int coord = ph < 0 ? p.num_blocks : ph;
-        const uint32_t d = is_v ? dst + lane * C::kVBlockBytes + C::kVBlockBytes / 2
+        const uint32_t d = is_v ? dst + lane * C::kVBlockBytes + kVCodeOff
                                 : dst + lane * kBlockSize * D;
         tma_load_3d(d, is_v ? &maps.v : &maps.k, 0, 0,
                     coord * kBlockSize * p.num_kv_heads + u.g, full);
@@ -405,14 +541,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                    : "memory");
     }
   };
-  // FP8: widen a tile of codes at src (blocks src_stride bytes apart) to f16
-  // at dst (one warp)
-  auto widen_tile = [&](uint32_t src, uint32_t src_stride, uint32_t dst, bool is_v) {
+  // Codes: widen a tile of K codes at src to f16 at dst (one warp)
+  auto widen_k_tile = [&](uint32_t src, uint32_t dst) {
+    if constexpr (I4) {
+#pragma unroll 2
+      for (int b = 0; b < kTileN / kBlockSize; ++b)
+        widen_k_int4<D>(src + b * kCodeBlock, dst + b * C::kVBlockBytes, lane);
+    } else {
 #pragma unroll 1
-    for (int b = 0; b < kTileN / kBlockSize; b += 2)
-      widen_blocks<D, 2>(src, src_stride, dst, is_v, b, lane);
+      for (int b = 0; b < kTileN / kBlockSize; b += 2)
+        widen_blocks<D, 2>(src, kCodeBlock, dst, false, b, lane);
+    }
   };
-  // FP8: the landed bf16 Q tile to f16, in place (an element keeps its slot)
+  // Codes: the landed bf16 Q tile to f16, in place (FP8: an element keeps its
+  // slot; 4-bit: the order of the widened K within every eight)
   auto q_to_f16 = [&]() {
 #pragma unroll 4
     for (int i = lane; i < C::kTileBytes / 16; i += 32) {
@@ -425,8 +567,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
       uint32_t h[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        h[e] = pack_f16(__uint_as_float(wd[e] << 16), __uint_as_float(wd[e] & 0xffff0000u));
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (I4) {
+          const uint32_t a = wd[e >> 1], b = wd[2 + (e >> 1)];  // elements e and e + 4
+          h[e] = (e & 1) ? pack_f16(bf16_hi(a), bf16_hi(b)) : pack_f16(bf16_lo(a), bf16_lo(b));
+        } else {
+          h[e] = pack_f16(__uint_as_float(wd[e] << 16), __uint_as_float(wd[e] & 0xffff0000u));
+        }
+      }
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(h[0]), "r"(h[1]),
                    "r"(h[2]), "r"(h[3])
                    : "memory");
@@ -529,7 +677,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if ((b ? kp1 : kp0) &&
             !wait_bar(bar(kKStFree + b), ((b ? ks1 : ks0) - 1) & 1, abort, p.status))
           return false;
-        copy_kv_tile(u, tile_of(u, sq), ph, false, sbase + C::kKCodeOff + b * C::kCodeBytes,
+        copy_kv_tile(u, tile_of(u, sq), ph, false, sbase + C::kKCodeOff + b * kCodeTile,
                      bar(kKLand + b));
         const bool soft = sq >= 2;
         if (b) {
@@ -544,11 +692,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         return true;
       };
       bool ok = true;
-      if constexpr (F8) ok = copy_codes(0) && (u.n_kv < 2 || copy_codes(1));  // ahead of Q
+      if constexpr (CODES) ok = copy_codes(0) && (u.n_kv < 2 || copy_codes(1));  // ahead of Q
       if (!ok) break;
       // Q tile: rows (position, head) of 128/G tokens x G heads, one box per 64 columns
       if (uc > 0 && !wait_bar(bar(kQEmpty), (uc - 1) & 1, abort, p.status)) break;
-      const uint32_t q_bar = F8 ? bar(kQLand) : bar(kQFull);
+      const uint32_t q_bar = CODES ? bar(kQLand) : bar(kQFull);
       if (lane == 0) {
         mbar_arrive_expect_tx(q_bar, C::kTileBytes);
 #pragma unroll
@@ -557,8 +705,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                       u.a + u.j0, q_bar);
       }
       ++nq;
-      q_wait = F8;
-      if constexpr (F8) {  // Q to f16 while the codes are on their way
+      q_wait = CODES;
+      if constexpr (CODES) {  // Q to f16 while the codes are on their way
         if (!wait_bar(bar(kQLand), (nq - 1) & 1, abort, p.status)) {
           ok = false;
         } else {
@@ -567,7 +715,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (lane == 0) mbar_arrive(bar(kQFull));
         }
       }
-      if constexpr (F8) {
+      if constexpr (CODES) {
         // the first two tiles into K buffers 0 / 1 (freed by the previous
         // unit: its last S of each parity was waited below), then every
         // later tile's codes as their staging buffer frees up
@@ -575,8 +723,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const uint32_t i = c0 + sq;
           ++nf[sq];
           if (!wait_bar(bar(kKLand + (i & 1)), (i >> 1) & 1, abort, p.status)) { ok = false; break; }
-          widen_tile(sbase + C::kKCodeOff + (i & 1) * C::kCodeBytes, kBlockSize * D,
-                     sbase + C::kKOff + sq * C::kTileBytes, false);
+          widen_k_tile(sbase + C::kKCodeOff + (i & 1) * kCodeTile,
+                       sbase + C::kKOff + sq * C::kTileBytes);
           fence_proxy_async_smem();  // the generic-proxy writes, before the tensor cores read them
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kKFirst + sq));
@@ -613,7 +761,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int w = t & 1;
         if (!wait_bar(bar(kSFull + w), sw[w] & 1, abort, p.status)) { ok = false; break; }
         ++sw[w];
-        if constexpr (!F8) {
+        if constexpr (!CODES) {
           ++ga[w];
           warp_arrive(bar(kGo + w));
         }
@@ -622,7 +770,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       u = nu;
     }
     if (*abort) {  // let every copy issued land before the CTA ends
-      if constexpr (F8) {
+      if constexpr (CODES) {
         if (q_wait) drain_wait(bar(kQLand), (nq - 1) & 1);
         // the last copy into each staging buffer (one at most is in flight per buffer)
         for (uint32_t i = kc > 2 ? kc - 2 : 0; i < kc; ++i)
@@ -653,7 +801,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (u.r < 0) break;
       int ph = tile_phys(u, tile_of(u, 0));
       bool ok = true;
-      if constexpr (F8) {
+      if constexpr (CODES) {
         // each tile's codes into V buffer w = sq & 1 once PV of the previous
         // tile of that parity is done; the softmax warps widen them there
         for (int sq = 0; sq < u.n_kv; ++sq) {
@@ -719,8 +867,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // Kept lean: every cycle this warp spends between products is tensor-core
     // idle time (the issue queue is shallow).  Counters live in registers,
     // descriptors are built once and advanced by their address field.
-    constexpr uint32_t kIdS = idesc_kind_f16(kTileM, kTileN, 0, F8);
-    constexpr uint32_t kIdPV = idesc_kind_f16(kTileM, D, 1, F8);
+    constexpr uint32_t kIdS = idesc_kind_f16(kTileM, kTileN, 0, CODES);
+    constexpr uint32_t kIdPV = idesc_kind_f16(kTileM, D, 1, CODES);
     const uint64_t dq = smem_desc_sw128(sbase + C::kQOff, 16, 1024);
     const uint64_t dk = smem_desc_sw128(sbase + C::kKOff, 16, C::kKGroupBytes);
     const uint64_t dv = smem_desc_sw128(sbase + C::kVOff, kBlockSize * 128, 1024);
@@ -820,6 +968,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tmem_o = tmem + 256 + lane_off;
     constexpr int kOCols = D / 2;  // O columns this group rescales and writes
+    // column of O that holds head dim e of every eight
+    auto col = [](int e) { return I4 ? (e < 4 ? 2 * e : 2 * e - 7) : e; };
     const float sl2 = p.scale_log2;
     const int Hq = p.num_q_heads;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
@@ -868,10 +1018,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         uint4* dst = reinterpret_cast<uint4*>(orow + c0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          dst[j] = make_uint4(pack_bf16(acc[8 * j] * inv, acc[8 * j + 1] * inv),
-                              pack_bf16(acc[8 * j + 2] * inv, acc[8 * j + 3] * inv),
-                              pack_bf16(acc[8 * j + 4] * inv, acc[8 * j + 5] * inv),
-                              pack_bf16(acc[8 * j + 6] * inv, acc[8 * j + 7] * inv));
+          dst[j] = make_uint4(
+              pack_bf16(acc[8 * j + col(0)] * inv, acc[8 * j + col(1)] * inv),
+              pack_bf16(acc[8 * j + col(2)] * inv, acc[8 * j + col(3)] * inv),
+              pack_bf16(acc[8 * j + col(4)] * inv, acc[8 * j + col(5)] * inv),
+              pack_bf16(acc[8 * j + col(6)] * inv, acc[8 * j + col(7)] * inv));
       }
     };
     for (int uc = 0;; ++uc) {
@@ -956,12 +1107,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             fma2(x0, x1, __uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1]), mul, -m_sub);
             const float p0 = ex2(x0), p1 = ex2(x1);
             add2(ps4[2 * (c & 1)], ps4[2 * (c & 1) + 1], p0, p1);
-            pw[c] = F8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+            pw[c] = CODES ? pack_f16(p0, p1) : pack_bf16(p0, p1);
           }
           PA_TMEM_ST32(tmem_s + w * 32, pw);
           l_part += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
         }
-        if constexpr (F8) {
+        if constexpr (CODES) {
           // this warp's 16-token block of K(t + 2), from its staging buffer
           // into K buffer b (S(t), its last reader, is done), and of V(t), in
           // place in V buffer b (PV(t - 2), its last reader, finished before
@@ -973,18 +1124,27 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               ok = false;
               break;
             }
-            widen_blocks<D, 1>(sbase + C::kKCodeOff + (ci & 1) * C::kCodeBytes, kBlockSize * D,
-                               sbase + C::kKOff + b * C::kTileBytes, false, warp, lane);
+            const uint32_t kcodes = sbase + C::kKCodeOff + (ci & 1) * kCodeTile;
+            const uint32_t kb = sbase + C::kKOff + b * C::kTileBytes;
+            if constexpr (I4)
+              widen_k_int4<D>(kcodes + warp * kCodeBlock, kb + warp * C::kVBlockBytes, lane);
+            else
+              widen_blocks<D, 1>(kcodes, kCodeBlock, kb, false, warp, lane);
             warp_arrive(bar(kKStFree + (ci & 1)));
           }
           {
             if (!wait_bar(bar(kVLand + b), nb & 1, abort, p.status)) { ok = false; break; }
             const uint32_t vb = sbase + C::kVOff + b * C::kTileBytes;
-            widen_blocks<D, 1>(vb + C::kVBlockBytes / 2, C::kVBlockBytes, vb, true, warp, lane);
             const int r0 = u.kv_end - kt * kTileN;
-            if (r0 < kTileN && (r0 >> 4) == warp) {
-              __syncwarp();
-              zero_v_rows(vb, r0, (r0 + kBlockSize - 1) & ~(kBlockSize - 1));
+            if constexpr (I4) {
+              const uint32_t blk = vb + warp * C::kVBlockBytes;
+              widen_v_int4<D>(blk + kVCodeOff, blk, r0 - warp * kBlockSize, lane);
+            } else {
+              widen_blocks<D, 1>(vb + kVCodeOff, C::kVBlockBytes, vb, true, warp, lane);
+              if (r0 < kTileN && (r0 >> 4) == warp) {
+                __syncwarp();
+                zero_v_rows(vb, r0, (r0 + kBlockSize - 1) & ~(kBlockSize - 1));
+              }
             }
           }
           fence_proxy_async_smem();  // generic-proxy writes, before the tensor cores read them
@@ -1052,7 +1212,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           for (int j = 0; j < 4; ++j) {
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * j + e]) * inv;
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * j + col(e)]) * inv;
             dst[j] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
                                 pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
           }
@@ -1137,22 +1297,24 @@ bool encode_map_u8(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
          CUDA_SUCCESS;
 }
 
-template <int D, int G, bool F8>
+template <int D, int G, pa_dtype KV>
 cudaError_t launch_pf(const AttnParams& p, int num_sms, cudaStream_t stream) {
   using C = PfCfg<D>;
-  constexpr int kSmem = F8 ? C::kSmemBytesF8 : C::kSmemBytes;
+  constexpr int kSmem = C::smem_bytes(KV);
+  // (4 KB: the kernel's static shared memory)
+  static_assert(kSmem + 4096 <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
   static bool configured[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(prefill_tc_kernel<D, G, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(prefill_tc_kernel<D, G, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmem);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  PfMaps maps;
+  PfMaps maps{};
   const cuuint64_t e2 = 2;
   {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.num_q_heads),
@@ -1161,7 +1323,9 @@ cudaError_t launch_pf(const AttnParams& p, int num_sms, cudaStream_t stream) {
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(kTileM / G)};
     if (!encode_map(&maps.q, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  if constexpr (F8) {
+  if constexpr (KV == PA_INT4) {
+    // pages are copied without a map
+  } else if constexpr (KV == PA_FP8_E4M3) {
     // codes of one (block, head): 16 rows of D bytes at a stride of Hkv x D;
     // the last index steps one head (D bytes), as in the bf16 K map
     const cuuint64_t hkv = static_cast<cuuint64_t>(p.num_kv_heads);
@@ -1195,29 +1359,29 @@ cudaError_t launch_pf(const AttnParams& p, int num_sms, cudaStream_t stream) {
                                 static_cast<cuuint32_t>(D / 64), 1, 1};
     if (!encode_map(&maps.v, p.v_cache, 5, vdims, vstrides, vbox)) return cudaErrorInvalidValue;
   }
-  prefill_tc_kernel<D, G, F8><<<num_sms, kPfThreads, kSmem, stream>>>(p, maps);
+  prefill_tc_kernel<D, G, KV><<<num_sms, kPfThreads, kSmem, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 namespace {
-template <bool F8>
+template <pa_dtype KV>
 cudaError_t launch_pf_dtype(const AttnParams& p, int head_size, int group, int num_sms,
                             cudaStream_t stream) {
   if (head_size == 128) {
     switch (group) {
-      case 1: return launch_pf<128, 1, F8>(p, num_sms, stream);
-      case 2: return launch_pf<128, 2, F8>(p, num_sms, stream);
-      case 4: return launch_pf<128, 4, F8>(p, num_sms, stream);
-      case 8: return launch_pf<128, 8, F8>(p, num_sms, stream);
+      case 1: return launch_pf<128, 1, KV>(p, num_sms, stream);
+      case 2: return launch_pf<128, 2, KV>(p, num_sms, stream);
+      case 4: return launch_pf<128, 4, KV>(p, num_sms, stream);
+      case 8: return launch_pf<128, 8, KV>(p, num_sms, stream);
     }
   } else if (head_size == 64) {
     switch (group) {
-      case 1: return launch_pf<64, 1, F8>(p, num_sms, stream);
-      case 2: return launch_pf<64, 2, F8>(p, num_sms, stream);
-      case 4: return launch_pf<64, 4, F8>(p, num_sms, stream);
-      case 8: return launch_pf<64, 8, F8>(p, num_sms, stream);
+      case 1: return launch_pf<64, 1, KV>(p, num_sms, stream);
+      case 2: return launch_pf<64, 2, KV>(p, num_sms, stream);
+      case 4: return launch_pf<64, 4, KV>(p, num_sms, stream);
+      case 8: return launch_pf<64, 8, KV>(p, num_sms, stream);
     }
   }
   return cudaErrorInvalidValue;
@@ -1225,9 +1389,13 @@ cudaError_t launch_pf_dtype(const AttnParams& p, int head_size, int group, int n
 }  // namespace
 
 cudaError_t launch_prefill_tc(const AttnParams& p, int head_size, int group, int num_sms,
-                              bool fp8_cache, cudaStream_t stream) {
-  return fp8_cache ? launch_pf_dtype<true>(p, head_size, group, num_sms, stream)
-                   : launch_pf_dtype<false>(p, head_size, group, num_sms, stream);
+                              pa_dtype cache_dtype, cudaStream_t stream) {
+  switch (cache_dtype) {
+    case PA_BF16: return launch_pf_dtype<PA_BF16>(p, head_size, group, num_sms, stream);
+    case PA_FP8_E4M3: return launch_pf_dtype<PA_FP8_E4M3>(p, head_size, group, num_sms, stream);
+    case PA_INT4: return launch_pf_dtype<PA_INT4>(p, head_size, group, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace pa
