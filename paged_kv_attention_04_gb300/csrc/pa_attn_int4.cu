@@ -5,43 +5,68 @@
 //
 // What bounds it: the pages, 20 D bytes per block and kv head, from HBM: at its
 // copy rate an SM takes one 2560-byte block (D = 128) per ~110 clocks, so each
-// of its four schedulers has ~440 issue slots per block.  So the codes are
-// never widened by conversions:
+// of its four schedulers has ~440 issue slots per block, and the integer pipe
+// (one instruction in two clocks) half as many.  So the codes are never widened
+// by conversions:
 //   K  S = sum_g s_g (q_g . c_g) + z_g sum(q_g) over the groups g of 32 dims.
 //      A code masked out of its word is an f16 subnormal: c 2^-24 (nibbles 0
 //      of each half) or c 2^-20 (nibbles 1), exact as a matrix operand, so 8
 //      codes take 4 ANDs and a shift.  q is staged in f16, scaled by a power of
-//      two per row (largest |q| in [2^9, 2^10)) and by 16 more for the dims
-//      whose codes are the c 2^-24, exact but for q below 2^-33 of the row's
-//      largest.  Each group accumulates by itself (two MMAs), the scales are
+//      two per row (largest |q| in [2^10, 2^11)) and by 16 more for the dims
+//      whose codes are the c 2^-24: exact but for q below 2^-34 of the row's
+//      largest.  Each group accumulates by itself (two MMAs) and the scales are
 //      applied to the float32 sums; the zeros term is one more MMA, z against
-//      the group sums of q split into three f16 parts (33 bits).
-//   V  v = fma(16 + c, s, z - 16 s) in f16, where 16 + c is the code placed in
-//      the top mantissa bits of 16.0: a shift, a masked OR and an FMA per two
-//      values.  Rounding z - 16 s (2^-12 of at most 1.6 times the group's
-//      range) and v to f16 is an eighth of what the bf16 output's rounding is.
+//      the group sums of q 2^-20 split into f16 parts (to 2^-24, 2^-14 of the
+//      row's largest q).
+//   V  v = fma(16 + c, s, z') in f16 with z' = f16(z - 16 s), where 16 + c is the code
+//      placed in the top mantissa bits of 16.0: a shift (as a multiplication, on
+//      the other pipe), a masked OR and an FMA per two values.  What z' is off by,
+//      d = z - (16 s + z') <= 2^-12 of 1.6 times the group's range, is the same for
+//      a token's 32 dims, and one more MMA sums p d; v itself is rounded to f16.
 //
 // The tile: S^T = K Q^T and O^T += V^T P^T with the 16 keys of a block, then 16
 // head dims, as the MMA's M, and the query rows as N: 8 (decode: the G heads
 // that share a kv head) or 16 (few tokens: 16 / G positions x G heads).
 // Lane (g, c) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 and rows 2c,
 // 2c + 1 of each n-tile, and O^T at dims (D/8) g + 2 mt, + 1 of m-tile mt: its
-// V codes are one run of the page, all of group g / (32 / (D/8)).
+// V codes are one run of the page, all of one group.
 //
 // The softmax keeps a running maximum per row that moves only when a logit
-// exceeds it by 2^8 (base 2), found by a vote; most blocks need no shuffle and
+// exceeds it by 2^8 (base 2), found by a vote; most steps need no shuffle and
 // no rescaling.  P <= 2^8 in f16, sums in float32.
 //
-// A CTA has NW compute warps and one scheduler warp (roles as in
-// pa_attn_mma.cuh).  Each compute warp streams its blocks through a ring of
-// NS stages, two bulk copies a block, one mbarrier a stage; every wait is
-// bounded: a warp that gives up flags PA_DEV_TIMEOUT and goes on with what the
-// stage holds, so the CTA ends.
+// A CTA has NW compute warps and one scheduler warp.  A compute warp takes pairs
+// of blocks w, w + NW, ... of a unit through a ring of NS stages (four bulk
+// copies and one mbarrier a stage, issued by four lanes) that runs on into the
+// next unit.  The scheduler warp claims and stages one unit ahead, and joins and
+// writes (or merges) the finished one; the roles meet on mbarriers only (unit
+// ready, warp states written, warp states read), so a warp that is done goes on.
+// Every wait is bounded: one that gives up flags PA_DEV_TIMEOUT and ends the CTA
+// after its copies have landed.
 #include <cuda_fp16.h>
 
 #include "pa_attn_mma.cuh"
 #include "pa_int4.cuh"
 #include "pa_tcgen05.cuh"
+
+#ifndef PA_I4_NW
+#define PA_I4_NW 4
+#endif
+#ifndef PA_I4_CTAS
+#define PA_I4_CTAS 3
+#endif
+#ifndef PA_I4_SNS
+#define PA_I4_SNS 3
+#endif
+#ifndef PA_I4_SBP
+#define PA_I4_SBP 1
+#endif
+#ifndef PA_I4_NS
+#define PA_I4_NS 2
+#endif
+#ifndef PA_I4_NS64
+#define PA_I4_NS64 4
+#endif
 
 namespace pa {
 
@@ -50,7 +75,7 @@ namespace {
 constexpr uint32_t kI4WaitLimit = 1u << 22;
 constexpr float kI4Rescale = 8.f;  // base-2 logit growth that moves the running maximum
 
-template <int D, int G, int P, int NW, int NS>
+template <int D, int G, int P, int NW, int NS, int BP>
 struct I4Cfg {
   using Pg = I4Page<D>;
   static constexpr int kR = P * G;               // real query rows
@@ -59,23 +84,29 @@ struct I4Cfg {
   static constexpr int kGroups = D / 32;
   static constexpr int kMT = D / 16;             // m-tiles of O^T
   static constexpr int kThreads = (NW + 1) * 32;
-  static constexpr int kStageBytes = 2 * Pg::kBytes;
+  static constexpr int kBlockBytes = 2 * Pg::kBytes;  // K and V page of a block
+  static constexpr int kStageBytes = BP * kBlockBytes;
   static constexpr int kRingBytes = NW * NS * kStageBytes;
   // q buffer: rows of D f16, then per row 16 f16 (group sums) and a float factor
   static constexpr int kQRowBytes = D * 2;
   static constexpr int kQBufBytes = kRows * (kQRowBytes + 32 + 4);
   static constexpr int kQOff = kRingBytes;
+  // the warps' states of finished units: two units' for decode tiles, one for
+  // 16 rows (64 KB a pair)
+  static constexpr int kNB = kNT == 1 ? 2 : 1;
   static constexpr int kCombOff = kQOff + 2 * kQBufBytes;
-  static constexpr int kCombBytes = 2 * NW * kR * D * 4;  // two units in flight
+  static constexpr int kCombBytes = kNB * NW * kR * D * 4;
   static constexpr int kMlOff = kCombOff + kCombBytes;
-  static constexpr int kMlBytes = 2 * NW * kR * 2 * 4;
+  static constexpr int kMlBytes = kNB * NW * kR * 2 * 4;
   static constexpr int kMetaOff = (kMlOff + kMlBytes + 15) / 16 * 16;
-  static constexpr int kBarOff = kMetaOff + 3 * (static_cast<int>(sizeof(UnitMeta)) + 15) / 16 * 16;
-  static constexpr int kSmemBytes = kBarOff + NW * NS * 8;
+  static constexpr int kBarOff = kMetaOff + 2 * ((static_cast<int>(sizeof(UnitMeta)) + 15) / 16 * 16);
+  static constexpr int kNumBars = NW * NS + 2 + 2 * kNB;
+  static constexpr int kSmemBytes = kBarOff + kNumBars * 8;
   static constexpr int kFit = (228 * 1024) / (kSmemBytes + 1024 + 64);
-  static constexpr int kMinCtas = kFit >= 3 ? 3 : (kFit >= 2 ? 2 : 1);
+  static constexpr int kMinCtas = kFit < PA_I4_CTAS ? kFit : PA_I4_CTAS;
   static_assert(kR <= 16 && kGroups <= 4, "at most 16 query rows and 4 groups");
   static_assert(kStageBytes % 16 == 0 && kQBufBytes % 16 == 0, "16-byte stages");
+  static_assert(kNumBars <= kThreads, "one thread initialises each barrier");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
 };
 
@@ -94,8 +125,10 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                  : "r"(addr));
-  else
+  else if constexpr (N == 2)
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(w[0]) : "r"(addr));
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -105,537 +138,607 @@ __device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c
   asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-// 16 + c as f16 for nibble n of both halves of w
-template <int N>
-__device__ __forceinline__ uint32_t code_plus_16(uint32_t w) {
-  constexpr int s = 6 - 4 * N;  // the nibble goes to bits 6-9
-  const uint32_t x = s >= 0 ? w << (s >= 0 ? s : 0) : w >> (s >= 0 ? 0 : -s);
-  return (x & 0x03c003c0u) | 0x4c004c00u;
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 16 + c as f16 of the nibbles of both halves of w that `mul` moves to bits 6-9
+__device__ __forceinline__ uint32_t code_plus_16(uint32_t w, uint32_t mul) {
+  return ((w * mul) & 0x03c003c0u) | 0x4c004c00u;
+}
+// A constant the compiler does not see through (it would turn a multiplication
+// by a power of two back into a shift).
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("mov.u32 %0, %0;\n" : "+r"(x));
+  return x;
+}
+// Whether phase `parity` has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 }  // namespace
 
-template <int D, int G, int P, int NW, int NS>
-__global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, P, NW, NS>::kMinCtas)
+template <int D, int G, int P, int NW, int NS, int BP>
+__global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D, G, P, NW, NS, BP>::kMinCtas)
     attn_int4_kernel(const AttnParams p) {
-  using C = I4Cfg<D, G, P, NW, NS>;
+  using C = I4Cfg<D, G, P, NW, NS, BP>;
   using Pg = typename C::Pg;
-  constexpr int R = C::kR, NT = C::kNT, NG = C::kGroups, MT = C::kMT;
+  constexpr int R = C::kR, NT = C::kNT, NG = C::kGroups, MT = C::kMT, NB = C::kNB;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ UnitTail s_tail;
   __shared__ int s_abort;
 
   const int tid = threadIdx.x;
   const int lane = tid & 31;
   const int warp = tid >> 5;
-  const bool sched = warp == NW;
   const int Hkv = p.num_kv_heads, Hq = p.num_q_heads;
-  UnitMeta* meta = reinterpret_cast<UnitMeta*>(smem + C::kMetaOff);
   float* comb = reinterpret_cast<float*>(smem + C::kCombOff);
   float* comb_ml = reinterpret_cast<float*>(smem + C::kMlOff);
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-  const uint32_t ring = smem_u32(smem) + warp * (NS * C::kStageBytes);
-  const uint32_t bars = smem_u32(smem + C::kBarOff) + warp * (NS * 8);
-  if (tid < NW * NS) mbar_init(smem_u32(smem + C::kBarOff) + tid * 8, 1);
-  if (tid == 0) {
-    s_abort = 0;
-    s_tail.valid = 0;
+  auto meta = [&](int k) -> UnitMeta& {  // of unit k of this CTA's sequence
+    return *reinterpret_cast<UnitMeta*>(smem + C::kMetaOff +
+                                        (k & 1) * ((static_cast<int>(sizeof(UnitMeta)) + 15) / 16 * 16));
+  };
+  // mbarriers: the ring stages of every warp, then
+  const uint32_t bars = smem_u32(smem + C::kBarOff);
+  const uint32_t bar_unit = bars + NW * NS * 8;   // [2] unit published (scheduler)
+  const uint32_t bar_full = bar_unit + 16;        // [NB] states written (NW warps)
+  const uint32_t bar_free = bar_full + NB * 8;    // [NB] ... and read (scheduler)
+  if (tid < C::kNumBars) {
+    const bool full = tid >= NW * NS + 2 && tid < NW * NS + 2 + NB;
+    mbar_init(bars + tid * 8, full ? NW : 1);
   }
+  if (tid == 0) s_abort = 0;
   mbar_fence_init();
-  wait_prior_grid();  // the plan's work lists
-  // (not through the read-only path, whose loads may be moved above the wait)
-  const int n_units = __ldcg(p.n_items) * Hkv;
-
-  // ---- scheduler-warp helpers -------------------------------------------
-  auto fetch_unit = [&](UnitMeta& m, int u) {  // whole scheduler warp
-    if (u >= n_units) {
-      if (lane == 0) m.valid = 0;
-      return;
-    }
-    const int k = u / Hkv;
-    const int item = p.order ? __ldg(p.order + k) : k;
-    const UnitRec* rec = p.recs + item;
-    const int4 ra = __ldg(&rec->a), rb = __ldg(&rec->b), rc = __ldg(&rec->c);
-    const int32_t* row = p.block_tables + static_cast<long long>(ra.x) * p.max_blocks_per_seq;
-    for (int i = lane; i < ra.w - ra.z; i += 32) m.bt[i] = __ldg(row + ra.z + i);
-    if (lane == 0) {
-      m.valid = 1; m.item = item; m.g = u - k * Hkv; m.r = ra.x; m.a = rb.w; m.j0 = ra.y;
-      m.npos = rc.x; m.pos0 = rc.y; m.kv_hi = rc.z; m.b0 = ra.z; m.b1 = ra.w;
-      m.tile = rb.x; m.first = rb.y; m.nsplit = rb.z;
-    }
-  };
-  auto claim = [&]() -> int {
-    int u = 0;
-    if (lane == 0) u = atomicAdd(p.next, 1);
-    return __shfl_sync(0xffffffffu, u, 0);
-  };
-  // q rows of unit m (row = position row/G, head row%G): loaded into registers
-  // first and staged later, so the loads overlap other scheduler work.
-  constexpr int kRowChunks = D / 8;                       // 8 dims a chunk
-  constexpr int kQPerLane = C::kRows * kRowChunks / 32;   // a row's chunks sit in adjacent lanes
-  auto load_q = [&](const UnitMeta& m, uint4 (&qv)[kQPerLane]) {
-#pragma unroll
-    for (int i = 0; i < kQPerLane; ++i) {
-      const int idx = lane + 32 * i;
-      const int row = idx / kRowChunks, c = idx - row * kRowChunks;
-      const int jj = row / G, hh = row - jj * G;
-      qv[i] = make_uint4(0, 0, 0, 0);
-      if (m.valid && row < R && jj < m.npos) {
-        const long long tok = m.a + m.j0 + jj;
-        qv[i] = __ldg(reinterpret_cast<const uint4*>(q + (tok * Hq + m.g * G + hh) * D) + c);
-      }
-    }
-  };
-  auto store_q = [&](const uint4 (&qv)[kQPerLane], int buf) {
-    unsigned char* qb = smem + C::kQOff + buf * C::kQBufBytes;
-#pragma unroll
-    for (int i = 0; i < kQPerLane; ++i) {
-      const int idx = lane + 32 * i;
-      const int row = idx / kRowChunks, c = idx - row * kRowChunks;
-      float x[8];
-      Chunk<__nv_bfloat16>::unpack(qv[i], x);
-      float mx = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
-#pragma unroll
-      for (int o = 1; o < kRowChunks; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      // 2^(9 - exponent) and its inverse
-      const int ex = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
-      const float f = __uint_as_float(static_cast<uint32_t>(9 - ex + 127) << 23);
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] *= f;
-        sum += x[e];
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      // the fragments of the group's two k-steps: nibbles (0, 4), (2, 6) and (1, 5), (3, 7)
-      *reinterpret_cast<uint4*>(qb + row * C::kQRowBytes + c * 16) =
-          make_uint4(pack_f16(16.f * x[0], 16.f * x[4]), pack_f16(16.f * x[2], 16.f * x[6]),
-                     pack_f16(x[1], x[5]), pack_f16(x[3], x[7]));
-      // group sums in three f16 parts: element NG j + g is part j of group g
-      __half* zs = reinterpret_cast<__half*>(qb + C::kRows * C::kQRowBytes + row * 32);
-      if ((c & 3) == 0) {
-        const int g = c >> 2;
-#pragma unroll
-        for (int j = 0; j < 16 / NG; ++j) {
-          const __half part = __float2half_rn(j < 3 ? sum : 0.f);
-          zs[NG * j + g] = part;
-          sum -= __half2float(part);
-        }
-      }
-      if (c == 0)  // S = acc 2^20 / f, times the softmax scale
-        *reinterpret_cast<float*>(qb + C::kRows * (C::kQRowBytes + 32) + row * 4) =
-            p.scale_log2 * 1048576.f * __uint_as_float(static_cast<uint32_t>(ex - 9 + 127) << 23);
-    }
-  };
-
-  if (sched) {
-    // a second unit is claimed up front only if every CTA can still get one
-    const int u0 = claim();
-    const int u1 = u0 + static_cast<int>(gridDim.x) < n_units ? claim() : n_units;
-    fetch_unit(meta[0], u0);
-    fetch_unit(meta[1], u1);
-    __syncwarp();
-    uint4 qv[kQPerLane];
-    load_q(meta[0], qv);
-    store_q(qv, 0);
-  }
   __syncthreads();
+  wait_prior_grid();  // the plan's work lists
 
-  // ---- compute-warp stream: its share of unit k's blocks, then of unit k+1's
-  int iss_unit = 0, iss_i = 0;  // next block to issue: (unit sequence, index in warp share)
-  int iss_st = 0, cur_st = 0;   // ring stages of the next issue and of the next block to compute
-  uint32_t cur_par = 0;         // its mbarrier phase
-  int in_flight = 0;
-
-  auto share = [&](const UnitMeta& m) -> int {
-    const int n = m.b1 - m.b0 - warp;
-    return (m.valid && n > 0) ? (n + NW - 1) / NW : 0;
-  };
-  // Issue the next block of the stream if it lies in unit `limit` or earlier.
-  auto issue_one = [&](int limit) -> bool {
-    while (iss_unit <= limit) {
-      if (iss_i < share(meta[iss_unit % 3])) break;
-      ++iss_unit;
-      iss_i = 0;
-    }
-    if (iss_unit > limit) return false;
-    const UnitMeta& m = meta[iss_unit % 3];
-    const int phys = m.bt[warp + iss_i * NW];
-    const uint32_t st = ring + iss_st * C::kStageBytes, bar = bars + iss_st * 8;
-    if (phys >= 0 && phys < p.num_blocks) {
-      if (lane == 0) {
-        const long long off = (static_cast<long long>(phys) * Hkv + m.g) * Pg::kBytes;
-        mbar_arrive_expect_tx(bar, C::kStageBytes);
-        bulk_load(st, static_cast<const unsigned char*>(p.k_cache) + off, Pg::kBytes, bar);
-        bulk_load(st + Pg::kBytes, static_cast<const unsigned char*>(p.v_cache) + off, Pg::kBytes, bar);
-      }
-    } else {  // a bad table entry reads as zeros
-      for (int i = lane; i < C::kStageBytes / 16; i += 32)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(st + i * 16), "r"(0u) : "memory");
-      fence_proxy_async_smem();  // before a later copy into this stage
-      __syncwarp();
-      if (lane == 0) {
-        flag_error(p.status, PA_DEV_BLOCK_RANGE);
-        mbar_arrive(bar);
-      }
-    }
-    iss_st = iss_st + 1 == NS ? 0 : iss_st + 1;
-    ++iss_i;
-    ++in_flight;
-    return true;
-  };
-  auto wait_block = [&]() {  // the next block to compute has landed
-    const uint32_t bar = bars + cur_st * 8;
-    if (!mbar_try_wait(bar, cur_par)) {
+  // Bounded wait (whole warp) for phase `parity`; false if it gave up.
+  auto wait_for = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (!mbar_try_wait(bar, parity)) {
       const uint32_t limit = *reinterpret_cast<volatile int*>(&s_abort) ? 1024u : kI4WaitLimit;
-      if (!mbar_wait(bar, cur_par, limit)) {
+      if (!mbar_wait(bar, parity, limit)) {
         s_abort = 1;
         flag_error(p.status, PA_DEV_TIMEOUT);
       }
     }
     __syncwarp();
+    return *reinterpret_cast<volatile int*>(&s_abort) == 0;
   };
 
-  if (!sched) {
-    while (in_flight < NS && issue_one(1)) {
-    }
-  }
-
-  // ---- scheduler warp: join the warps' states of a finished unit, write the
-  // output or the split's partial, and merge the splits if it is the last.
-  auto finish_unit = [&](const UnitTail& u, int buf) {
-    const float* cb = comb + buf * NW * R * D;
-    const float* cm = comb_ml + buf * NW * R * 2;
-    const long long part_base = (static_cast<long long>(u.item) * Hkv + u.g) * R;
-    for (int idx = lane; idx < R * D / 4; idx += 32) {
-      const int row = (idx * 4) / D, d = idx * 4 - row * D;
-      const int jj = row / G, hh = row - jj * G;
-      if (jj >= u.npos) continue;
-      float M = -CUDART_INF_F;
+  if (warp == NW) {
+    // ---------------------------------------------------------- scheduler warp
+    // (not through the read-only path, whose loads may be moved above the wait)
+    const int n_units = __ldcg(p.n_items) * Hkv;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+    // Metadata of unit u into m: one precomputed record and the unit's slice of
+    // the block table.
+    auto fetch_unit = [&](UnitMeta& m, int u) {
+      if (u >= n_units) {
+        if (lane == 0) m.valid = 0;
+        return;
+      }
+      const int k = u / Hkv;
+      const int item = p.order ? __ldg(p.order + k) : k;
+      const UnitRec* rec = p.recs + item;
+      const int4 ra = __ldg(&rec->a), rb = __ldg(&rec->b), rc = __ldg(&rec->c);
+      const int32_t* row = p.block_tables + static_cast<long long>(ra.x) * p.max_blocks_per_seq;
+      for (int i = lane; i < ra.w - ra.z; i += 32) m.bt[i] = __ldg(row + ra.z + i);
+      if (lane == 0) {
+        m.valid = 1; m.item = item; m.g = u - k * Hkv; m.r = ra.x; m.a = rb.w; m.j0 = ra.y;
+        m.npos = rc.x; m.pos0 = rc.y; m.kv_hi = rc.z; m.b0 = ra.z; m.b1 = ra.w;
+        m.tile = rb.x; m.first = rb.y; m.nsplit = rb.z;
+      }
+      __syncwarp();
+    };
+    // q rows of unit m (row = position row/G, head row%G) into buffer buf, eight
+    // dims a lane and step, a row's chunks in adjacent lanes.
+    constexpr int kRowChunks = D / 8;
+    constexpr int kQPerLane = C::kRows * kRowChunks / 32;
+    auto stage_q = [&](const UnitMeta& m, int buf) {
+      unsigned char* qb = smem + C::kQOff + buf * C::kQBufBytes;
+      uint4 qv[kQPerLane];
 #pragma unroll
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[(w * R + row) * 2]);
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      float den = 0.f;
-      if (M != -CUDART_INF_F) {
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float f = ex2_approx(cm[(w * R + row) * 2] - M);
-          const float4 c4 = *reinterpret_cast<const float4*>(cb + (w * R + row) * D + d);
-          num.x = fmaf(c4.x, f, num.x); num.y = fmaf(c4.y, f, num.y);
-          num.z = fmaf(c4.z, f, num.z); num.w = fmaf(c4.w, f, num.w);
-          den = fmaf(cm[(w * R + row) * 2 + 1], f, den);
+      for (int i = 0; i < kQPerLane; ++i) {
+        const int idx = lane + 32 * i;
+        const int row = idx / kRowChunks, c = idx - row * kRowChunks;
+        const int jj = row / G, hh = row - jj * G;
+        qv[i] = make_uint4(0, 0, 0, 0);
+        if (row < R && jj < m.npos) {
+          const long long tok = m.a + m.j0 + jj;
+          qv[i] = __ldg(reinterpret_cast<const uint4*>(q + (tok * Hq + m.g * G + hh) * D) + c);
         }
       }
-      if (u.nsplit == 1) {
-        const long long tok = u.a + u.j0 + jj;
-        const float inv = p.out_scale / den;
-        *reinterpret_cast<uint2*>(out + (tok * Hq + u.g * G + hh) * D + d) =
-            make_uint2(pack_bf16(num.x * inv, num.y * inv), pack_bf16(num.z * inv, num.w * inv));
-      } else {
-        *reinterpret_cast<float4*>(p.part_acc + (part_base + row) * D + d) = num;
-        if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (part_base + row) * 2) = make_float2(M, den);
-      }
-    }
-    if (u.nsplit > 1) {
-      __threadfence();
-      __syncwarp();
-      int last = 0;
-      if (lane == 0) last = atomicAdd(p.merge_cnt + u.tile * Hkv + u.g, 1) == u.nsplit - 1;
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (last) {
-        __threadfence();
-        // groups of kMergeChunk partials, loaded before any is used: one L2
-        // round trip a group
-        constexpr int kMergeChunk = 4;
-#pragma unroll 2
-        for (int idx = lane; idx < R * D / 4; idx += 32) {
-          const int row = (idx * 4) / D, d = idx * 4 - row * D;
-          const int jj = row / G, hh = row - jj * G;
-          if (jj >= u.npos) continue;
-          float M = -CUDART_INF_F, den = 0.f;
-          float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int sp0 = 0; sp0 < u.nsplit; sp0 += kMergeChunk) {
-            float2 ml[kMergeChunk];
-            float4 a4[kMergeChunk];
 #pragma unroll
-            for (int j = 0; j < kMergeChunk; ++j) {
-              ml[j] = make_float2(-CUDART_INF_F, 0.f);
-              a4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (sp0 + j < u.nsplit) {
-                const long long pb = (static_cast<long long>(u.first + sp0 + j) * Hkv + u.g) * R + row;
-                ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + pb * 2));
-                a4[j] = __ldcg(reinterpret_cast<const float4*>(p.part_acc + pb * D + d));
-              }
-            }
-            // a split with no visible key for this row holds (-inf, 0) and zeros
-            float mc = M;
+      for (int i = 0; i < kQPerLane; ++i) {
+        const int idx = lane + 32 * i;
+        const int row = idx / kRowChunks, c = idx - row * kRowChunks;
+        float x[8];
+        Chunk<__nv_bfloat16>::unpack(qv[i], x);
+        float mx = 0.f;
 #pragma unroll
-            for (int j = 0; j < kMergeChunk; ++j) mc = fmaxf(mc, ml[j].x);
-            if (mc == -CUDART_INF_F) continue;
-            if (mc > M) {  // rescale the running sums to the new maximum
-              const float sc = ex2_approx(M - mc);  // 0 while nothing was visible
-              num.x *= sc; num.y *= sc; num.z *= sc; num.w *= sc; den *= sc;
-              M = mc;
-            }
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
 #pragma unroll
-            for (int j = 0; j < kMergeChunk; ++j) {
-              const float f = ex2_approx(ml[j].x - M);  // 0 for an empty split
-              num.x = fmaf(a4[j].x, f, num.x); num.y = fmaf(a4[j].y, f, num.y);
-              num.z = fmaf(a4[j].z, f, num.z); num.w = fmaf(a4[j].w, f, num.w);
-              den = fmaf(ml[j].y, f, den);
-            }
+        for (int o = 1; o < kRowChunks; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // 2^(10 - exponent), with the softmax scale's sign; the inverse goes into
+        // the row's factor
+        const int ex = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
+        const float f = copysignf(__uint_as_float(static_cast<uint32_t>(10 - ex + 127) << 23), p.scale_log2);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] *= f;
+          sum += x[e];
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        // the fragments of the group's two k-steps: nibbles (0, 4), (2, 6) and (1, 5), (3, 7)
+        *reinterpret_cast<uint4*>(qb + row * C::kQRowBytes + c * 16) =
+            make_uint4(pack_f16(16.f * x[0], 16.f * x[4]), pack_f16(16.f * x[2], 16.f * x[6]),
+                       pack_f16(x[1], x[5]), pack_f16(x[3], x[7]));
+        // group sums x 2^-20 in f16 parts: element NG j + g is part j of group g
+        __half* zs = reinterpret_cast<__half*>(qb + C::kRows * C::kQRowBytes + row * 32);
+        if ((c & 3) == 0) {
+          const int g = c >> 2;
+          sum *= 0x1p-20f;
+#pragma unroll
+          for (int j = 0; j < 16 / NG; ++j) {
+            const __half part = __float2half_rn(j < 3 ? sum : 0.f);
+            zs[NG * j + g] = part;
+            sum -= __half2float(part);
           }
+        }
+        if (c == 0)  // base-2 logit = (accumulated sum) x factor; kept positive
+          *reinterpret_cast<float*>(qb + C::kRows * (C::kQRowBytes + 32) + row * 4) =
+              fmaxf(fabsf(p.scale_log2) * 1048576.f *
+                        __uint_as_float(static_cast<uint32_t>(ex - 10 + 127) << 23),
+                    1e-37f);
+      }
+    };
+    auto publish = [&](int k, int u) {  // unit k of the sequence is unit u of the list
+      UnitMeta& m = meta(k);
+      fetch_unit(m, u);
+      if (u < n_units) stage_q(m, k & 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_unit + (k & 1) * 8);
+    };
+    // Join the warps' states of a finished unit, write the output or the split's
+    // partial, and merge the splits if it is the last.
+    auto finish_unit = [&](const UnitTail& u, int buf) {
+      const float* cb = comb + buf * NW * R * D;
+      const float* cm = comb_ml + buf * NW * R * 2;
+      const long long part_base = (static_cast<long long>(u.item) * Hkv + u.g) * R;
+      for (int idx = lane; idx < R * D / 4; idx += 32) {
+        const int row = (idx * 4) / D, d = idx * 4 - row * D;
+        const int jj = row / G, hh = row - jj * G;
+        if (jj >= u.npos) continue;
+        float M = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[(w * R + row) * 2]);
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
+        if (M != -CUDART_INF_F) {
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const float f = ex2_approx(cm[(w * R + row) * 2] - M);
+            const float4 c4 = *reinterpret_cast<const float4*>(cb + (w * R + row) * D + d);
+            num.x = fmaf(c4.x, f, num.x); num.y = fmaf(c4.y, f, num.y);
+            num.z = fmaf(c4.z, f, num.z); num.w = fmaf(c4.w, f, num.w);
+            den = fmaf(cm[(w * R + row) * 2 + 1], f, den);
+          }
+        }
+        if (u.nsplit == 1) {
           const long long tok = u.a + u.j0 + jj;
           const float inv = p.out_scale / den;
           *reinterpret_cast<uint2*>(out + (tok * Hq + u.g * G + hh) * D + d) =
               make_uint2(pack_bf16(num.x * inv, num.y * inv), pack_bf16(num.z * inv, num.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(p.part_acc + (part_base + row) * D + d) = num;
+          if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (part_base + row) * 2) = make_float2(M, den);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_free + buf * 8);  // the states have been read
+      if (u.nsplit > 1) {
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) last = atomicAdd(p.merge_cnt + u.tile * Hkv + u.g, 1) == u.nsplit - 1;
+        last = __shfl_sync(0xffffffffu, last, 0);
+        if (last) {
+          __threadfence();
+          // groups of kMergeChunk partials, loaded before any is used: one L2
+          // round trip a group
+          constexpr int kMergeChunk = 4;
+#pragma unroll 2
+          for (int idx = lane; idx < R * D / 4; idx += 32) {
+            const int row = (idx * 4) / D, d = idx * 4 - row * D;
+            const int jj = row / G, hh = row - jj * G;
+            if (jj >= u.npos) continue;
+            float M = -CUDART_INF_F, den = 0.f;
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int sp0 = 0; sp0 < u.nsplit; sp0 += kMergeChunk) {
+              float2 ml[kMergeChunk];
+              float4 a4[kMergeChunk];
+#pragma unroll
+              for (int j = 0; j < kMergeChunk; ++j) {
+                ml[j] = make_float2(-CUDART_INF_F, 0.f);
+                a4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (sp0 + j < u.nsplit) {
+                  const long long pb = (static_cast<long long>(u.first + sp0 + j) * Hkv + u.g) * R + row;
+                  ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + pb * 2));
+                  a4[j] = __ldcg(reinterpret_cast<const float4*>(p.part_acc + pb * D + d));
+                }
+              }
+              // a split with no visible key for this row holds (-inf, 0) and zeros
+              float mc = M;
+#pragma unroll
+              for (int j = 0; j < kMergeChunk; ++j) mc = fmaxf(mc, ml[j].x);
+              if (mc == -CUDART_INF_F) continue;
+              if (mc > M) {  // rescale the running sums to the new maximum
+                const float sc = ex2_approx(M - mc);  // 0 while nothing was visible
+                num.x *= sc; num.y *= sc; num.z *= sc; num.w *= sc; den *= sc;
+                M = mc;
+              }
+#pragma unroll
+              for (int j = 0; j < kMergeChunk; ++j) {
+                const float f = ex2_approx(ml[j].x - M);  // 0 for an empty split
+                num.x = fmaf(a4[j].x, f, num.x); num.y = fmaf(a4[j].y, f, num.y);
+                num.z = fmaf(a4[j].z, f, num.z); num.w = fmaf(a4[j].w, f, num.w);
+                den = fmaf(ml[j].y, f, den);
+              }
+            }
+            const long long tok = u.a + u.j0 + jj;
+            const float inv = p.out_scale / den;
+            *reinterpret_cast<uint2*>(out + (tok * Hq + u.g * G + hh) * D + d) =
+                make_uint2(pack_bf16(num.x * inv, num.y * inv), pack_bf16(num.z * inv, num.w * inv));
+          }
+        }
+      }
+    };
+    // A CTA's first unit is its own index, later ones count on from the grid
+    // size; a second one is claimed up front only if every CTA can still get one.
+    const int grid = static_cast<int>(gridDim.x);
+    auto claim = [&]() -> int {
+      int u = 0;
+      if (lane == 0) u = grid + atomicAdd(p.next, 1);
+      return __shfl_sync(0xffffffffu, u, 0);
+    };
+    const int u0 = blockIdx.x;
+    publish(0, u0);
+    bool more[2] = {u0 < n_units, false};  // units k, k + 1 are real
+    {
+      const int u1 = u0 + grid < n_units ? claim() : n_units;
+      publish(1, u1);
+      more[1] = u1 < n_units;
     }
+    for (int k = 0; more[0]; ++k) {
+      if (!wait_for(bar_full + (k % NB) * 8, (k / NB) & 1)) break;
+      const UnitMeta& m = meta(k);
+      UnitTail t;
+      t.valid = 1; t.item = m.item; t.g = m.g; t.a = m.a; t.j0 = m.j0;
+      t.npos = m.npos; t.tile = m.tile; t.nsplit = m.nsplit; t.first = m.first;
+      __syncwarp();
+      // the finished unit's slot takes the unit after the next
+      const int u2 = more[1] ? claim() : n_units;
+      publish(k + 2, u2);
+      finish_unit(t, k % NB);
+      more[0] = more[1];
+      more[1] = u2 < n_units;
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------ compute warps
+  const int g = lane >> 2, c4 = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * (NS * C::kStageBytes);
+  const uint32_t ring_bars = bars + warp * (NS * 8);
+  const uint32_t mul64 = opaque(64u), mul4 = opaque(4u);
+
+  // ---- the stream of block pairs: this warp's share of unit k, then of unit k+1
+  int iss_unit = -1;                // unit being issued
+  int iss_bl = 0, iss_n = 0;        // its next pair's first block, its blocks
+  int iss_g = 0;
+  bool iss_end = false;             // no unit after it
+  int iss_st = 0, in_flight = 0;    // ring stage of the next issue, stages under way
+  // lanes 0-3 copy the pair's K and V pages: block lane / 2, K (0) or V (1)
+  const unsigned char* my_cache = static_cast<const unsigned char*>((lane & 1) ? p.v_cache : p.k_cache);
+  const uint32_t my_dst = (lane >> 1) * C::kBlockBytes + (lane & 1) * Pg::kBytes;
+
+  // Issue the next pair if it lies in unit `limit` or earlier and is known.
+  auto issue_one = [&](int limit) -> bool {
+    while (iss_bl >= iss_n) {
+      if (iss_unit >= limit || iss_end) return false;
+      const int k = iss_unit + 1;
+      if (!mbar_test(bar_unit + (k & 1) * 8, (k >> 1) & 1)) return false;
+      const UnitMeta& m = meta(k);
+      iss_unit = k;
+      iss_end = !m.valid;
+      iss_n = m.valid ? m.b1 - m.b0 : 0;
+      iss_bl = BP * warp;
+      iss_g = m.g;
+    }
+    const int bl = iss_bl + (lane >> 1);
+    const bool want = lane < 2 * BP && bl < iss_n;
+    const int phys = want ? meta(iss_unit).bt[bl] : 0;
+    const bool ok = want && static_cast<uint32_t>(phys) < static_cast<uint32_t>(p.num_blocks);
+    const uint32_t st = ring + iss_st * C::kStageBytes, bar = ring_bars + iss_st * 8;
+    const uint32_t copies = __ballot_sync(0xffffffffu, ok);
+    if (__any_sync(0xffffffffu, want && !ok)) {  // a bad table entry reads as zeros
+      if (want && !ok) {
+        for (int i = 0; i < Pg::kBytes / 16; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(st + my_dst + i * 16), "r"(0u)
+                       : "memory");
+        fence_proxy_async_smem();  // before a later copy into this stage
+        flag_error(p.status, PA_DEV_BLOCK_RANGE);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(copies) * Pg::kBytes);
+    __syncwarp();
+    if (ok)
+      bulk_load(st + my_dst, my_cache + (static_cast<long long>(phys) * Hkv + iss_g) * Pg::kBytes,
+                Pg::kBytes, bar);
+    iss_st = iss_st + 1 == NS ? 0 : iss_st + 1;
+    iss_bl += BP * NW;
+    ++in_flight;
+    return true;
   };
 
-  const int g = lane >> 2, c4 = lane & 3;
-  int k = 0;
-  for (;; ++k) {
-    const UnitMeta& cur = meta[k % 3];
+  int cur_st = 0;        // ring stage of the next pair to compute
+  uint32_t cur_par = 0;  // and its mbarrier phase
+  for (int k = 0;; ++k) {
+    if (!wait_for(bar_unit + (k & 1) * 8, (k >> 1) & 1)) break;
+    const UnitMeta& cur = meta(k);
     if (!cur.valid) break;
-    if (sched) {
-      // while the compute warps stream unit k: load unit k+1's q, finish unit
-      // k-1, stage the q rows, claim and decode unit k+2
-      uint4 qv[kQPerLane];
-      load_q(meta[(k + 1) % 3], qv);
-      const UnitTail tail = s_tail;
-      if (tail.valid) finish_unit(tail, (k - 1) & 1);
-      store_q(qv, (k + 1) & 1);
-      const int nu = meta[(k + 1) % 3].valid ? claim() : n_units;
-      fetch_unit(meta[(k + 2) % 3], nu);
-      __syncwarp();
-      if (lane == 0) {
-        s_tail.valid = 1; s_tail.item = cur.item; s_tail.g = cur.g; s_tail.a = cur.a;
-        s_tail.j0 = cur.j0; s_tail.npos = cur.npos; s_tail.tile = cur.tile;
-        s_tail.nsplit = cur.nsplit; s_tail.first = cur.first;
-      }
-      __syncwarp();
-    } else {
-      // Every block of units < k has been issued and computed; move the issue
-      // pointer off unit k-1, whose metadata slot is now being overwritten.
-      if (iss_unit < k) {
-        iss_unit = k;
-        iss_i = 0;
-      }
-      while (in_flight < NS && issue_one(k + 1)) {  // stages left free while unit k + 1 was unknown
-      }
-      // q^T fragments, the group sums' and the rows' factors
-      uint32_t qb[NT][NG][4], zb[NT][2];
-      float rm[NT][2];
-      {
-        const unsigned char* buf = smem + C::kQOff + (k & 1) * C::kQBufBytes;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint32_t row = smem_u32(buf) + (8 * n + g) * C::kQRowBytes;
-#pragma unroll
-          for (int e = 0; e < NG; ++e) lds_words<4>(row + (4 * e + c4) * 16, qb[n][e]);
-          const uint32_t* zs = reinterpret_cast<const uint32_t*>(buf + C::kRows * C::kQRowBytes + (8 * n + g) * 32);
-          zb[n][0] = zs[c4];
-          zb[n][1] = zs[4 + c4];
-          const float* fr = reinterpret_cast<const float*>(buf + C::kRows * (C::kQRowBytes + 32)) + 8 * n;
-          rm[n][0] = fr[2 * c4];
-          rm[n][1] = fr[2 * c4 + 1];
-        }
-      }
-      float o[NT][MT][4];
-      float m[NT][2], l[NT][2];
+    while (in_flight < NS && issue_one(k + 1)) {
+    }
+    const int nblk = cur.b1 - cur.b0;
+    const int pos0 = cur.pos0, kv_hi = cur.kv_hi;
+    const int plain_end = min(pos0 + 1, kv_hi) - BP * kBlockSize;  // no mask up to this first key
+    // q^T fragments, the group sums' and the rows' factors
+    uint32_t qb[NT][NG][4], zb[NT][2];
+    float rm[NT][2];
+    {
+      const unsigned char* buf = smem + C::kQOff + (k & 1) * C::kQBufBytes;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        const uint32_t row = smem_u32(buf) + (8 * n + g) * C::kQRowBytes;
 #pragma unroll
-        for (int j = 0; j < MT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
-        m[n][0] = m[n][1] = -CUDART_INF_F;
-        l[n][0] = l[n][1] = 0.f;
+        for (int e = 0; e < NG; ++e) lds_words<4>(row + (4 * e + c4) * 16, qb[n][e]);
+        const uint32_t* zs = reinterpret_cast<const uint32_t*>(buf + C::kRows * C::kQRowBytes + (8 * n + g) * 32);
+        zb[n][0] = zs[c4];
+        zb[n][1] = zs[4 + c4];
+        const float* fr = reinterpret_cast<const float*>(buf + C::kRows * (C::kQRowBytes + 32)) + 8 * n;
+        rm[n][0] = fr[2 * c4];
+        rm[n][1] = fr[2 * c4 + 1];
       }
-      const int nb = share(cur);
-      for (int i = 0; i < nb; ++i) {
-        wait_block();
-        const uint32_t kp = ring + cur_st * C::kStageBytes, vp = kp + Pg::kBytes;
-        const int tok0 = (cur.b0 + warp + i * NW) * kBlockSize;
-        // S^T of keys g, g + 8
-        float s[NT][4];
-        {
-          uint32_t kw[2][NG], pw[2][NG];  // codes; scales then zeros as f16 pairs
+    }
+    // running state per row: maximum (before the row factor), the value that
+    // moves it, minus the maximum's logit, sum; O^T and the sum of p d
+    float o[NT][MT][4], od[NT][4];
+    float m[NT][2], thr[NT][2], mneg[NT][2], l[NT][2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            lds_words<NG>(kp + Pg::k_word(g + 8 * h, 0, c4), kw[h]);
-            lds_words<NG>(kp + Pg::k_scale(g + 8 * h, 0), pw[h]);
-          }
-          // zeros: lane c4 takes groups 2 c4, 2 c4 + 1 (modulo the groups)
-          uint32_t za[4];
-          za[0] = za[2] = NG == 4 ? ((c4 & 1) ? pw[0][NG - 1] : pw[0][NG / 2]) : pw[0][1];
-          za[1] = za[3] = NG == 4 ? ((c4 & 1) ? pw[1][NG - 1] : pw[1][NG / 2]) : pw[1][1];
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_f16_zero(s[n], za, zb[n][0], zb[n][1]);
+      for (int j = 0; j < MT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+      od[n][0] = od[n][1] = od[n][2] = od[n][3] = 0.f;
+      m[n][0] = m[n][1] = thr[n][0] = thr[n][1] = -CUDART_INF_F;
+      mneg[n][0] = mneg[n][1] = l[n][0] = l[n][1] = 0.f;
+    }
+    for (int bl = BP * warp; bl < nblk; bl += BP * NW) {
+      wait_for(ring_bars + cur_st * 8, cur_par);
+      const uint32_t stage = ring + cur_st * C::kStageBytes;
+      const int tok0 = (cur.b0 + bl) * kBlockSize;
+      // S^T of keys g, g + 8 of both blocks
+      float s[BP][NT][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] *= 0x1p-20f;
-          }
+      for (int j = 0; j < BP; ++j) {
+        const uint32_t kp = stage + j * C::kBlockBytes;
+        uint32_t kw[2][NG], sw[2][NG / 2], zw[2][1];  // codes, scales, the lane's pair of zeros
 #pragma unroll
-          for (int e = 0; e < NG; ++e) {
-            uint32_t a[4], b[4];
-            a[0] = kw[0][e] & 0x000f000fu;
-            a[1] = kw[1][e] & 0x000f000fu;
-            b[0] = kw[0][e] & 0x00f000f0u;
-            b[1] = kw[1][e] & 0x00f000f0u;
-            const uint32_t k0 = kw[0][e] >> 8, k1 = kw[1][e] >> 8;
-            a[2] = k0 & 0x000f000fu;
-            a[3] = k1 & 0x000f000fu;
-            b[2] = k0 & 0x00f000f0u;
-            b[3] = k1 & 0x00f000f0u;
-            const float2 f0 = half2_floats(pw[0][e / 2]), f1 = half2_floats(pw[1][e / 2]);
-            const float s0 = (e & 1) ? f0.y : f0.x, s1 = (e & 1) ? f1.y : f1.x;
+        for (int h = 0; h < 2; ++h) {
+          lds_words<NG>(kp + Pg::k_word(g + 8 * h, 0, c4), kw[h]);
+          lds_words<NG / 2>(kp + Pg::k_scale(g + 8 * h, 0), sw[h]);
+          // lane c4 takes groups 2 c4, 2 c4 + 1 (modulo the groups)
+          lds_words<1>(kp + Pg::k_scale(g + 8 * h, 0) + 2 * NG + (NG == 4 ? (c4 & 1) * 4 : 0), zw[h]);
+        }
+        const uint32_t za[4] = {zw[0][0], zw[1][0], zw[0][0], zw[1][0]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float acc[4];
-              mma_f16_zero(acc, a, qb[n][e][0], qb[n][e][1]);
-              mma_f16(acc, b, qb[n][e][2], qb[n][e][3]);
-              s[n][0] = fmaf(acc[0], s0, s[n][0]);
-              s[n][1] = fmaf(acc[1], s0, s[n][1]);
-              s[n][2] = fmaf(acc[2], s1, s[n][2]);
-              s[n][3] = fmaf(acc[3], s1, s[n][3]);
-            }
-          }
+        for (int n = 0; n < NT; ++n) mma_f16_zero(s[j][n], za, zb[n][0], zb[n][1]);
+#pragma unroll
+        for (int e = 0; e < NG; ++e) {
+          uint32_t a[4], b[4];
+          const uint32_t k0 = kw[0][e] >> 8, k1 = kw[1][e] >> 8;
+          a[0] = kw[0][e] & 0x000f000fu;
+          a[1] = kw[1][e] & 0x000f000fu;
+          a[2] = k0 & 0x000f000fu;
+          a[3] = k1 & 0x000f000fu;
+          b[0] = kw[0][e] & 0x00f000f0u;
+          b[1] = kw[1][e] & 0x00f000f0u;
+          b[2] = k0 & 0x00f000f0u;
+          b[3] = k1 & 0x00f000f0u;
+          const float2 f0 = half2_floats(sw[0][e / 2]), f1 = half2_floats(sw[1][e / 2]);
+          const float s0 = (e & 1) ? f0.y : f0.x, s1 = (e & 1) ? f1.y : f1.x;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            s[n][0] *= rm[n][0]; s[n][1] *= rm[n][1];
-            s[n][2] *= rm[n][0]; s[n][3] *= rm[n][1];
+            float acc[4];
+            mma_f16_zero(acc, a, qb[n][e][0], qb[n][e][1]);
+            mma_f16(acc, b, qb[n][e][2], qb[n][e][3]);
+            s[j][n][0] = fmaf(acc[0], s0, s[j][n][0]);
+            s[j][n][1] = fmaf(acc[1], s0, s[j][n][1]);
+            s[j][n][2] = fmaf(acc[2], s1, s[j][n][2]);
+            s[j][n][3] = fmaf(acc[3], s1, s[j][n][3]);
           }
         }
-        // V parameters: scales and zeros of tokens (2 c4, 2 c4 + 1) and
-        // (2 c4 + 8, 2 c4 + 9), all in the group of the lane's run of dims
-        uint32_t vq[4];
-        lds_words<4>(vp + Pg::kCodeBytes + (g * Pg::kRun / 32) * 64 + c4 * 16, vq);
-        if (tok0 + kBlockSize - 1 > cur.pos0 || tok0 + kBlockSize > cur.kv_hi) {
-          // causal edge or unwritten slots (their K, V and parameters may be anything)
+      }
+      // V parameters: scales and zeros of tokens (2 c4, 2 c4 + 1) and
+      // (2 c4 + 8, 2 c4 + 9), all in the group of the lane's run of dims
+      uint32_t vq[BP][4];
+#pragma unroll
+      for (int j = 0; j < BP; ++j)
+        lds_words<4>(stage + j * C::kBlockBytes + Pg::kBytes + Pg::kCodeBytes + (g * Pg::kRun / 32) * 64 +
+                         c4 * 16,
+                     vq[j]);
+      if (tok0 > plain_end) {
+        // causal edge, unwritten slots or no second block (K, V and parameters
+        // there may be anything)
+#pragma unroll
+        for (int j = 0; j < BP; ++j) {
+          const int tj = tok0 + j * kBlockSize;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int tok = tok0 + g + 8 * (e >> 1);
+              const int tok = tj + g + 8 * (e >> 1);
               const int jj = (8 * n + 2 * c4 + (e & 1)) / G;
-              if (tok >= cur.kv_hi || tok > cur.pos0 + jj) s[n][e] = -CUDART_INF_F;
+              if (tok >= kv_hi || tok > pos0 + jj) s[j][n][e] = -CUDART_INF_F;
             }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int left = cur.kv_hi - (tok0 + 2 * c4 + 8 * h);  // written tokens of the pair
+            const int left = kv_hi - (tj + 2 * c4 + 8 * h);  // written tokens of the pair
             const uint32_t keep = left >= 2 ? 0xffffffffu : (left == 1 ? 0x0000ffffu : 0u);
-            vq[h] &= keep;
-            vq[2 + h] &= keep;
+            vq[j][h] &= keep;
+            vq[j][2 + h] &= keep;
           }
         }
-        // online softmax (base 2)
-        float pr[NT][4];
-        bool grew = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          grew |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kI4Rescale ||
-                  fmaxf(s[n][1], s[n][3]) > m[n][1] + kI4Rescale;
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(m[n][e], fmaxf(s[n][e], s[n][2 + e]));
-#pragma unroll
-              for (int o8 = 4; o8 < 32; o8 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o8));
-              if (mx > m[n][e]) {
-                const float corr = ex2_approx(m[n][e] - mx);  // 0 before the first visible key
-                m[n][e] = mx;
-                l[n][e] *= corr;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  o[n][mt][e] *= corr;
-                  o[n][mt][2 + e] *= corr;
-                }
-              }
-            }
-        }
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float ms = m[n][e] == -CUDART_INF_F ? 0.f : m[n][e];
-            pr[n][e] = ex2_approx(s[n][e] - ms);
-            pr[n][2 + e] = ex2_approx(s[n][2 + e] - ms);
-            l[n][e] += pr[n][e] + pr[n][2 + e];
-          }
-          // P^T as the B operand: an 8 x 8 transpose per half of the block's keys
-          pb[n][0] = movm_trans(pack_f16(pr[n][0], pr[n][1]));
-          pb[n][1] = movm_trans(pack_f16(pr[n][2], pr[n][3]));
-        }
-        // O^T += V^T P^T
-        {
-          const uint32_t minus16 = 0xcc00cc00u;
-          const uint32_t z0 = fma_half2(vq[0], minus16, vq[2]), z1 = fma_half2(vq[1], minus16, vq[3]);
-          uint32_t vw[2][NG];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) lds_words<NG>(vp + h * 4 * D + g * (D / 2) + c4 * Pg::kRun, vw[h]);
-          __syncwarp();  // the stage has been read
-#pragma unroll
-          for (int w = 0; w < NG; ++w) {
-            uint32_t a[4], b[4];
-            a[0] = fma_half2(code_plus_16<0>(vw[0][w]), vq[0], z0);
-            a[1] = fma_half2(code_plus_16<1>(vw[0][w]), vq[0], z0);
-            a[2] = fma_half2(code_plus_16<0>(vw[1][w]), vq[1], z1);
-            a[3] = fma_half2(code_plus_16<1>(vw[1][w]), vq[1], z1);
-            b[0] = fma_half2(code_plus_16<2>(vw[0][w]), vq[0], z0);
-            b[1] = fma_half2(code_plus_16<3>(vw[0][w]), vq[0], z0);
-            b[2] = fma_half2(code_plus_16<2>(vw[1][w]), vq[1], z1);
-            b[3] = fma_half2(code_plus_16<3>(vw[1][w]), vq[1], z1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_f16(o[n][2 * w], a, pb[n][0], pb[n][1]);
-              mma_f16(o[n][2 * w + 1], b, pb[n][0], pb[n][1]);
-            }
-          }
-        }
-        // this stage is free: the stream's next block goes into it
-        if (++cur_st == NS) {
-          cur_st = 0;
-          cur_par ^= 1;
-        }
-        --in_flight;
-        issue_one(k + 1);
       }
-      // the warp's state for this unit -> shared memory (real rows only)
-      float* cb = comb + (k & 1) * NW * R * D;
-      float* cm = comb_ml + (k & 1) * NW * R * 2;
+      // online softmax
+      auto step_max = [&](int n, int e) {
+        float mx = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+        for (int j = 1; j < BP; ++j) mx = fmaxf(mx, fmaxf(s[j][n][e], s[j][n][2 + e]));
+        return mx;
+      };
+      bool grew = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float sum = l[n][e];
+        for (int e = 0; e < 2; ++e)
+          grew |= step_max(n, e) > thr[n][e];
+      if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-          for (int o8 = 4; o8 < 32; o8 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o8);
-          const int row = 8 * n + 2 * c4 + e;
-          if (row < R) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              *reinterpret_cast<float2*>(cb + (warp * R + row) * D + (D / 8) * g + 2 * mt) =
-                  make_float2(o[n][mt][e], o[n][mt][2 + e]);
-            if (g == 0) {
-              cm[(warp * R + row) * 2] = m[n][e];
-              cm[(warp * R + row) * 2 + 1] = sum;
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(m[n][e], step_max(n, e));
+#pragma unroll
+            for (int o8 = 4; o8 < 32; o8 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o8));
+            if (mx > m[n][e]) {
+              const float corr = ex2_approx((m[n][e] - mx) * rm[n][e]);  // 0 before the first visible key
+              m[n][e] = mx;
+              thr[n][e] = mx + kI4Rescale / rm[n][e];
+              mneg[n][e] = -mx * rm[n][e];
+              l[n][e] *= corr;
+              od[n][e] *= corr;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                o[n][mt][e] *= corr;
+                o[n][mt][2 + e] *= corr;
+              }
             }
           }
+      }
+      uint32_t pb[BP][NT][2];
+#pragma unroll
+      for (int j = 0; j < BP; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float pr[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(fmaf(s[j][n][e], rm[n][e & 1], mneg[n][e & 1]));
+          l[n][0] += pr[0] + pr[2];
+          l[n][1] += pr[1] + pr[3];
+          // P^T as the B operand: an 8 x 8 transpose per half of the block's keys
+          pb[j][n][0] = movm_trans(pack_f16(pr[0], pr[1]));
+          pb[j][n][1] = movm_trans(pack_f16(pr[2], pr[3]));
         }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int j = 0; j < BP; ++j) {
+        const uint32_t vp = stage + j * C::kBlockBytes + Pg::kBytes;
+        uint32_t vw[2][NG];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) lds_words<NG>(vp + h * 4 * D + g * (D / 2) + c4 * Pg::kRun, vw[h]);
+        const uint32_t s0 = vq[j][0], s1 = vq[j][1];
+        const uint32_t z0 = fma_half2(s0, 0xcc00cc00u, vq[j][2]), z1 = fma_half2(s1, 0xcc00cc00u, vq[j][3]);
+        {
+          // d of both token pairs in rows 0-7: row g's are of the lane's own group
+          const uint32_t da[4] = {sub_half2(vq[j][2], fma_half2(s0, 0x4c004c00u, z0)), 0u,
+                                  sub_half2(vq[j][3], fma_half2(s1, 0x4c004c00u, z1)), 0u};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(od[n], da, pb[j][n][0], pb[j][n][1]);
+        }
+#pragma unroll
+        for (int w = 0; w < NG; ++w) {
+          const uint32_t w0 = vw[0][w] >> 8, w1 = vw[1][w] >> 8;
+          uint32_t a[4], b[4];
+          a[0] = fma_half2(code_plus_16(vw[0][w], mul64), s0, z0);
+          a[1] = fma_half2(code_plus_16(vw[0][w], mul4), s0, z0);
+          a[2] = fma_half2(code_plus_16(vw[1][w], mul64), s1, z1);
+          a[3] = fma_half2(code_plus_16(vw[1][w], mul4), s1, z1);
+          b[0] = fma_half2(code_plus_16(w0, mul64), s0, z0);
+          b[1] = fma_half2(code_plus_16(w0, mul4), s0, z0);
+          b[2] = fma_half2(code_plus_16(w1, mul64), s1, z1);
+          b[3] = fma_half2(code_plus_16(w1, mul4), s1, z1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(o[n][2 * w], a, pb[j][n][0], pb[j][n][1]);
+            mma_f16(o[n][2 * w + 1], b, pb[j][n][0], pb[j][n][1]);
+          }
+        }
+      }
+      __syncwarp();  // the stage has been read: the stream's next pair goes into it
+      if (++cur_st == NS) {
+        cur_st = 0;
+        cur_par ^= 1;
+      }
+      --in_flight;
+      issue_one(k + 1);
     }
-    __syncthreads();
+    // the warp's state for this unit -> shared memory (real rows only), once the
+    // unit that used the buffer before has been read
+    if (k >= NB && !wait_for(bar_free + (k % NB) * 8, (k / NB - 1) & 1)) break;
+    float* cb = comb + (k % NB) * NW * R * D;
+    float* cm = comb_ml + (k % NB) * NW * R * 2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int o8 = 4; o8 < 32; o8 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o8);
+        const int row = 8 * n + 2 * c4 + e;
+        if (row < R) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            *reinterpret_cast<float2*>(cb + (warp * R + row) * D + (D / 8) * g + 2 * mt) =
+                make_float2(o[n][mt][e] + od[n][e], o[n][mt][2 + e] + od[n][e]);
+          if (g == 0) {
+            cm[(warp * R + row) * 2] = m[n][e] * rm[n][e];
+            cm[(warp * R + row) * 2 + 1] = sum;
+          }
+        }
+      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_full + (k % NB) * 8);
   }
-  if (sched) {
-    const UnitTail tail = s_tail;
-    if (tail.valid) finish_unit(tail, (k - 1) & 1);
+  // after a time-out: the copies under way land before the CTA ends
+  for (; in_flight > 0; --in_flight) {
+    for (uint32_t i = 0; i < kI4WaitLimit && !mbar_try_wait(ring_bars + cur_st * 8, cur_par); ++i) {
+    }
+    if (++cur_st == NS) {
+      cur_st = 0;
+      cur_par ^= 1;
+    }
   }
 }
 
@@ -643,20 +746,20 @@ namespace {
 
 // Launches the kernel, or with grid_only set only stores the grid size it
 // would use (CTAs per SM by occupancy x SMs).
-template <int D, int G, int P, int NW, int NS>
+template <int D, int G, int P, int NW, int NS, int BP>
 cudaError_t launch_i4(const AttnParams& p, int num_sms, cudaStream_t stream, int* grid_only) {
-  using C = I4Cfg<D, G, P, NW, NS>;
+  using C = I4Cfg<D, G, P, NW, NS, BP>;
   static int ctas_per_sm[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (ctas_per_sm[dev] == 0) {
-    e = cudaFuncSetAttribute(attn_int4_kernel<D, G, P, NW, NS>,
+    e = cudaFuncSetAttribute(attn_int4_kernel<D, G, P, NW, NS, BP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_int4_kernel<D, G, P, NW, NS>, C::kThreads,
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_int4_kernel<D, G, P, NW, NS, BP>, C::kThreads,
                                                       C::kSmemBytes);
     if (e != cudaSuccess) return e;
     ctas_per_sm[dev] = n > 0 ? n : 1;
@@ -677,15 +780,15 @@ cudaError_t launch_i4(const AttnParams& p, int num_sms, cudaStream_t stream, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.after_plan ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_int4_kernel<D, G, P, NW, NS>, p);
+  return cudaLaunchKernelEx(&cfg, attn_int4_kernel<D, G, P, NW, NS, BP>, p);
 }
 
 template <int D, int G>
 cudaError_t dispatch_positions_int4(const AttnParams& p, int positions, int num_sms,
                                     cudaStream_t stream, int* grid_only) {
-  constexpr int NS = D == 128 ? 4 : 8;
-  return positions == 1 ? launch_i4<D, G, 1, 4, NS>(p, num_sms, stream, grid_only)
-                        : launch_i4<D, G, kSmallRows / G, 4, NS>(p, num_sms, stream, grid_only);
+  constexpr int NS = D == 128 ? PA_I4_NS : PA_I4_NS64;
+  return positions == 1 ? launch_i4<D, G, 1, PA_I4_NW, NS, 2>(p, num_sms, stream, grid_only)
+                        : launch_i4<D, G, kSmallRows / G, 3, PA_I4_SNS, PA_I4_SBP>(p, num_sms, stream, grid_only);
 }
 
 template <int D>
