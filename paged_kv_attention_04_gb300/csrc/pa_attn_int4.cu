@@ -61,6 +61,9 @@
 #ifndef PA_I4_SBP
 #define PA_I4_SBP 1
 #endif
+#ifndef PA_I4_NB
+#define PA_I4_NB 2
+#endif
 #ifndef PA_I4_NS
 #define PA_I4_NS 2
 #endif
@@ -72,7 +75,7 @@ namespace pa {
 
 namespace {
 
-constexpr uint32_t kI4WaitLimit = 1u << 22;
+constexpr uint32_t kI4WaitLimit = 1u << 18;
 constexpr float kI4Rescale = 8.f;  // base-2 logit growth that moves the running maximum
 
 template <int D, int G, int P, int NW, int NS, int BP>
@@ -80,7 +83,6 @@ struct I4Cfg {
   using Pg = I4Page<D>;
   static constexpr int kR = P * G;               // real query rows
   static constexpr int kNT = (kR + 7) / 8;       // n-tiles of 8 query rows
-  static constexpr int kRows = 8 * kNT;          // with padding
   static constexpr int kGroups = D / 32;
   static constexpr int kMT = D / 16;             // m-tiles of O^T
   static constexpr int kThreads = (NW + 1) * 32;
@@ -89,18 +91,18 @@ struct I4Cfg {
   static constexpr int kRingBytes = NW * NS * kStageBytes;
   // q buffer: rows of D f16, then per row 16 f16 (group sums) and a float factor
   static constexpr int kQRowBytes = D * 2;
-  static constexpr int kQBufBytes = kRows * (kQRowBytes + 32 + 4);
+  static constexpr int kQBufBytes = (kR * (kQRowBytes + 32 + 4) + 15) / 16 * 16;
   static constexpr int kQOff = kRingBytes;
   // the warps' states of finished units: two units' for decode tiles, one for
   // 16 rows (64 KB a pair)
-  static constexpr int kNB = kNT == 1 ? 2 : 1;
+  static constexpr int kNB = kNT == 1 ? PA_I4_NB : 1;
   static constexpr int kCombOff = kQOff + 2 * kQBufBytes;
   static constexpr int kCombBytes = kNB * NW * kR * D * 4;
   static constexpr int kMlOff = kCombOff + kCombBytes;
   static constexpr int kMlBytes = kNB * NW * kR * 2 * 4;
   static constexpr int kMetaOff = (kMlOff + kMlBytes + 15) / 16 * 16;
   static constexpr int kBarOff = kMetaOff + 2 * ((static_cast<int>(sizeof(UnitMeta)) + 15) / 16 * 16);
-  static constexpr int kNumBars = NW * NS + 2 + 2 * kNB;
+  static constexpr int kNumBars = 2 + 2 * kNB;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8;
   static constexpr int kFit = (228 * 1024) / (kSmemBytes + 1024 + 64);
   static constexpr int kMinCtas = kFit < PA_I4_CTAS ? kFit : PA_I4_CTAS;
@@ -153,6 +155,18 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
   asm volatile("mov.u32 %0, %0;\n" : "+r"(x));
   return x;
 }
+// mbar_try_wait that may suspend the thread for some 16 us: a waiting warp takes
+// few issue slots from the others.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(16384u)
+      : "memory");
+  return ok != 0;
+}
 // Whether phase `parity` has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -186,14 +200,13 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     return *reinterpret_cast<UnitMeta*>(smem + C::kMetaOff +
                                         (k & 1) * ((static_cast<int>(sizeof(UnitMeta)) + 15) / 16 * 16));
   };
-  // mbarriers: the ring stages of every warp, then
-  const uint32_t bars = smem_u32(smem + C::kBarOff);
-  const uint32_t bar_unit = bars + NW * NS * 8;   // [2] unit published (scheduler)
+  // mbarriers
+  const uint32_t bar_unit = smem_u32(smem + C::kBarOff);  // [2] unit published (scheduler)
   const uint32_t bar_full = bar_unit + 16;        // [NB] states written (NW warps)
   const uint32_t bar_free = bar_full + NB * 8;    // [NB] ... and read (scheduler)
   if (tid < C::kNumBars) {
-    const bool full = tid >= NW * NS + 2 && tid < NW * NS + 2 + NB;
-    mbar_init(bars + tid * 8, full ? NW : 1);
+    const bool full = tid >= 2 && tid < 2 + NB;
+    mbar_init(bar_unit + tid * 8, full ? NW : 1);
   }
   if (tid == 0) s_abort = 0;
   mbar_fence_init();
@@ -202,15 +215,16 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
 
   // Bounded wait (whole warp) for phase `parity`; false if it gave up.
   auto wait_for = [&](uint32_t bar, uint32_t parity) -> bool {
-    if (!mbar_try_wait(bar, parity)) {
-      const uint32_t limit = *reinterpret_cast<volatile int*>(&s_abort) ? 1024u : kI4WaitLimit;
-      if (!mbar_wait(bar, parity, limit)) {
+    bool ok = mbar_try_wait_long(bar, parity);
+    if (!ok) {
+      const uint32_t limit = *reinterpret_cast<volatile int*>(&s_abort) ? 16u : kI4WaitLimit;
+      for (uint32_t i = 0; i < limit && !ok; ++i) ok = mbar_try_wait_long(bar, parity);
+      if (!ok) {
         s_abort = 1;
         flag_error(p.status, PA_DEV_TIMEOUT);
       }
     }
-    __syncwarp();
-    return *reinterpret_cast<volatile int*>(&s_abort) == 0;
+    return __all_sync(0xffffffffu, ok);
   };
 
   if (warp == NW) {
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     // q rows of unit m (row = position row/G, head row%G) into buffer buf, eight
     // dims a lane and step, a row's chunks in adjacent lanes.
     constexpr int kRowChunks = D / 8;
-    constexpr int kQPerLane = C::kRows * kRowChunks / 32;
+    constexpr int kQPerLane = (R * kRowChunks + 31) / 32;
     auto stage_q = [&](const UnitMeta& m, int buf) {
       unsigned char* qb = smem + C::kQOff + buf * C::kQBufBytes;
       uint4 qv[kQPerLane];
@@ -281,11 +295,12 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         // the fragments of the group's two k-steps: nibbles (0, 4), (2, 6) and (1, 5), (3, 7)
+        if (row >= R) continue;
         *reinterpret_cast<uint4*>(qb + row * C::kQRowBytes + c * 16) =
             make_uint4(pack_f16(16.f * x[0], 16.f * x[4]), pack_f16(16.f * x[2], 16.f * x[6]),
                        pack_f16(x[1], x[5]), pack_f16(x[3], x[7]));
         // group sums x 2^-20 in f16 parts: element NG j + g is part j of group g
-        __half* zs = reinterpret_cast<__half*>(qb + C::kRows * C::kQRowBytes + row * 32);
+        __half* zs = reinterpret_cast<__half*>(qb + R * C::kQRowBytes + row * 32);
         if ((c & 3) == 0) {
           const int g = c >> 2;
           sum *= 0x1p-20f;
@@ -297,7 +312,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
           }
         }
         if (c == 0)  // base-2 logit = (accumulated sum) x factor; kept positive
-          *reinterpret_cast<float*>(qb + C::kRows * (C::kQRowBytes + 32) + row * 4) =
+          *reinterpret_cast<float*>(qb + R * (C::kQRowBytes + 32) + row * 4) =
               fmaxf(fabsf(p.scale_log2) * 1048576.f *
                         __uint_as_float(static_cast<uint32_t>(ex - 10 + 127) << 23),
                     1e-37f);
@@ -440,7 +455,6 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
   // ------------------------------------------------------------ compute warps
   const int g = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * (NS * C::kStageBytes);
-  const uint32_t ring_bars = bars + warp * (NS * 8);
   const uint32_t mul64 = opaque(64u), mul4 = opaque(4u);
 
   // ---- the stream of block pairs: this warp's share of unit k, then of unit k+1
@@ -449,9 +463,6 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
   int iss_g = 0;
   bool iss_end = false;             // no unit after it
   int iss_st = 0, in_flight = 0;    // ring stage of the next issue, stages under way
-  // lanes 0-3 copy the pair's K and V pages: block lane / 2, K (0) or V (1)
-  const unsigned char* my_cache = static_cast<const unsigned char*>((lane & 1) ? p.v_cache : p.k_cache);
-  const uint32_t my_dst = (lane >> 1) * C::kBlockBytes + (lane & 1) * Pg::kBytes;
 
   // Issue the next pair if it lies in unit `limit` or earlier and is known.
   auto issue_one = [&](int limit) -> bool {
@@ -466,35 +477,32 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       iss_bl = BP * warp;
       iss_g = m.g;
     }
-    const int bl = iss_bl + (lane >> 1);
-    const bool want = lane < 2 * BP && bl < iss_n;
-    const int phys = want ? meta(iss_unit).bt[bl] : 0;
-    const bool ok = want && static_cast<uint32_t>(phys) < static_cast<uint32_t>(p.num_blocks);
-    const uint32_t st = ring + iss_st * C::kStageBytes, bar = ring_bars + iss_st * 8;
-    const uint32_t copies = __ballot_sync(0xffffffffu, ok);
-    if (__any_sync(0xffffffffu, want && !ok)) {  // a bad table entry reads as zeros
-      if (want && !ok) {
-        for (int i = 0; i < Pg::kBytes / 16; ++i)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(st + my_dst + i * 16), "r"(0u)
-                       : "memory");
-        fence_proxy_async_smem();  // before a later copy into this stage
-        flag_error(p.status, PA_DEV_BLOCK_RANGE);
-      }
-      __syncwarp();
+    const uint32_t st = ring + iss_st * C::kStageBytes + lane * 16;
+    const int32_t* bt = meta(iss_unit).bt + iss_bl;
+#pragma unroll
+    for (int b = 0; b < BP; ++b) {
+      // an absent block and one with a bad table entry become zeros
+      const bool want = iss_bl + b < iss_n;
+      const int phys = want ? bt[b] : 0;
+      const bool ok = static_cast<uint32_t>(phys) < static_cast<uint32_t>(p.num_blocks);
+      if (!ok && lane == 0) flag_error(p.status, PA_DEV_BLOCK_RANGE);
+      const int bytes = want && ok ? 16 : 0;
+      const long long off = (static_cast<long long>(phys) * Hkv + iss_g) * Pg::kBytes + lane * 16;
+      const unsigned char* ks = static_cast<const unsigned char*>(p.k_cache) + off;
+      const unsigned char* vs = static_cast<const unsigned char*>(p.v_cache) + off - Pg::kBytes;
+#pragma unroll
+      for (int i = 0; i < C::kBlockBytes; i += 512)  // the K page, then the V page, 512 bytes a step
+        if (i + 512 <= C::kBlockBytes || lane * 16 < C::kBlockBytes - i)
+          cp_async16(st + b * C::kBlockBytes + i, (i + lane * 16 < Pg::kBytes ? ks : vs) + i, bytes);
     }
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(copies) * Pg::kBytes);
-    __syncwarp();
-    if (ok)
-      bulk_load(st + my_dst, my_cache + (static_cast<long long>(phys) * Hkv + iss_g) * Pg::kBytes,
-                Pg::kBytes, bar);
+    cp_async_commit();
     iss_st = iss_st + 1 == NS ? 0 : iss_st + 1;
     iss_bl += BP * NW;
     ++in_flight;
     return true;
   };
 
-  int cur_st = 0;        // ring stage of the next pair to compute
-  uint32_t cur_par = 0;  // and its mbarrier phase
+  int cur_st = 0;  // ring stage of the next pair to compute
   for (int k = 0;; ++k) {
     if (!wait_for(bar_unit + (k & 1) * 8, (k >> 1) & 1)) break;
     const UnitMeta& cur = meta(k);
@@ -511,15 +519,16 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       const unsigned char* buf = smem + C::kQOff + (k & 1) * C::kQBufBytes;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint32_t row = smem_u32(buf) + (8 * n + g) * C::kQRowBytes;
+        const int r = min(8 * n + g, R - 1);  // (columns past the last row repeat it)
+        const uint32_t row = smem_u32(buf) + r * C::kQRowBytes;
 #pragma unroll
         for (int e = 0; e < NG; ++e) lds_words<4>(row + (4 * e + c4) * 16, qb[n][e]);
-        const uint32_t* zs = reinterpret_cast<const uint32_t*>(buf + C::kRows * C::kQRowBytes + (8 * n + g) * 32);
+        const uint32_t* zs = reinterpret_cast<const uint32_t*>(buf + R * C::kQRowBytes + r * 32);
         zb[n][0] = zs[c4];
         zb[n][1] = zs[4 + c4];
-        const float* fr = reinterpret_cast<const float*>(buf + C::kRows * (C::kQRowBytes + 32)) + 8 * n;
-        rm[n][0] = fr[2 * c4];
-        rm[n][1] = fr[2 * c4 + 1];
+        const float* fr = reinterpret_cast<const float*>(buf + R * (C::kQRowBytes + 32));
+        rm[n][0] = fr[min(8 * n + 2 * c4, R - 1)];
+        rm[n][1] = fr[min(8 * n + 2 * c4 + 1, R - 1)];
       }
     }
     // running state per row: maximum (before the row factor), the value that
@@ -535,7 +544,8 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       mneg[n][0] = mneg[n][1] = l[n][0] = l[n][1] = 0.f;
     }
     for (int bl = BP * warp; bl < nblk; bl += BP * NW) {
-      wait_for(ring_bars + cur_st * 8, cur_par);
+      if (in_flight == NS) cp_async_wait<NS - 1>(); else cp_async_wait<0>();
+      __syncwarp();
       const uint32_t stage = ring + cur_st * C::kStageBytes;
       const int tok0 = (cur.b0 + bl) * kBlockSize;
       // S^T of keys g, g + 8 of both blocks
@@ -697,10 +707,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
         }
       }
       __syncwarp();  // the stage has been read: the stream's next pair goes into it
-      if (++cur_st == NS) {
-        cur_st = 0;
-        cur_par ^= 1;
-      }
+      cur_st = cur_st + 1 == NS ? 0 : cur_st + 1;
       --in_flight;
       issue_one(k + 1);
     }
@@ -731,15 +738,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_full + (k % NB) * 8);
   }
-  // after a time-out: the copies under way land before the CTA ends
-  for (; in_flight > 0; --in_flight) {
-    for (uint32_t i = 0; i < kI4WaitLimit && !mbar_try_wait(ring_bars + cur_st * 8, cur_par); ++i) {
-    }
-    if (++cur_st == NS) {
-      cur_st = 0;
-      cur_par ^= 1;
-    }
-  }
+  cp_async_wait<0>();
 }
 
 namespace {
