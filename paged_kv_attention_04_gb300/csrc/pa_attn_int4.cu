@@ -64,6 +64,9 @@
 #ifndef PA_I4_NB
 #define PA_I4_NB 2
 #endif
+#ifndef PA_I4_PREFETCH
+#define PA_I4_PREFETCH 0
+#endif
 #ifndef PA_I4_NS
 #define PA_I4_NS 2
 #endif
@@ -145,9 +148,13 @@ __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 16 + c as f16 of the nibbles of both halves of w that `mul` moves to bits 6-9
-__device__ __forceinline__ uint32_t code_plus_16(uint32_t w, uint32_t mul) {
-  return ((w * mul) & 0x03c003c0u) | 0x4c004c00u;
+// 16 + c as f16 of the nibbles of both halves of w that `mul` moves to bits 6-9;
+// sixteen = 16.0 in both halves, in a register (an instruction takes one
+// constant, so with two the masked OR would be two).
+__device__ __forceinline__ uint32_t code_plus_16(uint32_t w, uint32_t mul, uint32_t sixteen) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;\n" : "=r"(r) : "r"(w * mul), "r"(sixteen));
+  return r;
 }
 // A constant the compiler does not see through (it would turn a multiplication
 // by a power of two back into a shift).
@@ -245,7 +252,17 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       const UnitRec* rec = p.recs + item;
       const int4 ra = __ldg(&rec->a), rb = __ldg(&rec->b), rc = __ldg(&rec->c);
       const int32_t* row = p.block_tables + static_cast<long long>(ra.x) * p.max_blocks_per_seq;
-      for (int i = lane; i < ra.w - ra.z; i += 32) m.bt[i] = __ldg(row + ra.z + i);
+      // a bad entry, and the one after an odd count, become -1: a block of zeros
+      const int n = ra.w - ra.z;
+      for (int i = lane; i < n; i += 32) {
+        int b = __ldg(row + ra.z + i);
+        if (static_cast<uint32_t>(b) >= static_cast<uint32_t>(p.num_blocks)) {
+          flag_error(p.status, PA_DEV_BLOCK_RANGE);
+          b = -1;
+        }
+        m.bt[i] = b;
+      }
+      if (lane == 0 && (n & 1)) m.bt[n] = -1;
       if (lane == 0) {
         m.valid = 1; m.item = item; m.g = u - k * Hkv; m.r = ra.x; m.a = rb.w; m.j0 = ra.y;
         m.npos = rc.x; m.pos0 = rc.y; m.kv_hi = rc.z; m.b0 = ra.z; m.b1 = ra.w;
@@ -455,12 +472,15 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
   // ------------------------------------------------------------ compute warps
   const int g = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * (NS * C::kStageBytes);
-  const uint32_t mul64 = opaque(64u), mul4 = opaque(4u);
+  const uint32_t mul64 = opaque(64u), mul4 = opaque(4u), sixteen = opaque(0x4c004c00u);
 
   // ---- the stream of block pairs: this warp's share of unit k, then of unit k+1
   int iss_unit = -1;                // unit being issued
   int iss_bl = 0, iss_n = 0;        // its next pair's first block, its blocks
-  int iss_g = 0;
+  const unsigned char* iss_k = nullptr;  // block 0's K page of its head, at this lane's 16 bytes
+  const uint32_t block_stride = static_cast<uint32_t>(Hkv) * Pg::kBytes;
+  const long long k_to_v = static_cast<const unsigned char*>(p.v_cache) -
+                           static_cast<const unsigned char*>(p.k_cache) - Pg::kBytes;
   bool iss_end = false;             // no unit after it
   int iss_st = 0, in_flight = 0;    // ring stage of the next issue, stages under way
 
@@ -475,25 +495,28 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       iss_end = !m.valid;
       iss_n = m.valid ? m.b1 - m.b0 : 0;
       iss_bl = BP * warp;
-      iss_g = m.g;
+      iss_k = static_cast<const unsigned char*>(p.k_cache) + m.g * Pg::kBytes + lane * 16;
     }
     const uint32_t st = ring + iss_st * C::kStageBytes + lane * 16;
     const int32_t* bt = meta(iss_unit).bt + iss_bl;
 #pragma unroll
     for (int b = 0; b < BP; ++b) {
-      // an absent block and one with a bad table entry become zeros
-      const bool want = iss_bl + b < iss_n;
-      const int phys = want ? bt[b] : 0;
-      const bool ok = static_cast<uint32_t>(phys) < static_cast<uint32_t>(p.num_blocks);
-      if (!ok && lane == 0) flag_error(p.status, PA_DEV_BLOCK_RANGE);
-      const int bytes = want && ok ? 16 : 0;
-      const long long off = (static_cast<long long>(phys) * Hkv + iss_g) * Pg::kBytes + lane * 16;
-      const unsigned char* ks = static_cast<const unsigned char*>(p.k_cache) + off;
-      const unsigned char* vs = static_cast<const unsigned char*>(p.v_cache) + off - Pg::kBytes;
+      const int phys = bt[b];
+      const int bytes = phys >= 0 ? 16 : 0;
+      const unsigned char* ks = iss_k + static_cast<unsigned long long>(static_cast<uint32_t>(max(phys, 0))) * block_stride;
+      const unsigned char* vs = ks + k_to_v;
 #pragma unroll
       for (int i = 0; i < C::kBlockBytes; i += 512)  // the K page, then the V page, 512 bytes a step
         if (i + 512 <= C::kBlockBytes || lane * 16 < C::kBlockBytes - i)
           cp_async16(st + b * C::kBlockBytes + i, (i + lane * 16 < Pg::kBytes ? ks : vs) + i, bytes);
+      if (PA_I4_PREFETCH && lane < (C::kBlockBytes + 127) / 128) {
+        // towards L2: the lines of the block that goes into this place next
+        const int next = iss_bl + b + BP * NW < iss_n ? bt[b + BP * NW] : -1;
+        if (next >= 0)
+          asm volatile("prefetch.global.L2 [%0];\n" ::"l"(
+              (lane * 128 < Pg::kBytes ? iss_k : iss_k + k_to_v) + lane * 112 +
+              static_cast<unsigned long long>(static_cast<uint32_t>(next)) * block_stride));
+      }
     }
     cp_async_commit();
     iss_st = iss_st + 1 == NS ? 0 : iss_st + 1;
@@ -691,14 +714,14 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
         for (int w = 0; w < NG; ++w) {
           const uint32_t w0 = vw[0][w] >> 8, w1 = vw[1][w] >> 8;
           uint32_t a[4], b[4];
-          a[0] = fma_half2(code_plus_16(vw[0][w], mul64), s0, z0);
-          a[1] = fma_half2(code_plus_16(vw[0][w], mul4), s0, z0);
-          a[2] = fma_half2(code_plus_16(vw[1][w], mul64), s1, z1);
-          a[3] = fma_half2(code_plus_16(vw[1][w], mul4), s1, z1);
-          b[0] = fma_half2(code_plus_16(w0, mul64), s0, z0);
-          b[1] = fma_half2(code_plus_16(w0, mul4), s0, z0);
-          b[2] = fma_half2(code_plus_16(w1, mul64), s1, z1);
-          b[3] = fma_half2(code_plus_16(w1, mul4), s1, z1);
+          a[0] = fma_half2(code_plus_16(vw[0][w], mul64, sixteen), s0, z0);
+          a[1] = fma_half2(code_plus_16(vw[0][w], mul4, sixteen), s0, z0);
+          a[2] = fma_half2(code_plus_16(vw[1][w], mul64, sixteen), s1, z1);
+          a[3] = fma_half2(code_plus_16(vw[1][w], mul4, sixteen), s1, z1);
+          b[0] = fma_half2(code_plus_16(w0, mul64, sixteen), s0, z0);
+          b[1] = fma_half2(code_plus_16(w0, mul4, sixteen), s0, z0);
+          b[2] = fma_half2(code_plus_16(w1, mul64, sixteen), s1, z1);
+          b[3] = fma_half2(code_plus_16(w1, mul4, sixteen), s1, z1);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             mma_f16(o[n][2 * w], a, pb[j][n][0], pb[j][n][1]);
