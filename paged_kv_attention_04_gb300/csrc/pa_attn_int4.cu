@@ -78,7 +78,7 @@ namespace pa {
 
 namespace {
 
-constexpr uint32_t kI4WaitLimit = 1u << 18;
+constexpr unsigned long long kI4WaitNs = 2000000000ull;  // a wait gives up after two seconds
 constexpr float kI4Rescale = 8.f;  // base-2 logit growth that moves the running maximum
 
 template <int D, int G, int P, int NW, int NS, int BP>
@@ -162,17 +162,10 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
   asm volatile("mov.u32 %0, %0;\n" : "+r"(x));
   return x;
 }
-// mbar_try_wait that may suspend the thread for some 16 us: a waiting warp takes
-// few issue slots from the others.
-__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(16384u)
-      : "memory");
-  return ok != 0;
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+  return t;
 }
 // Whether phase `parity` has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -222,10 +215,11 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
 
   // Bounded wait (whole warp) for phase `parity`; false if it gave up.
   auto wait_for = [&](uint32_t bar, uint32_t parity) -> bool {
-    bool ok = mbar_try_wait_long(bar, parity);
+    bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
-      const uint32_t limit = *reinterpret_cast<volatile int*>(&s_abort) ? 16u : kI4WaitLimit;
-      for (uint32_t i = 0; i < limit && !ok; ++i) ok = mbar_try_wait_long(bar, parity);
+      const unsigned long long t0 = now_ns();
+      while (!ok && *reinterpret_cast<volatile int*>(&s_abort) == 0 && now_ns() - t0 < kI4WaitNs)
+        ok = mbar_try_wait(bar, parity);
       if (!ok) {
         s_abort = 1;
         flag_error(p.status, PA_DEV_TIMEOUT);
@@ -243,10 +237,6 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     // Metadata of unit u into m: one precomputed record and the unit's slice of
     // the block table.
     auto fetch_unit = [&](UnitMeta& m, int u) {
-      if (u >= n_units) {
-        if (lane == 0) m.valid = 0;
-        return;
-      }
       const int k = u / Hkv;
       const int item = p.order ? __ldg(p.order + k) : k;
       const UnitRec* rec = p.recs + item;
@@ -338,13 +328,13 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     auto publish = [&](int k, int u) {  // unit k of the sequence is unit u of the list
       UnitMeta& m = meta(k);
       fetch_unit(m, u);
-      if (u < n_units) stage_q(m, k & 1);
+      stage_q(m, k & 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_unit + (k & 1) * 8);
     };
-    // Join the warps' states of a finished unit, write the output or the split's
-    // partial, and merge the splits if it is the last.
-    auto finish_unit = [&](const UnitTail& u, int buf) {
+    // Join the warps' states of a finished unit and write the output or the split's
+    // partial; true if that was the tile's last split.
+    auto finish_unit = [&](const UnitTail& u, int buf) -> bool {
       const float* cb = comb + buf * NW * R * D;
       const float* cm = comb_ml + buf * NW * R * 2;
       const long long part_base = (static_cast<long long>(u.item) * Hkv + u.g) * R;
@@ -366,6 +356,9 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
             num.z = fmaf(c4.z, f, num.z); num.w = fmaf(c4.w, f, num.w);
             den = fmaf(cm[(w * R + row) * 2 + 1], f, den);
           }
+        } else {  // no visible key (0), or logits of NaN alone (NaN)
+#pragma unroll
+          for (int w = 0; w < NW; ++w) den += cm[(w * R + row) * 2 + 1];
         }
         if (u.nsplit == 1) {
           const long long tok = u.a + u.j0 + jj;
@@ -379,62 +372,15 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_free + buf * 8);  // the states have been read
-      if (u.nsplit > 1) {
+      if (u.nsplit == 1) return false;
+      __threadfence();
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) {
+        last = atomicAdd(p.merge_cnt + u.tile * Hkv + u.g, 1) == u.nsplit - 1;
         __threadfence();
-        __syncwarp();
-        int last = 0;
-        if (lane == 0) last = atomicAdd(p.merge_cnt + u.tile * Hkv + u.g, 1) == u.nsplit - 1;
-        last = __shfl_sync(0xffffffffu, last, 0);
-        if (last) {
-          __threadfence();
-          // groups of kMergeChunk partials, loaded before any is used: one L2
-          // round trip a group
-          constexpr int kMergeChunk = 4;
-#pragma unroll 2
-          for (int idx = lane; idx < R * D / 4; idx += 32) {
-            const int row = (idx * 4) / D, d = idx * 4 - row * D;
-            const int jj = row / G, hh = row - jj * G;
-            if (jj >= u.npos) continue;
-            float M = -CUDART_INF_F, den = 0.f;
-            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int sp0 = 0; sp0 < u.nsplit; sp0 += kMergeChunk) {
-              float2 ml[kMergeChunk];
-              float4 a4[kMergeChunk];
-#pragma unroll
-              for (int j = 0; j < kMergeChunk; ++j) {
-                ml[j] = make_float2(-CUDART_INF_F, 0.f);
-                a4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (sp0 + j < u.nsplit) {
-                  const long long pb = (static_cast<long long>(u.first + sp0 + j) * Hkv + u.g) * R + row;
-                  ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + pb * 2));
-                  a4[j] = __ldcg(reinterpret_cast<const float4*>(p.part_acc + pb * D + d));
-                }
-              }
-              // a split with no visible key for this row holds (-inf, 0) and zeros
-              float mc = M;
-#pragma unroll
-              for (int j = 0; j < kMergeChunk; ++j) mc = fmaxf(mc, ml[j].x);
-              if (mc == -CUDART_INF_F) continue;
-              if (mc > M) {  // rescale the running sums to the new maximum
-                const float sc = ex2_approx(M - mc);  // 0 while nothing was visible
-                num.x *= sc; num.y *= sc; num.z *= sc; num.w *= sc; den *= sc;
-                M = mc;
-              }
-#pragma unroll
-              for (int j = 0; j < kMergeChunk; ++j) {
-                const float f = ex2_approx(ml[j].x - M);  // 0 for an empty split
-                num.x = fmaf(a4[j].x, f, num.x); num.y = fmaf(a4[j].y, f, num.y);
-                num.z = fmaf(a4[j].z, f, num.z); num.w = fmaf(a4[j].w, f, num.w);
-                den = fmaf(ml[j].y, f, den);
-              }
-            }
-            const long long tok = u.a + u.j0 + jj;
-            const float inv = p.out_scale / den;
-            *reinterpret_cast<uint2*>(out + (tok * Hq + u.g * G + hh) * D + d) =
-                make_uint2(pack_bf16(num.x * inv, num.y * inv), pack_bf16(num.z * inv, num.w * inv));
-          }
-        }
       }
+      return __shfl_sync(0xffffffffu, last, 0) != 0;
     };
     // A CTA's first unit is its own index, later ones count on from the grid
     // size; a second one is claimed up front only if every CTA can still get one.
@@ -444,27 +390,54 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       if (lane == 0) u = grid + atomicAdd(p.next, 1);
       return __shfl_sync(0xffffffffu, u, 0);
     };
-    const int u0 = blockIdx.x;
-    publish(0, u0);
-    bool more[2] = {u0 < n_units, false};  // units k, k + 1 are real
-    {
-      const int u1 = u0 + grid < n_units ? claim() : n_units;
-      publish(1, u1);
-      more[1] = u1 < n_units;
-    }
-    for (int k = 0; more[0]; ++k) {
-      if (!wait_for(bar_full + (k % NB) * 8, (k / NB) & 1)) break;
+    auto publish_merge = [&](int k, const UnitTail& t) {  // a merge as unit k
+      __syncwarp();
+      if (lane == 0) {
+        UnitMeta& m = meta(k);
+        m.valid = 2; m.g = t.g; m.a = t.a; m.j0 = t.j0; m.npos = t.npos;
+        m.nsplit = t.nsplit; m.first = t.first; m.b0 = 0; m.b1 = 0;
+        mbar_arrive(bar_unit + (k & 1) * 8);
+      }
+      __syncwarp();
+    };
+    int published = 0;  // units published so far
+    bool left = true;   // the list may hold more
+    auto publish_next = [&](int u) {
+      left = u < n_units;
+      if (left) publish(published++, u);
+    };
+    publish_next(blockIdx.x);
+    if (left) publish_next(static_cast<int>(blockIdx.x) + grid < n_units ? claim() : n_units);
+    UnitTail merge;
+    merge.valid = 0;  // a merge to publish
+    int k = 0;
+    for (; k < published; ++k) {
+      if (!wait_for(bar_full + (k % NB) * 8, (k / NB) & 1)) return;
       const UnitMeta& m = meta(k);
       UnitTail t;
-      t.valid = 1; t.item = m.item; t.g = m.g; t.a = m.a; t.j0 = m.j0;
+      t.valid = m.valid; t.item = m.item; t.g = m.g; t.a = m.a; t.j0 = m.j0;
       t.npos = m.npos; t.tile = m.tile; t.nsplit = m.nsplit; t.first = m.first;
       __syncwarp();
-      // the finished unit's slot takes the unit after the next
-      const int u2 = more[1] ? claim() : n_units;
-      publish(k + 2, u2);
-      finish_unit(t, k % NB);
-      more[0] = more[1];
-      more[1] = u2 < n_units;
+      // the finished unit's slot takes the next one, a merge before a new unit
+      if (merge.valid) {
+        publish_merge(published++, merge);
+        merge.valid = 0;
+      } else if (left) {
+        publish_next(claim());
+      }
+      if (t.valid == 1) {
+        if (finish_unit(t, k % NB)) merge = t;
+      } else if (lane == 0) {
+        mbar_arrive(bar_free + (k % NB) * 8);
+      }
+      if (merge.valid && published <= k + 2) {
+        publish_merge(published++, merge);
+        merge.valid = 0;
+      }
+    }
+    if (lane == 0) {  // the end
+      meta(k).valid = 0;
+      mbar_arrive(bar_unit + (k & 1) * 8);
     }
     return;
   }
@@ -492,7 +465,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       if (!mbar_test(bar_unit + (k & 1) * 8, (k >> 1) & 1)) return false;
       const UnitMeta& m = meta(k);
       iss_unit = k;
-      iss_end = !m.valid;
+      iss_end = m.valid == 0;
       iss_n = m.valid ? m.b1 - m.b0 : 0;
       iss_bl = BP * warp;
       iss_k = static_cast<const unsigned char*>(p.k_cache) + m.g * Pg::kBytes + lane * 16;
@@ -525,11 +498,77 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     return true;
   };
 
+  // Merge of a split tile, one float4 of the output a thread; the partials of
+  // kMergeChunk splits are loaded before any is used: one L2 round trip for all.
+  auto merge_splits = [&](const UnitMeta& u) {
+    constexpr int kMergeChunk = 8;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+    for (int idx = warp * 32 + lane; idx < R * D / 4; idx += NW * 32) {
+      const int row = (idx * 4) / D, d = idx * 4 - row * D;
+      const int jj = row / G, hh = row - jj * G;
+      if (jj >= u.npos) continue;
+      float M = -CUDART_INF_F, den = 0.f;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int sp0 = 0; sp0 < u.nsplit; sp0 += kMergeChunk) {
+        float2 ml[kMergeChunk];
+        float4 a4[kMergeChunk];
+#pragma unroll
+        for (int j = 0; j < kMergeChunk; ++j) {
+          ml[j] = make_float2(-CUDART_INF_F, 0.f);
+          a4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (sp0 + j < u.nsplit) {
+            const long long pb = (static_cast<long long>(u.first + sp0 + j) * Hkv + u.g) * R + row;
+            ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + pb * 2));
+            a4[j] = __ldcg(reinterpret_cast<const float4*>(p.part_acc + pb * D + d));
+          }
+        }
+        // a split with no visible key for this row holds (-inf, 0) and zeros, one
+        // with logits of NaN alone (-inf, NaN)
+        float mc = M;
+#pragma unroll
+        for (int j = 0; j < kMergeChunk; ++j) mc = fmaxf(mc, ml[j].x);
+        if (mc == -CUDART_INF_F) {
+#pragma unroll
+          for (int j = 0; j < kMergeChunk; ++j) den += ml[j].y;  // 0, or NaN
+          continue;
+        }
+        if (mc > M) {  // rescale the running sums to the new maximum
+          const float sc = ex2_approx(M - mc);  // 0 while nothing was visible
+          num.x *= sc; num.y *= sc; num.z *= sc; num.w *= sc; den *= sc;
+          M = mc;
+        }
+#pragma unroll
+        for (int j = 0; j < kMergeChunk; ++j) {
+          const float f = ex2_approx(ml[j].x - M);  // 0 for an empty split
+          num.x = fmaf(a4[j].x, f, num.x); num.y = fmaf(a4[j].y, f, num.y);
+          num.z = fmaf(a4[j].z, f, num.z); num.w = fmaf(a4[j].w, f, num.w);
+          den = fmaf(ml[j].y, f, den);
+        }
+      }
+      const long long tok = u.a + u.j0 + jj;
+      const float inv = p.out_scale / den;
+      *reinterpret_cast<uint2*>(out + (tok * Hq + u.g * G + hh) * D + d) =
+          make_uint2(pack_bf16(num.x * inv, num.y * inv), pack_bf16(num.z * inv, num.w * inv));
+    }
+  };
+
   int cur_st = 0;  // ring stage of the next pair to compute
   for (int k = 0;; ++k) {
     if (!wait_for(bar_unit + (k & 1) * 8, (k >> 1) & 1)) break;
     const UnitMeta& cur = meta(k);
     if (!cur.valid) break;
+    if (iss_unit < k - 1) {  // units before this one need no copies any more
+      iss_unit = k - 1;
+      iss_n = 0;
+    }
+    if (cur.valid == 2) {
+      merge_splits(cur);
+      // (an arrival for this unit must not count for the one before, see below)
+      if (k >= NB && !wait_for(bar_free + (k % NB) * 8, (k / NB - 1) & 1)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_full + (k % NB) * 8);
+      continue;
+    }
     while (in_flight < NS && issue_one(k + 1)) {
     }
     const int nblk = cur.b1 - cur.b0;
@@ -735,7 +774,8 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       issue_one(k + 1);
     }
     // the warp's state for this unit -> shared memory (real rows only), once the
-    // unit that used the buffer before has been read
+    // unit that used the buffer before has been read: by then every warp has
+    // arrived for that unit, so no phase completes without one of them
     if (k >= NB && !wait_for(bar_free + (k % NB) * 8, (k / NB - 1) & 1)) break;
     float* cb = comb + (k % NB) * NW * R * D;
     float* cm = comb_ml + (k % NB) * NW * R * 2;
