@@ -146,6 +146,8 @@ Capacity capacity(const pa_layout* L, int B, int T, int max_seq_len) {
   c.decode_items = static_cast<long long>(B) * splits + cdiv(kSmallStepUnits, L->num_kv_heads);
   c.small_tiles = (T > B ? cdiv(T - B, small_positions(L)) : 0) + multi;
   c.small_items = c.small_tiles * splits;
+  if (int4_cache(L) && c.small_tiles > 0)  // finer few-token splits, in the same way
+    c.small_items += cdiv(kSmallStepUnits, L->num_kv_heads);
   const long long group = L->num_q_heads / L->num_kv_heads;
   c.prefill_tiles = L->dtype == PA_BF16
                         ? cdiv(static_cast<long long>(T) * group, kPrefillRows) + multi : 0;
@@ -403,7 +405,9 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
   {
     AttnParams none{};
     e = launch_attn(none, layout, 1, keys_as_m, num_sms, st, &pp.num_ctas);
-    if (e != cudaSuccess) return fail_cuda(e, "decode grid size");
+    if (e == cudaSuccess && int4_cache(layout) && max_query_len > 1)
+      e = launch_attn(none, layout, small_positions(layout), false, num_sms, st, &pp.num_ctas_small);
+    if (e != cudaSuccess) return fail_cuda(e, "attention grid size");
   }
   pp.small_positions = small_positions(layout);
   pp.prefill_min_qlen = tc_prefill ? kPrefillMinQlen : 0x7fffffff;

@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
   __shared__ int size_hist[kMaxUnitBlocks + 1];  // short decode items per size (blocks)
   __shared__ unsigned long long s_blocks;        // KV blocks of the requests that split
   __shared__ unsigned long long s_blocks_d;      // ... of the decode requests among them
+  __shared__ unsigned long long s_blocks_s;      // KV blocks of the few-token tiles
+  __shared__ int s_tiles_s;                      // ... and their number
   __shared__ int2 s_short[kShortItems];          // short decode items: (item, blocks)
   __shared__ int s_nshort;
   static_assert(kMaxUnitBlocks == 8 * 32, "the dispatch-order scan gives each lane 8 sizes");
@@ -187,6 +189,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
     err = 0;
     s_blocks = 0;
     s_blocks_d = 0;
+    s_blocks_s = 0;
+    s_tiles_s = 0;
     s_nshort = 0;
     for (int i = 0; i < kLists; ++i) carry[i] = 0;
   }
@@ -209,6 +213,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
       if (L < p.prefill_min_qlen) {
         mine += static_cast<unsigned long long>(ceil_div(S, kBlockSize));
         if (L == 1) mine_d += static_cast<unsigned long long>(ceil_div(S, kBlockSize));
+        else if (p.num_ctas_small) {
+          const int tiles = ceil_div(L, p.small_positions);
+          atomicAdd(&s_blocks_s, static_cast<unsigned long long>(tiles) * ceil_div(S, kBlockSize));
+          atomicAdd(&s_tiles_s, tiles);
+        }
       }
     }
 #pragma unroll
@@ -242,6 +251,21 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
       bps_d = static_cast<int>(min(static_cast<long long>(p.bps),
                                    max(max(want, need), static_cast<long long>(PA_SPLIT_MIN))));
     }
+  }
+
+  // Few-token splits of a 4-bit cache: a quarter of a CTA's share of the tiles'
+  // blocks (their kernel takes ~4 times as long per byte, so a CTA left with a
+  // whole split more than the others shows: 48 requests of 2-8 tokens),
+  // within the same bounds.
+  int bps_s = bps;
+  if (p.num_ctas_small && s_tiles_s > 0) {
+    const long long total_s = static_cast<long long>(s_blocks_s) * p.num_kv_heads;
+    const long long want = (total_s + 4LL * p.num_ctas_small - 1) / (4LL * p.num_ctas_small);
+    const long long room = p.cap.small_items - s_tiles_s;
+    const long long need = room > 0 ? (static_cast<long long>(s_blocks_s) + room - 1) / room
+                                     : static_cast<long long>(p.bps);
+    bps_s = static_cast<int>(min(static_cast<long long>(bps),
+                                 max(max(want, need), static_cast<long long>(PA_SPLIT_MIN))));
   }
 
   // One pass: classify and count, exclusive-scan the counts across the CTA,
@@ -282,7 +306,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
       } else {
         c = kClassSmall;
         cnt[3] = ceil_div(L, p.small_positions);
-        const int rb = request_bps(ceil_div(S, kBlockSize), bps);
+        const int rb = request_bps(ceil_div(S, kBlockSize), bps_s);
         for (int m = 0; m < cnt[3]; ++m) {
           const int last = min(L, (m + 1) * p.small_positions) - 1;
           cnt[2] += splits_for(S - L + last, rb);
@@ -321,7 +345,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
       }
     } else if (c == kClassSmall) {
       // tiles of small_positions positions, each expanded into its splits
-      const int rb = request_bps(ceil_div(S, kBlockSize), bps);
+      const int rb = request_bps(ceil_div(S, kBlockSize), bps_s);
       const int P = p.small_positions;
       int first = off[2];
       for (int m = 0; m < cnt[3]; ++m) {
