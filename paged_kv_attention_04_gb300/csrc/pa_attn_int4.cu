@@ -138,29 +138,10 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
 __device__ __forceinline__ float2 half2_floats(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
 __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-// 16 + c as f16 of the nibbles of both halves of w that `mul` moves to bits 6-9;
-// sixteen = 16.0 in both halves, in a register (an instruction takes one
-// constant, so with two the masked OR would be two).
-__device__ __forceinline__ uint32_t code_plus_16(uint32_t w, uint32_t mul, uint32_t sixteen) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;\n" : "=r"(r) : "r"(w * mul), "r"(sixteen));
-  return r;
-}
-// A constant the compiler does not see through (it would turn a multiplication
-// by a power of two back into a shift).
-__device__ __forceinline__ uint32_t opaque(uint32_t x) {
-  asm volatile("mov.u32 %0, %0;\n" : "+r"(x));
-  return x;
 }
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;

@@ -50,4 +50,25 @@ struct I4Page {
   static_assert(kCodeBytes + kBlockSize * kRun == kBytes, "codes and parameters fill the page");
 };
 
+// A constant the compiler does not see through (it would turn a multiplication
+// by a power of two back into a shift).
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("mov.u32 %0, %0;\n" : "+r"(x));
+  return x;
+}
+// 16 + c as f16 of the nibbles of both halves of w that `mul` moves to bits 6-9
+// (a multiplication leaves the integer pipe to the masks); sixteen = 16.0 in both
+// halves, in a register (an instruction takes one constant, so with two the
+// masked OR would be two).
+__device__ __forceinline__ uint32_t code_plus_16(uint32_t w, uint32_t mul, uint32_t sixteen) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;\n" : "=r"(r) : "r"(w * mul), "r"(sixteen));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
 }  // namespace pa

@@ -62,7 +62,13 @@ constexpr int kTileN = 128;  // keys per KV tile
 constexpr int kKLoadWarp = 8;   // unit fetch, Q (TMA), K tiles
 constexpr int kMmaWarp = 9;
 constexpr int kVLoadWarp = 10;  // V tiles
-constexpr int kPfThreads = 352;
+constexpr int kWidenWarp = 12;  // 4-bit cache: the first of four warps that widen pages
+constexpr int kWidenWarps = 4;
+// Threads: roles 0-10, with a 4-bit cache 0-15 (11 has none).  Those sixteen warps
+// are launched with 128 registers a thread; the softmax warpgroups take 152 and
+// the other two keep 104: 256 x 152 + 256 x 104 = 512 x 128.
+constexpr int pf_threads(pa_dtype kv) { return kv == PA_INT4 ? 512 : 352; }
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kRescaleThreshold = 8.f;  // base-2 logit growth that forces a rescale
 
@@ -87,15 +93,16 @@ struct PfCfg {
   // ahead of its widening; V codes go into the upper half of each block's
   // region of the V buffer they are widened into (one warp widens a block in
   // place), so a V copy starts as soon as PV has read that buffer.
-  // A 4-bit cache: the same with pages of 10 D bytes, V pages at the end of
-  // each block's region.
+  // A 4-bit cache: pages of 10 D bytes, two staging buffers for K and two for V
+  // behind them, so both are copied two tiles ahead.
   static constexpr int kKCodeOff = kVOff + 2 * kTileBytes;
   static constexpr int code_block(pa_dtype kv) {  // bytes of a block's codes
     return kv == PA_INT4 ? I4Page<D>::kBytes : kBlockSize * D;
   }
   static constexpr int code_tile(pa_dtype kv) { return kTileN / kBlockSize * code_block(kv); }
   static constexpr int smem_bytes(pa_dtype kv) {
-    return kv == PA_BF16 ? kSmemBytes : kKCodeOff + 2 * code_tile(kv) + 1024;
+    return kv == PA_BF16 ? kSmemBytes
+                         : kKCodeOff + (kv == PA_INT4 ? 4 : 2) * code_tile(kv) + 1024;
   }
   // S0, S1 (consecutive tiles) at 0 / 128, each tile's P (bf16 pairs) over the
   // first 64 columns of its S once read; O at 256
@@ -132,7 +139,8 @@ enum Bar : int {
   kQLand = 24,      // FP8 cache: the bf16 Q tile landed (TMA), before its f16 conversion
   kKLand = 25,      // [2] FP8 cache: codes landed in K staging buffer 0 / 1 (TMA)
   kKStFree = 27,    // [2] FP8 cache: K staging buffer 0 / 1 widened by the 8 softmax warps
-  kNumBars = 29
+  kVStFree = 29,    // [2] 4-bit cache: V staging buffer 0 / 1 widened
+  kNumBars = 31
 };
 
 struct UnitInfo {
@@ -209,10 +217,17 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 }
 
 // Arrivals that complete a phase of each barrier.
-template <bool F8>
+template <pa_dtype KV>
 __device__ __forceinline__ uint32_t bar_count(int i) {
-  if (i == kUnitEmpty || i == kUnitEmpty + 1) return 10;  // 8 softmax warps, MMA, V loader
-  if (i == kGo || i == kGo + 1) return F8 ? 8 : 10;  // 8 softmax warps (+ V and K loaders)
+  constexpr bool kI4 = KV == PA_INT4;
+  constexpr uint32_t w = kWidenWarps;
+  if (i == kUnitEmpty || i == kUnitEmpty + 1)
+    return kI4 ? 10 + w : 10;  // 8 softmax warps, MMA, V loader (+ the widening warps)
+  // 8 softmax warps (+ the widening warps, or the bf16 cache's V and K loaders)
+  if (i == kGo || i == kGo + 1) return kI4 ? 8 + w : (KV == PA_BF16 ? 10 : 8);
+  if (kI4 && (i == kKFirst || i == kKFirst + 1 || i == kKStFree || i == kKStFree + 1 ||
+              i == kVStFree || i == kVStFree + 1))
+    return w;
   if (i == kMx || i == kMx + 1 || i == kMlFull || i == kMlRead || i == kOFree ||
       i == kPieceDone || i == kKStFree || i == kKStFree + 1)
     return 8;
@@ -317,26 +332,23 @@ __device__ __forceinline__ void widen_blocks(uint32_t src, uint32_t src_stride, 
     }
 }
 
-// Values of nibble J of both halves of w as f16: (code s + z) of either half.
-template <int J>
-__device__ __forceinline__ uint32_t int4_values(uint32_t w, uint32_t s, uint32_t z16) {
-  constexpr int sh = 6 - 4 * J;  // the nibble goes to bits 6-9 of 16.0
-  const uint32_t x = sh >= 0 ? w << (sh >= 0 ? sh : 0) : w >> (sh >= 0 ? 0 : -sh);
-  const uint32_t c = (x & 0x03c003c0u) | 0x4c004c00u;
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(c), "r"(s), "r"(z16));
-  return r;
-}
+// The constants of code_plus_16, in registers.
+struct I4Consts {
+  uint32_t mul64, mul4, sixteen;
+};
 // z - 16 s of an f16 pair
 __device__ __forceinline__ uint32_t int4_offset(uint32_t s, uint32_t z) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(s), "r"(0xcc00cc00u), "r"(z));
-  return r;
+  return fma_half2(s, 0xcc00cc00u, z);
 }
-__device__ __forceinline__ void st_shared_int4(uint32_t addr, uint32_t w, uint32_t s, uint32_t z16) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(int4_values<0>(w, s, z16)),
-               "r"(int4_values<1>(w, s, z16)), "r"(int4_values<2>(w, s, z16)),
-               "r"(int4_values<3>(w, s, z16))
+// The values of w's nibbles 0 .. 3 of both halves (scale s, z16 = z - 16 s) to addr.
+__device__ __forceinline__ void st_shared_int4(uint32_t addr, uint32_t w, uint32_t s, uint32_t z16,
+                                               const I4Consts& c) {
+  const uint32_t w8 = w >> 8;
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr),
+               "r"(fma_half2(code_plus_16(w, c.mul64, c.sixteen), s, z16)),
+               "r"(fma_half2(code_plus_16(w, c.mul4, c.sixteen), s, z16)),
+               "r"(fma_half2(code_plus_16(w8, c.mul64, c.sixteen), s, z16)),
+               "r"(fma_half2(code_plus_16(w8, c.mul4, c.sixteen), s, z16))
                : "memory");
 }
 template <int N>
@@ -355,7 +367,7 @@ __device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t (&w)[N])
 // and t ^ 5 share each quarter-warp: their loads (64 bytes a row) and their
 // stores (swizzled by row) then hit distinct banks.
 template <int D>
-__device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lane) {
+__device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lane, const I4Consts& k) {
   using C = PfCfg<D>;
   using Pg = I4Page<D>;
   constexpr int NG = Pg::kGroups;
@@ -376,15 +388,15 @@ __device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lan
       const uint32_t z16 = int4_offset(s, __byte_perm(q[h][NG / 2 + g / 2], 0, sel));
       const int ch = 4 * g + c;  // 16-byte chunk of the row
       st_shared_int4(dst + h * C::kKGroupBytes + (ch >> 3) * 1024 + t * 128 + (((ch & 7) ^ t) << 4),
-                     w[h][g], s, z16);
+                     w[h][g], s, z16, k);
     }
 }
 
-// 4-bit: one page of V at src (which may be the end of the block's own region)
-// to f16 at dst, in the V layout above; rows from `rows` on become zeros.  A lane
+// 4-bit: one page of V at src to f16 at dst, in the V layout above; rows from `rows` on become zeros.  A lane
 // takes one run of each token pair (2c, 2c + 1) + 8 h.
 template <int D>
-__device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int rows, int lane) {
+__device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int rows, int lane,
+                                             const I4Consts& k) {
   using Pg = I4Page<D>;
   constexpr int NG = Pg::kGroups;
   const int e = lane >> 2, c = lane & 3;
@@ -393,7 +405,6 @@ __device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int row
   for (int h = 0; h < 2; ++h)
     ld_shared_words<NG>(src + h * 4 * D + e * (D / 2) + c * Pg::kRun, w[h]);
   ld_shared_words<4>(src + Pg::kCodeBytes + (e * Pg::kRun / 32) * 64 + c * 16, q);
-  __syncwarp();  // every load, before any store
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int t = 2 * c + 8 * h;
@@ -408,7 +419,7 @@ __device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int row
         st_shared_int4(dst + (ch >> 3) * (kBlockSize * 128) + (t + b) * 128 +
                            (((ch & 7) ^ ((t + b) & 7)) << 4),
                        __byte_perm(w[h][2 * i], w[h][2 * i + 1], b ? 0x7632u : 0x5410u),
-                       __byte_perm(s2, 0, sel), __byte_perm(z2, 0, sel));
+                       __byte_perm(s2, 0, sel), __byte_perm(z2, 0, sel), k);
       }
   }
 }
@@ -424,13 +435,13 @@ __device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int row
 // in f16).  The K scale is folded into the softmax scale and the V scale
 // into the normalisation.
 template <int D, int G, pa_dtype KV>
-__global__ void __launch_bounds__(kPfThreads, 1)
+__global__ void __launch_bounds__(pf_threads(KV), 1)
     prefill_tc_kernel(const AttnParams p, const __grid_constant__ PfMaps maps) {
   using C = PfCfg<D>;
   constexpr int PM = kTileM / G;  // positions per unit
   constexpr bool CODES = KV != PA_BF16, I4 = KV == PA_INT4;
   constexpr int kCodeBlock = C::code_block(KV), kCodeTile = C::code_tile(KV);
-  constexpr int kVCodeOff = C::kVBlockBytes - kCodeBlock;  // V codes in their block's region
+  constexpr int kVCodeOff = C::kVBlockBytes / 2;  // FP8: V codes in their block's region
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ UnitInfo s_units[2];
@@ -449,7 +460,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), bar_count<CODES>(i));
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), bar_count<KV>(i));
     s_abort = 0;
     mbar_fence_init();
   }
@@ -480,13 +491,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       ph = -1;
     }
     if constexpr (I4) {
-      // the pages, K into the staging buffer at dst, V to the ends of the blocks'
-      // regions; a bad table entry leaves a page of zeros (its scales and zeros
+      // the pages into the staging buffer at dst; a bad table entry leaves a page of zeros (its scales and zeros
       // too), a block past the unit's keys what was there (K is masked, V rows
       // past the last key are zeroed as they are widened)
       const bool have = lane < kTileN / kBlockSize && ph >= 0;
       const bool bad = lane < kTileN / kBlockSize && lb_of(t) * kBlockSize < u.kv_end && !have;
-      const uint32_t d = dst + lane * (is_v ? C::kVBlockBytes : kCodeBlock) + (is_v ? kVCodeOff : 0);
+      const uint32_t d = dst + lane * kCodeBlock;
       if (bad) {
         flag_error(p.status, PA_DEV_BLOCK_RANGE);
         for (int i = 0; i < kCodeBlock / 16; ++i)
@@ -541,17 +551,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                    : "memory");
     }
   };
-  // Codes: widen a tile of K codes at src to f16 at dst (one warp)
+  // FP8: widen a tile of K codes at src to f16 at dst (one warp)
   auto widen_k_tile = [&](uint32_t src, uint32_t dst) {
-    if constexpr (I4) {
-#pragma unroll 2
-      for (int b = 0; b < kTileN / kBlockSize; ++b)
-        widen_k_int4<D>(src + b * kCodeBlock, dst + b * C::kVBlockBytes, lane);
-    } else {
 #pragma unroll 1
-      for (int b = 0; b < kTileN / kBlockSize; b += 2)
-        widen_blocks<D, 2>(src, kCodeBlock, dst, false, b, lane);
-    }
+    for (int b = 0; b < kTileN / kBlockSize; b += 2)
+      widen_blocks<D, 2>(src, kCodeBlock, dst, false, b, lane);
   };
   // Codes: the landed bf16 Q tile to f16, in place (FP8: an element keeps its
   // slot; 4-bit: the order of the widened K within every eight)
@@ -582,6 +586,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     fence_proxy_async_smem();
     __syncwarp();
   };
+
+  if constexpr (I4) {
+    if (warp < 8)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+  }
 
   if (warp == kKLoadWarp) {
     // ------------------------------------------------------------ units, Q, K
@@ -674,9 +685,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint32_t c0 = kc;
       auto copy_codes = [&](int sq) -> bool {
         const uint32_t b = kc & 1;
-        if ((b ? kp1 : kp0) &&
-            !wait_bar(bar(kKStFree + b), ((b ? ks1 : ks0) - 1) & 1, abort, p.status))
+        if constexpr (I4) {  // every tile is widened by the widening warps
+          if (kc >= 2 && !wait_bar(bar(kKStFree + b), ((kc >> 1) - 1) & 1, abort, p.status))
+            return false;
+        } else if ((b ? kp1 : kp0) &&
+                   !wait_bar(bar(kKStFree + b), ((b ? ks1 : ks0) - 1) & 1, abort, p.status)) {
           return false;
+        }
         copy_kv_tile(u, tile_of(u, sq), ph, false, sbase + C::kKCodeOff + b * kCodeTile,
                      bar(kKLand + b));
         const bool soft = sq >= 2;
@@ -715,7 +730,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (lane == 0) mbar_arrive(bar(kQFull));
         }
       }
-      if constexpr (CODES) {
+      if constexpr (I4) {
+        for (int sq = 2; ok && sq < u.n_kv; ++sq) ok = copy_codes(sq);
+      } else if constexpr (CODES) {
         // the first two tiles into K buffers 0 / 1 (freed by the previous
         // unit: its last S of each parity was waited below), then every
         // later tile's codes as their staging buffer frees up
@@ -757,7 +774,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (ok) ok = claim(uc + 1, nu);
       // the unit's last two S done (K buffers free for the next unit); bf16:
       // tiles with no K two places on make a plain kGo arrival then
-      for (int t = max(0, u.n_kv - 2); ok && t < u.n_kv; ++t) {
+      // (4-bit: the widening warps wait for them)
+      for (int t = max(0, u.n_kv - 2); !I4 && ok && t < u.n_kv; ++t) {
         const int w = t & 1;
         if (!wait_bar(bar(kSFull + w), sw[w] & 1, abort, p.status)) { ok = false; break; }
         ++sw[w];
@@ -791,6 +809,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint32_t nv[2] = {0, 0}, gv[2] = {0, 0}, nl[2] = {0, 0};
     bool landing = false;  // a kVLand copy not yet waited for
     int land_w = 0;
+    uint32_t vi = 0;  // 4-bit: page copies issued
     bool vland = false;  // FP8: a code copy into V buffer vland_w not yet drained
     int vland_w = 0;
     for (int uc = 0;; ++uc) {
@@ -801,7 +820,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (u.r < 0) break;
       int ph = tile_phys(u, tile_of(u, 0));
       bool ok = true;
-      if constexpr (CODES) {
+      if constexpr (I4) {
+        // copy i into staging buffer i & 1, once the one before has been widened
+        for (int sq = 0; sq < u.n_kv; ++sq) {
+          if (vi >= 2 && !wait_bar(bar(kVStFree + (vi & 1)), ((vi >> 1) - 1) & 1, abort, p.status)) {
+            ok = false;
+            break;
+          }
+          copy_kv_tile(u, tile_of(u, sq), ph, true, sbase + C::kKCodeOff + (2 + (vi & 1)) * kCodeTile,
+                       bar(kVLand + (vi & 1)));
+          ++vi;
+          if (sq + 1 < u.n_kv) ph = tile_phys(u, tile_of(u, sq + 1));
+        }
+      } else if constexpr (CODES) {
         // each tile's codes into V buffer w = sq & 1 once PV of the previous
         // tile of that parity is done; the softmax warps widen them there
         for (int sq = 0; sq < u.n_kv; ++sq) {
@@ -852,6 +883,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (!ok) break;
     }
     if (*abort) {
+      if constexpr (I4) {
+        for (uint32_t i = vi > 2 ? vi - 2 : 0; i < vi; ++i)
+          drain_wait(bar(kVLand + (i & 1)), (i >> 1) & 1);
+      }
       if (landing) drain_wait(bar(kVLand + land_w), nl[land_w] & 1);
       // FP8: the last code copy into each V buffer
       if (vland) {
@@ -860,6 +895,65 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       for (int w = 0; w < 2; ++w)
         if (gv[w] > 0) drain_wait(bar(kGo + w), (gv[w] - 1) & 1, kGoDrainLimit);
+    }
+    __syncwarp();
+  } else if (I4 && warp >= 11) {
+    // ------------------------------------------------------------ widening (4-bit)
+    // Four warps, two blocks of every tile each: K(0), K(1) of the unit, then V(t)
+    // and K(t + 2) for every tile t, behind the S that read the K buffer before.
+    // V(t) goes into its buffer behind PV(t - 2).
+    const int b0 = (warp - kWidenWarp) * 2;
+    const I4Consts kc4{opaque(64u), opaque(4u), opaque(0x4c004c00u)};
+    uint32_t kc = 0, vc = 0;            // K and V code tiles so far (staging buffer: & 1)
+    uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};  // tiles per K and V buffer so far
+    bool ok = warp >= kWidenWarp;
+    for (int uc = 0; ok; ++uc) {
+      const int slot = uc & 1;
+      if (!wait_bar(bar(kUnitFull + slot), (uc >> 1) & 1, abort, p.status)) break;
+      const UnitInfo u = s_units[slot];
+      warp_arrive(bar(kUnitEmpty + slot));
+      if (u.r < 0) break;
+      // (one copy of each page's code, not unrolled: the softmax warps on the same
+      // scheduler want the instruction cache too)
+#pragma unroll 1
+      for (int t = -2; ok && t < u.n_kv; ++t) {
+        const int w = t & 1;
+        if (t >= 0) {
+          const uint32_t n = w ? nv[1]++ : nv[0]++, vi = vc++;
+          if (!wait_bar(bar(kVLand + (vi & 1)), (vi >> 1) & 1, abort, p.status) ||
+              (n > 0 && !wait_bar(bar(kPVDone + w), (n - 1) & 1, abort, p.status))) {
+            ok = false;
+            break;
+          }
+          const uint32_t src = sbase + C::kKCodeOff + (2 + (vi & 1)) * kCodeTile;
+          const uint32_t vb = sbase + C::kVOff + w * C::kTileBytes;
+          const int rows = u.kv_end - tile_of(u, t) * kTileN;  // written rows of the tile
+#pragma unroll 1
+          for (int b = b0; b < b0 + 2; ++b)
+            widen_v_int4<D>(src + b * kCodeBlock, vb + b * C::kVBlockBytes, rows - b * kBlockSize, lane,
+                            kc4);
+          warp_arrive(bar(kVStFree + (vi & 1)));
+        }
+        if (t + 2 < u.n_kv) {
+          const uint32_t n = w ? nk[1]++ : nk[0]++, ci = kc++;
+          if (!wait_bar(bar(kKLand + (ci & 1)), (ci >> 1) & 1, abort, p.status) ||
+              (n > 0 && !wait_bar(bar(kSFull + w), (n - 1) & 1, abort, p.status))) {
+            ok = false;
+            break;
+          }
+          const uint32_t src = sbase + C::kKCodeOff + (ci & 1) * kCodeTile;
+          const uint32_t dst = sbase + C::kKOff + w * C::kTileBytes;
+#pragma unroll 1
+          for (int b = b0; b < b0 + 2; ++b)
+            widen_k_int4<D>(src + b * kCodeBlock, dst + b * C::kVBlockBytes, lane, kc4);
+          warp_arrive(bar(kKStFree + (ci & 1)));
+        }
+        fence_proxy_async_smem();  // generic-proxy writes, before the tensor cores read them
+        if (t >= 0)
+          warp_arrive(bar(kGo + w));
+        else if (t + 2 < u.n_kv)
+          warp_arrive(bar(kKFirst + w));
+      }
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -1112,7 +1206,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           PA_TMEM_ST32(tmem_s + w * 32, pw);
           l_part += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
         }
-        if constexpr (CODES) {
+        if constexpr (CODES && !I4) {
           // this warp's 16-token block of K(t + 2), from its staging buffer
           // into K buffer b (S(t), its last reader, is done), and of V(t), in
           // place in V buffer b (PV(t - 2), its last reader, finished before
@@ -1124,27 +1218,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               ok = false;
               break;
             }
-            const uint32_t kcodes = sbase + C::kKCodeOff + (ci & 1) * kCodeTile;
-            const uint32_t kb = sbase + C::kKOff + b * C::kTileBytes;
-            if constexpr (I4)
-              widen_k_int4<D>(kcodes + warp * kCodeBlock, kb + warp * C::kVBlockBytes, lane);
-            else
-              widen_blocks<D, 1>(kcodes, kCodeBlock, kb, false, warp, lane);
+            widen_blocks<D, 1>(sbase + C::kKCodeOff + (ci & 1) * kCodeTile, kCodeBlock,
+                               sbase + C::kKOff + b * C::kTileBytes, false, warp, lane);
             warp_arrive(bar(kKStFree + (ci & 1)));
           }
           {
             if (!wait_bar(bar(kVLand + b), nb & 1, abort, p.status)) { ok = false; break; }
             const uint32_t vb = sbase + C::kVOff + b * C::kTileBytes;
+            widen_blocks<D, 1>(vb + kVCodeOff, C::kVBlockBytes, vb, true, warp, lane);
             const int r0 = u.kv_end - kt * kTileN;
-            if constexpr (I4) {
-              const uint32_t blk = vb + warp * C::kVBlockBytes;
-              widen_v_int4<D>(blk + kVCodeOff, blk, r0 - warp * kBlockSize, lane);
-            } else {
-              widen_blocks<D, 1>(vb + kVCodeOff, C::kVBlockBytes, vb, true, warp, lane);
-              if (r0 < kTileN && (r0 >> 4) == warp) {
-                __syncwarp();
-                zero_v_rows(vb, r0, (r0 + kBlockSize - 1) & ~(kBlockSize - 1));
-              }
+            if (r0 < kTileN && (r0 >> 4) == warp) {
+              __syncwarp();
+              zero_v_rows(vb, r0, (r0 + kBlockSize - 1) & ~(kBlockSize - 1));
             }
           }
           fence_proxy_async_smem();  // generic-proxy writes, before the tensor cores read them
@@ -1359,7 +1444,7 @@ cudaError_t launch_pf(const AttnParams& p, int num_sms, cudaStream_t stream) {
                                 static_cast<cuuint32_t>(D / 64), 1, 1};
     if (!encode_map(&maps.v, p.v_cache, 5, vdims, vstrides, vbox)) return cudaErrorInvalidValue;
   }
-  prefill_tc_kernel<D, G, KV><<<num_sms, kPfThreads, kSmem, stream>>>(p, maps);
+  prefill_tc_kernel<D, G, KV><<<num_sms, pf_threads(KV), kSmem, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
