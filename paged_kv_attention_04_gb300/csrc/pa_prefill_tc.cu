@@ -62,13 +62,19 @@ constexpr int kTileN = 128;  // keys per KV tile
 constexpr int kKLoadWarp = 8;   // unit fetch, Q (TMA), K tiles
 constexpr int kMmaWarp = 9;
 constexpr int kVLoadWarp = 10;  // V tiles
-constexpr int kWidenWarp = 12;  // 4-bit cache: the first of four warps that widen pages
-constexpr int kWidenWarps = 4;
-// Threads: roles 0-10, with a 4-bit cache 0-15 (11 has none).  Those sixteen warps
-// are launched with 128 registers a thread; the softmax warpgroups take 152 and
-// the other two keep 104: 256 x 152 + 256 x 104 = 512 x 128.
-constexpr int pf_threads(pa_dtype kv) { return kv == PA_INT4 ? 512 : 352; }
-constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
+// 4-bit cache: warp 11 converts Q, warps 12-19 widen pages.  The 20 warps are
+// launched with 96 registers a thread; the softmax warpgroups take 152, warps 8-11
+// keep 80 and the widening warpgroups 48: 256 x 152 + 128 x 80 + 256 x 48 = 640 x 96.
+#ifndef PF_SR
+#define PF_SR 152
+#define PF_OR 80
+#define PF_WR 48
+#endif
+constexpr int kQWarp = 11;
+constexpr int kWidenWarp = 12;
+constexpr int kWidenWarps = 8;
+constexpr int pf_threads(pa_dtype kv) { return kv == PA_INT4 ? 640 : 352; }
+constexpr int kSoftmaxRegs = PF_SR, kCopyRegs = PF_OR, kWidenRegs = PF_WR;
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kRescaleThreshold = 8.f;  // base-2 logit growth that forces a rescale
 
@@ -222,7 +228,7 @@ __device__ __forceinline__ uint32_t bar_count(int i) {
   constexpr bool kI4 = KV == PA_INT4;
   constexpr uint32_t w = kWidenWarps;
   if (i == kUnitEmpty || i == kUnitEmpty + 1)
-    return kI4 ? 10 + w : 10;  // 8 softmax warps, MMA, V loader (+ the widening warps)
+    return kI4 ? 11 + w : 10;  // 8 softmax warps, MMA, V loader (+ Q and widening warps)
   // 8 softmax warps (+ the widening warps, or the bf16 cache's V and K loaders)
   if (i == kGo || i == kGo + 1) return kI4 ? 8 + w : (KV == PA_BF16 ? 10 : 8);
   if (kI4 && (i == kKFirst || i == kKFirst + 1 || i == kKStFree || i == kKStFree + 1 ||
@@ -358,14 +364,17 @@ __device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t (&w)[N])
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                  : "r"(addr)
                  : "memory");
-  else
+  else if constexpr (N == 2)
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  else
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(w[0]) : "r"(addr) : "memory");
 }
 
 // 4-bit: one page of K at src to f16 at dst, in the K layout above; one warp.
 // A lane takes one run (8 dims of every group) of tokens t and t + 8.  Rows t
 // and t ^ 5 share each quarter-warp: their loads (64 bytes a row) and their
-// stores (swizzled by row) then hit distinct banks.
+// stores (swizzled by row) then hit distinct banks.  The loop is not unrolled:
+// eight such warps hide each other's latency, and they have few registers.
 template <int D>
 __device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lane, const I4Consts& k) {
   using C = PfCfg<D>;
@@ -373,54 +382,53 @@ __device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lan
   constexpr int NG = Pg::kGroups;
   const int c = lane & 3;
   const int t = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
-  uint32_t w[2][NG], q[2][NG];
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
-    ld_shared_words<NG>(src + Pg::k_word(t + 8 * h, 0, c), w[h]);
-    ld_shared_words<NG>(src + Pg::k_scale(t + 8 * h, 0), q[h]);  // scales, then zeros
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
+    uint32_t w[NG], q[NG];
+    ld_shared_words<NG>(src + Pg::k_word(t, 0, c) + h * Pg::k_word(8, 0, 0), w);
+    ld_shared_words<NG>(src + Pg::k_scale(t, 0) + h * 8 * Pg::kRun, q);  // scales, then zeros
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const uint32_t sel = (g & 1) ? 0x3232u : 0x1010u;
-      const uint32_t s = __byte_perm(q[h][g / 2], 0, sel);
-      const uint32_t z16 = int4_offset(s, __byte_perm(q[h][NG / 2 + g / 2], 0, sel));
+      const uint32_t s = __byte_perm(q[g / 2], 0, sel);
+      const uint32_t z16 = __byte_perm(int4_offset(q[g / 2], q[NG / 2 + g / 2]), 0, sel);
       const int ch = 4 * g + c;  // 16-byte chunk of the row
       st_shared_int4(dst + h * C::kKGroupBytes + (ch >> 3) * 1024 + t * 128 + (((ch & 7) ^ t) << 4),
-                     w[h][g], s, z16, k);
+                     w[g], s, z16, k);
     }
+  }
 }
 
-// 4-bit: one page of V at src to f16 at dst, in the V layout above; rows from `rows` on become zeros.  A lane
-// takes one run of each token pair (2c, 2c + 1) + 8 h.
+// 4-bit: one page of V at src to f16 at dst, in the V layout above; rows from
+// `rows` on become zeros.  A lane takes one run of each token pair (2c, 2c + 1) + 8 h.
 template <int D>
 __device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int rows, int lane,
                                              const I4Consts& k) {
   using Pg = I4Page<D>;
   constexpr int NG = Pg::kGroups;
   const int e = lane >> 2, c = lane & 3;
-  uint32_t w[2][NG], q[4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    ld_shared_words<NG>(src + h * 4 * D + e * (D / 2) + c * Pg::kRun, w[h]);
-  ld_shared_words<4>(src + Pg::kCodeBytes + (e * Pg::kRun / 32) * 64 + c * 16, q);
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
+    uint32_t w[NG], s1[1], z1[1];
+    const uint32_t par = src + Pg::kCodeBytes + (e * Pg::kRun / 32) * 64 + c * 16 + h * 4;
+    ld_shared_words<NG>(src + h * 4 * D + e * (D / 2) + c * Pg::kRun, w);
+    ld_shared_words<1>(par, s1);
+    ld_shared_words<1>(par + 8, z1);
     const int t = 2 * c + 8 * h;
     const uint32_t keep = rows >= t + 2 ? 0xffffffffu : (rows == t + 1 ? 0x0000ffffu : 0u);
-    const uint32_t s2 = q[h] & keep, z2 = int4_offset(s2, q[2 + h] & keep);
+    const uint32_t s2 = s1[0] & keep, z2 = int4_offset(s2, z1[0] & keep);
 #pragma unroll
-    for (int i = 0; i < NG / 2; ++i)
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t sel = b ? 0x3232u : 0x1010u;
+      const uint32_t s = __byte_perm(s2, 0, sel), z16 = __byte_perm(z2, 0, sel);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int i = 0; i < NG / 2; ++i) {
         const int ch = e * (NG / 2) + i;
-        const uint32_t sel = b ? 0x3232u : 0x1010u;
         st_shared_int4(dst + (ch >> 3) * (kBlockSize * 128) + (t + b) * 128 +
                            (((ch & 7) ^ ((t + b) & 7)) << 4),
-                       __byte_perm(w[h][2 * i], w[h][2 * i + 1], b ? 0x7632u : 0x5410u),
-                       __byte_perm(s2, 0, sel), __byte_perm(z2, 0, sel), k);
+                       __byte_perm(w[2 * i], w[2 * i + 1], b ? 0x7632u : 0x5410u), s, z16, k);
       }
+    }
   }
 }
 
@@ -587,13 +595,64 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
     __syncwarp();
   };
 
-  if constexpr (I4) {
-    if (warp < 8)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-  }
-
+  if (I4 && warp >= kWidenWarp) {
+    if constexpr (I4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kWidenRegs));
+    // ------------------------------------------------------------ widening (4-bit)
+    // Eight warps, a block of every tile each: K(0), K(1) of the unit, then V(t)
+    // and K(t + 2) for every tile t, behind the S that read the K buffer before.
+    // V(t) goes into its buffer behind PV(t - 2).
+    const int b = warp - kWidenWarp;    // the block of every tile this warp widens
+    const I4Consts kc4{opaque(64u), opaque(4u), opaque(0x4c004c00u)};
+    uint32_t kc = 0, vc = 0;            // K and V code tiles so far (staging buffer: & 1)
+    uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};  // tiles per K and V buffer so far
+    bool ok = true;
+    for (int uc = 0; ok; ++uc) {
+      const int slot = uc & 1;
+      if (!wait_bar(bar(kUnitFull + slot), (uc >> 1) & 1, abort, p.status)) break;
+      const UnitInfo u = s_units[slot];
+      warp_arrive(bar(kUnitEmpty + slot));
+      if (u.r < 0) break;
+      // (one copy of each page's code, not unrolled: the softmax warps on the same
+      // scheduler want the instruction cache too)
+#pragma unroll 1
+      for (int t = -2; ok && t < u.n_kv; ++t) {
+        const int w = t & 1;
+        if (t >= 0) {
+          const uint32_t n = w ? nv[1]++ : nv[0]++, vi = vc++;
+          if (!wait_bar(bar(kVLand + (vi & 1)), (vi >> 1) & 1, abort, p.status) ||
+              (n > 0 && !wait_bar(bar(kPVDone + w), (n - 1) & 1, abort, p.status))) {
+            ok = false;
+            break;
+          }
+          const uint32_t src = sbase + C::kKCodeOff + (2 + (vi & 1)) * kCodeTile;
+          const uint32_t vb = sbase + C::kVOff + w * C::kTileBytes;
+          const int rows = u.kv_end - tile_of(u, t) * kTileN;  // written rows of the tile
+          widen_v_int4<D>(src + b * kCodeBlock, vb + b * C::kVBlockBytes, rows - b * kBlockSize, lane,
+                          kc4);
+          warp_arrive(bar(kVStFree + (vi & 1)));
+        }
+        if (t + 2 < u.n_kv) {
+          const uint32_t n = w ? nk[1]++ : nk[0]++, ci = kc++;
+          if (!wait_bar(bar(kKLand + (ci & 1)), (ci >> 1) & 1, abort, p.status) ||
+              (n > 0 && !wait_bar(bar(kSFull + w), (n - 1) & 1, abort, p.status))) {
+            ok = false;
+            break;
+          }
+          const uint32_t src = sbase + C::kKCodeOff + (ci & 1) * kCodeTile;
+          const uint32_t dst = sbase + C::kKOff + w * C::kTileBytes;
+          widen_k_int4<D>(src + b * kCodeBlock, dst + b * C::kVBlockBytes, lane, kc4);
+          warp_arrive(bar(kKStFree + (ci & 1)));
+        }
+        fence_proxy_async_smem();  // generic-proxy writes, before the tensor cores read them
+        if (t >= 0)
+          warp_arrive(bar(kGo + w));
+        else if (t + 2 < u.n_kv)
+          warp_arrive(bar(kKFirst + w));
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+  if constexpr (I4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kCopyRegs));
   if (warp == kKLoadWarp) {
     // ------------------------------------------------------------ units, Q, K
     // Work comes in chunks of pieces (PfItem), fetched from a counter: chunk
@@ -721,7 +780,7 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       }
       ++nq;
       q_wait = CODES;
-      if constexpr (CODES) {  // Q to f16 while the codes are on their way
+      if constexpr (CODES && !I4) {  // Q to f16 while the codes are on their way
         if (!wait_bar(bar(kQLand), (nq - 1) & 1, abort, p.status)) {
           ok = false;
         } else {
@@ -897,66 +956,19 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
         if (gv[w] > 0) drain_wait(bar(kGo + w), (gv[w] - 1) & 1, kGoDrainLimit);
     }
     __syncwarp();
-  } else if (I4 && warp >= 11) {
-    // ------------------------------------------------------------ widening (4-bit)
-    // Four warps, two blocks of every tile each: K(0), K(1) of the unit, then V(t)
-    // and K(t + 2) for every tile t, behind the S that read the K buffer before.
-    // V(t) goes into its buffer behind PV(t - 2).
-    const int b0 = (warp - kWidenWarp) * 2;
-    const I4Consts kc4{opaque(64u), opaque(4u), opaque(0x4c004c00u)};
-    uint32_t kc = 0, vc = 0;            // K and V code tiles so far (staging buffer: & 1)
-    uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};  // tiles per K and V buffer so far
-    bool ok = warp >= kWidenWarp;
-    for (int uc = 0; ok; ++uc) {
+  } else if (I4 && warp == kQWarp) {
+    // ------------------------------------------------------------ Q (4-bit)
+    for (int uc = 0;; ++uc) {
       const int slot = uc & 1;
       if (!wait_bar(bar(kUnitFull + slot), (uc >> 1) & 1, abort, p.status)) break;
-      const UnitInfo u = s_units[slot];
+      const bool end = s_units[slot].r < 0;
       warp_arrive(bar(kUnitEmpty + slot));
-      if (u.r < 0) break;
-      // (one copy of each page's code, not unrolled: the softmax warps on the same
-      // scheduler want the instruction cache too)
-#pragma unroll 1
-      for (int t = -2; ok && t < u.n_kv; ++t) {
-        const int w = t & 1;
-        if (t >= 0) {
-          const uint32_t n = w ? nv[1]++ : nv[0]++, vi = vc++;
-          if (!wait_bar(bar(kVLand + (vi & 1)), (vi >> 1) & 1, abort, p.status) ||
-              (n > 0 && !wait_bar(bar(kPVDone + w), (n - 1) & 1, abort, p.status))) {
-            ok = false;
-            break;
-          }
-          const uint32_t src = sbase + C::kKCodeOff + (2 + (vi & 1)) * kCodeTile;
-          const uint32_t vb = sbase + C::kVOff + w * C::kTileBytes;
-          const int rows = u.kv_end - tile_of(u, t) * kTileN;  // written rows of the tile
-#pragma unroll 1
-          for (int b = b0; b < b0 + 2; ++b)
-            widen_v_int4<D>(src + b * kCodeBlock, vb + b * C::kVBlockBytes, rows - b * kBlockSize, lane,
-                            kc4);
-          warp_arrive(bar(kVStFree + (vi & 1)));
-        }
-        if (t + 2 < u.n_kv) {
-          const uint32_t n = w ? nk[1]++ : nk[0]++, ci = kc++;
-          if (!wait_bar(bar(kKLand + (ci & 1)), (ci >> 1) & 1, abort, p.status) ||
-              (n > 0 && !wait_bar(bar(kSFull + w), (n - 1) & 1, abort, p.status))) {
-            ok = false;
-            break;
-          }
-          const uint32_t src = sbase + C::kKCodeOff + (ci & 1) * kCodeTile;
-          const uint32_t dst = sbase + C::kKOff + w * C::kTileBytes;
-#pragma unroll 1
-          for (int b = b0; b < b0 + 2; ++b)
-            widen_k_int4<D>(src + b * kCodeBlock, dst + b * C::kVBlockBytes, lane, kc4);
-          warp_arrive(bar(kKStFree + (ci & 1)));
-        }
-        fence_proxy_async_smem();  // generic-proxy writes, before the tensor cores read them
-        if (t >= 0)
-          warp_arrive(bar(kGo + w));
-        else if (t + 2 < u.n_kv)
-          warp_arrive(bar(kKFirst + w));
-      }
+      if (end || !wait_bar(bar(kQLand), uc & 1, abort, p.status)) break;
+      q_to_f16();
+      if (lane == 0) mbar_arrive(bar(kQFull));
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else {  // kMmaWarp
     // ------------------------------------------------------------ MMA issue
     // Kept lean: every cycle this warp spends between products is tensor-core
     // idle time (the issue queue is shallow).  Counters live in registers,
@@ -1051,7 +1063,9 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       drain_wait(bar(kDrain), 0);
     }
     __syncwarp();
+  }
   } else {
+    if constexpr (I4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------ softmax
     // Warpgroup w takes keys 64w .. 64w + 63 of every tile; thread i owns
     // query row i = TMEM lane i.  The two threads of a row trade their half
