@@ -88,9 +88,10 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _on_one_device(**tensors) -> None:
+def _on_one_device(**tensors) -> int:
     """Every tensor argument must be a contiguous CUDA tensor, all on one
-    device (a host pointer would reach the kernels unchecked)."""
+    device (a host pointer would reach the kernels unchecked).  Returns the
+    device's index."""
     dev = None
     for name, t in tensors.items():
         if t is None:
@@ -99,10 +100,12 @@ def _on_one_device(**tensors) -> None:
             raise PaError(PA_ERR_INVALID, f"{name} is not a CUDA tensor")
         if not t.is_contiguous():
             raise PaError(PA_ERR_INVALID, f"{name} is not contiguous")
+        d = t.get_device()
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise PaError(PA_ERR_INVALID, f"{name} is on {t.device}, expected {dev}")
+            dev = d
+        elif d != dev:
+            raise PaError(PA_ERR_INVALID, f"{name} is on cuda:{d}, expected cuda:{dev}")
+    return dev
 
 
 def _int4_pages(layout: pa_layout, *caches) -> None:
@@ -110,18 +113,36 @@ def _int4_pages(layout: pa_layout, *caches) -> None:
     rows' size that the other types share)."""
     if layout.cache_dtype != PA_INT4:
         return
-    shape = cache_shape(layout)
+    n = layout.num_blocks * layout.num_kv_heads * layout.head_size * 10
     for c in caches:
-        if c.dtype != torch.uint8 or tuple(c.shape) != shape:
-            raise PaError(PA_ERR_INVALID, f"a 4-bit cache is uint8 {shape}, got {c.dtype} {tuple(c.shape)}")
+        if c.dtype != torch.uint8 or c.numel() != n:
+            raise PaError(PA_ERR_INVALID, f"a 4-bit cache is uint8 {cache_shape(layout)}, got {c.dtype} "
+                                          f"{tuple(c.shape)}")
 
 
-def _stream(stream) -> int | None:
+# the current stream's handle without building a Stream object (about a microsecond a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, dev: int) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _launch(fn, dev: int, stream, *args) -> None:
+    """Call fn(*args, stream) with the tensors' device current: the library
+    launches on the current device."""
+    s = _stream(stream, dev)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != PA_OK:
+        raise PaError(rc, last_error())
 
 
 def make_layout(num_q_heads: int, num_kv_heads: int, head_size: int, num_blocks: int,
@@ -162,12 +183,11 @@ def layout_of(k_cache: torch.Tensor, num_q_heads: int, dtype=None, k_scale: floa
 def pa_cache_write(k, v, slot_mapping, k_cache, v_cache, layout: pa_layout,
                    status: torch.Tensor | None = None, stream=None) -> None:
     """Write k[t], v[t] into slot slot_mapping[t] of the caches (in place)."""
-    _on_one_device(k=k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache,
-                   status=status)
+    dev = _on_one_device(k=k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache,
+                         status=status)
     _int4_pages(layout, k_cache, v_cache)
-    _check(lib().pa_cache_write(_ptr(k), _ptr(v), _ptr(slot_mapping), int(k.shape[0]),
-                                _ptr(k_cache), _ptr(v_cache), ctypes.byref(layout),
-                                _ptr(status), _stream(stream)))
+    _launch(lib().pa_cache_write, dev, stream, _ptr(k), _ptr(v), _ptr(slot_mapping), k.shape[0],
+            _ptr(k_cache), _ptr(v_cache), ctypes.byref(layout), _ptr(status))
 
 
 def cache_shape(layout: pa_layout) -> tuple:
@@ -181,20 +201,19 @@ def pa_cache_read(k_cache, v_cache, slot_mapping, k, v, layout: pa_layout,
                   status: torch.Tensor | None = None, stream=None) -> None:
     """Read slot slot_mapping[t] of the caches into k[t], v[t] (in place); the
     values of a quantised cache come rounded to layout.dtype."""
-    _on_one_device(k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, k=k, v=v,
-                   status=status)
+    dev = _on_one_device(k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, k=k, v=v,
+                         status=status)
     _int4_pages(layout, k_cache, v_cache)
-    n = int(slot_mapping.shape[0])
-    row = layout.num_kv_heads * layout.head_size
+    n = slot_mapping.shape[0]
     if slot_mapping.dtype != torch.int64:
         raise PaError(PA_ERR_INVALID, f"slot_mapping is {slot_mapping.dtype}, expected torch.int64")
+    elems = n * layout.num_kv_heads * layout.head_size
     for name, t in (("k", k), ("v", v)):
-        if t.numel() != n * row or _DTYPES.get(t.dtype) != layout.dtype:
+        if t.numel() != elems or _DTYPES.get(t.dtype) != layout.dtype:
             raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, expected {n} rows of "
-                                          f"{row} elements of the layout's dtype")
-    _check(lib().pa_cache_read(_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-                               n, _ptr(k), _ptr(v), ctypes.byref(layout),
-                               _ptr(status), _stream(stream)))
+                                          f"{layout.num_kv_heads} x {layout.head_size} of the layout's dtype")
+    _launch(lib().pa_cache_read, dev, stream, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n,
+            _ptr(k), _ptr(v), ctypes.byref(layout), _ptr(status))
 
 
 def pa_forward_workspace_size(layout: pa_layout, num_seqs: int, num_tokens: int,
@@ -210,16 +229,15 @@ def pa_forward(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
                max_query_len: int, max_seq_len: int, scale: float, out, workspace,
                layout: pa_layout, status: torch.Tensor | None = None, stream=None) -> None:
     """Attention for every row of the flattened step, written into `out`."""
-    _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                   seq_lens=seq_lens, query_start_loc=query_start_loc, out=out,
-                   workspace=workspace, status=status)
+    dev = _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                         seq_lens=seq_lens, query_start_loc=query_start_loc, out=out,
+                         workspace=workspace, status=status)
     _int4_pages(layout, k_cache, v_cache)
-    _check(lib().pa_forward(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                            int(block_tables.shape[1]), _ptr(seq_lens), _ptr(query_start_loc),
-                            int(seq_lens.shape[0]), int(q.shape[0]), int(max_query_len),
-                            int(max_seq_len), float(scale), _ptr(out), _ptr(workspace),
-                            int(workspace.numel() * workspace.element_size()),
-                            ctypes.byref(layout), _ptr(status), _stream(stream)))
+    _launch(lib().pa_forward, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache),
+            _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), _ptr(query_start_loc),
+            seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), float(scale),
+            _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            ctypes.byref(layout), _ptr(status))
 
 
 def pa_forward_noalloc(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc,
@@ -227,14 +245,13 @@ def pa_forward_noalloc(q, k_cache, v_cache, block_tables, seq_lens, query_start_
                        layout: pa_layout, status: torch.Tensor | None = None, stream=None) -> None:
     """pa_forward using the library's built-in device scratch instead of a
     caller workspace (for callers that cannot allocate device memory)."""
-    _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                   seq_lens=seq_lens, query_start_loc=query_start_loc, out=out, status=status)
+    dev = _on_one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                         seq_lens=seq_lens, query_start_loc=query_start_loc, out=out, status=status)
     _int4_pages(layout, k_cache, v_cache)
-    _check(lib().pa_forward_noalloc(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                                    int(block_tables.shape[1]), _ptr(seq_lens),
-                                    _ptr(query_start_loc), int(seq_lens.shape[0]), int(q.shape[0]),
-                                    int(max_query_len), int(max_seq_len), float(scale), _ptr(out),
-                                    ctypes.byref(layout), _ptr(status), _stream(stream)))
+    _launch(lib().pa_forward_noalloc, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache),
+            _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), _ptr(query_start_loc),
+            seq_lens.shape[0], q.shape[0], int(max_query_len), int(max_seq_len), float(scale),
+            _ptr(out), ctypes.byref(layout), _ptr(status))
 
 
 def _event_handles(start, stop) -> list:

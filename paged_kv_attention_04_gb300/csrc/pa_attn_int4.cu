@@ -49,31 +49,6 @@
 #include "pa_int4.cuh"
 #include "pa_tcgen05.cuh"
 
-#ifndef PA_I4_NW
-#define PA_I4_NW 4
-#endif
-#ifndef PA_I4_CTAS
-#define PA_I4_CTAS 3
-#endif
-#ifndef PA_I4_SNS
-#define PA_I4_SNS 3
-#endif
-#ifndef PA_I4_SBP
-#define PA_I4_SBP 1
-#endif
-#ifndef PA_I4_NB
-#define PA_I4_NB 2
-#endif
-#ifndef PA_I4_PREFETCH
-#define PA_I4_PREFETCH 0
-#endif
-#ifndef PA_I4_NS
-#define PA_I4_NS 2
-#endif
-#ifndef PA_I4_NS64
-#define PA_I4_NS64 4
-#endif
-
 namespace pa {
 
 namespace {
@@ -96,9 +71,9 @@ struct I4Cfg {
   static constexpr int kQRowBytes = D * 2;
   static constexpr int kQBufBytes = (kR * (kQRowBytes + 32 + 4) + 15) / 16 * 16;
   static constexpr int kQOff = kRingBytes;
-  // the warps' states of finished units: two units' for decode tiles, one for
-  // 16 rows (64 KB a pair)
-  static constexpr int kNB = kNT == 1 ? PA_I4_NB : 1;
+  // the warps' states of finished units: two units' up to 4 rows, one unit's with
+  // more (16 KB at 8 rows; a third CTA would not fit beside two)
+  static constexpr int kNB = kR <= 4 ? 2 : 1;
   static constexpr int kCombOff = kQOff + 2 * kQBufBytes;
   static constexpr int kCombBytes = kNB * NW * kR * D * 4;
   static constexpr int kMlOff = kCombOff + kCombBytes;
@@ -108,7 +83,7 @@ struct I4Cfg {
   static constexpr int kNumBars = 2 + 2 * kNB;
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8;
   static constexpr int kFit = (228 * 1024) / (kSmemBytes + 1024 + 64);
-  static constexpr int kMinCtas = kFit < PA_I4_CTAS ? kFit : PA_I4_CTAS;
+  static constexpr int kMinCtas = kFit < 3 ? kFit : 3;
   static_assert(kR <= 16 && kGroups <= 4, "at most 16 query rows and 4 groups");
   static_assert(kStageBytes % 16 == 0 && kQBufBytes % 16 == 0, "16-byte stages");
   static_assert(kNumBars <= kThreads, "one thread initialises each barrier");
@@ -463,14 +438,6 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       for (int i = 0; i < C::kBlockBytes; i += 512)  // the K page, then the V page, 512 bytes a step
         if (i + 512 <= C::kBlockBytes || lane * 16 < C::kBlockBytes - i)
           cp_async16(st + b * C::kBlockBytes + i, (i + lane * 16 < Pg::kBytes ? ks : vs) + i, bytes);
-      if (PA_I4_PREFETCH && lane < (C::kBlockBytes + 127) / 128) {
-        // towards L2: the lines of the block that goes into this place next
-        const int next = iss_bl + b + BP * NW < iss_n ? bt[b + BP * NW] : -1;
-        if (next >= 0)
-          asm volatile("prefetch.global.L2 [%0];\n" ::"l"(
-              (lane * 128 < Pg::kBytes ? iss_k : iss_k + k_to_v) + lane * 112 +
-              static_cast<unsigned long long>(static_cast<uint32_t>(next)) * block_stride));
-      }
     }
     cp_async_commit();
     iss_st = iss_st + 1 == NS ? 0 : iss_st + 1;
@@ -556,16 +523,21 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     const int pos0 = cur.pos0, kv_hi = cur.kv_hi;
     const int plain_end = min(pos0 + 1, kv_hi) - BP * kBlockSize;  // no mask up to this first key
     // q^T fragments, the group sums' and the rows' factors
-    uint32_t qb[NT][NG][4], zb[NT][2];
+    // (q^T of one n-tile stays in registers; two are read again for every block,
+    // which leaves room for a third CTA on the SM)
+    constexpr bool kQRegs = NT == 1;
+    uint32_t qb[kQRegs ? NT : 1][NG][4], qrow[NT], zb[NT][2];
     float rm[NT][2];
     {
       const unsigned char* buf = smem + C::kQOff + (k & 1) * C::kQBufBytes;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = min(8 * n + g, R - 1);  // (columns past the last row repeat it)
-        const uint32_t row = smem_u32(buf) + r * C::kQRowBytes;
+        qrow[n] = smem_u32(buf) + r * C::kQRowBytes + c4 * 16;
+        if constexpr (kQRegs) {
 #pragma unroll
-        for (int e = 0; e < NG; ++e) lds_words<4>(row + (4 * e + c4) * 16, qb[n][e]);
+          for (int e = 0; e < NG; ++e) lds_words<4>(qrow[n] + e * 64, qb[n][e]);
+        }
         const uint32_t* zs = reinterpret_cast<const uint32_t*>(buf + R * C::kQRowBytes + r * 32);
         zb[n][0] = zs[c4];
         zb[n][1] = zs[4 + c4];
@@ -624,8 +596,15 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float acc[4];
-            mma_f16_zero(acc, a, qb[n][e][0], qb[n][e][1]);
-            mma_f16(acc, b, qb[n][e][2], qb[n][e][3]);
+            uint32_t qf[4];
+            if constexpr (kQRegs) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) qf[x] = qb[n][e][x];
+            } else {
+              lds_words<4>(qrow[n] + e * 64, qf);
+            }
+            mma_f16_zero(acc, a, qf[0], qf[1]);
+            mma_f16(acc, b, qf[2], qf[3]);
             s[j][n][0] = fmaf(acc[0], s0, s[j][n][0]);
             s[j][n][1] = fmaf(acc[1], s0, s[j][n][1]);
             s[j][n][2] = fmaf(acc[2], s1, s[j][n][2]);
@@ -826,12 +805,18 @@ cudaError_t launch_i4(const AttnParams& p, int num_sms, cudaStream_t stream, int
   return cudaLaunchKernelEx(&cfg, attn_int4_kernel<D, G, P, NW, NS, BP>, p);
 }
 
+// CTAs of four compute warps, three to an SM at 128 registers a thread; few-token
+// tiles at head size 128 need more registers: three compute warps of 168 (four of
+// 128 spill: 48 requests of 2-8 tokens 173 us instead of 130).  Two stages of two
+// blocks (head size 64: four) keep 120 KB of pages per SM in flight or in use;
+// three stages and two CTAs, or four CTAs of three warps, were slower (long
+// context: 375 and 347 us instead of 320).
 template <int D, int G>
 cudaError_t dispatch_positions_int4(const AttnParams& p, int positions, int num_sms,
                                     cudaStream_t stream, int* grid_only) {
-  constexpr int NS = D == 128 ? PA_I4_NS : PA_I4_NS64;
-  return positions == 1 ? launch_i4<D, G, 1, PA_I4_NW, NS, 2>(p, num_sms, stream, grid_only)
-                        : launch_i4<D, G, kSmallRows / G, 3, PA_I4_SNS, PA_I4_SBP>(p, num_sms, stream, grid_only);
+  return positions == 1
+             ? launch_i4<D, G, 1, 4, D == 128 ? 2 : 4, 2>(p, num_sms, stream, grid_only)
+             : launch_i4<D, G, kSmallRows / G, D == 128 ? 3 : 4, 3, 1>(p, num_sms, stream, grid_only);
 }
 
 template <int D>

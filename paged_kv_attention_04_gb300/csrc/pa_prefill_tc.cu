@@ -65,16 +65,11 @@ constexpr int kVLoadWarp = 10;  // V tiles
 // 4-bit cache: warp 11 converts Q, warps 12-19 widen pages.  The 20 warps are
 // launched with 96 registers a thread; the softmax warpgroups take 152, warps 8-11
 // keep 80 and the widening warpgroups 48: 256 x 152 + 128 x 80 + 256 x 48 = 640 x 96.
-#ifndef PF_SR
-#define PF_SR 152
-#define PF_OR 80
-#define PF_WR 48
-#endif
 constexpr int kQWarp = 11;
 constexpr int kWidenWarp = 12;
 constexpr int kWidenWarps = 8;
 constexpr int pf_threads(pa_dtype kv) { return kv == PA_INT4 ? 640 : 352; }
-constexpr int kSoftmaxRegs = PF_SR, kCopyRegs = PF_OR, kWidenRegs = PF_WR;
+constexpr int kSoftmaxRegs = 152, kCopyRegs = 80, kWidenRegs = 48;
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kRescaleThreshold = 8.f;  // base-2 logit growth that forces a rescale
 
