@@ -166,7 +166,9 @@ size_t pa_forward_workspace_size(const pa_layout* layout, int num_seqs, int num_
  *
  *   out[t][h] = sum_p softmax_p(scale * q[t][h] . K[p]) V[p]
  *
- * computed with fp32 accumulation and written in layout->dtype.
+ * computed with fp32 accumulation and written in layout->dtype.  (A key that a row
+ * may not see has weight 0 there; a NaN or infinity in such a key's V, where the
+ * query has another row that does see it, makes the row NaN all the same.)
  *
  *   block_tables     device int32 [num_seqs][max_blocks_per_seq]; entries past
  *                    ceil(S/block_size) are never read

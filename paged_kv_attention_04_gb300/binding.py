@@ -186,6 +186,8 @@ def pa_cache_write(k, v, slot_mapping, k_cache, v_cache, layout: pa_layout,
     dev = _on_one_device(k=k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache,
                          status=status)
     _int4_pages(layout, k_cache, v_cache)
+    if slot_mapping.numel() < k.shape[0]:
+        raise PaError(PA_ERR_INVALID, f"{slot_mapping.numel()} slots for {k.shape[0]} tokens")
     _launch(lib().pa_cache_write, dev, stream, _ptr(k), _ptr(v), _ptr(slot_mapping), k.shape[0],
             _ptr(k_cache), _ptr(v_cache), ctypes.byref(layout), _ptr(status))
 

@@ -129,7 +129,8 @@ int blocks_per_split(const pa_layout* L) {
   return b < 1 ? 1 : b;
 }
 
-int small_positions(const pa_layout* L) { return kSmallRows / (L->num_q_heads / L->num_kv_heads); }
+int small_rows(const pa_layout* L) { return int4_cache(L) ? kSmallRowsInt4 : kSmallRows; }
+int small_positions(const pa_layout* L) { return small_rows(L) / (L->num_q_heads / L->num_kv_heads); }
 
 Capacity capacity(const pa_layout* L, int B, int T, int max_seq_len) {
   Capacity c{};
@@ -218,12 +219,12 @@ int set_last_error(int code, const char* msg) {
   return code;
 }
 
-WsLayout ws_layout(const Capacity& cap, int Hkv, int D, int group) {
+WsLayout ws_layout(const Capacity& cap, int Hkv, int D, int group, int small_rows) {
   WsLayout w{};
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   const size_t rows_d = static_cast<size_t>(group);
-  const size_t rows_s = static_cast<size_t>(kSmallRows);
+  const size_t rows_s = static_cast<size_t>(small_rows);
   w.hdr = take(kHdrWords * sizeof(int));
   w.items_d = take(sizeof(int4) * cap.decode_items);
   w.tiles_d = take(sizeof(int4) * cap.decode_tiles);
@@ -256,7 +257,7 @@ extern "C" {
 
 const char* pa_last_error(void) { return g_last_error.c_str(); }
 
-int pa_version(void) { return 200; }
+int pa_version(void) { return 300; }
 
 int pa_set_profile_events(void* start, void* stop) {
   g_prof_start = static_cast<cudaEvent_t>(start);
@@ -337,7 +338,7 @@ size_t pa_forward_workspace_size(const pa_layout* layout, int num_seqs, int num_
   }
   const Capacity cap = capacity(layout, num_seqs, num_tokens, max_seq_len);
   return ws_layout(cap, layout->num_kv_heads, layout->head_size,
-                   layout->num_q_heads / layout->num_kv_heads)
+                   layout->num_q_heads / layout->num_kv_heads, small_rows(layout))
       .total;
 }
 
@@ -374,7 +375,8 @@ int pa_forward(const void* q, const void* k_cache, const void* v_cache,
   const Capacity cap = capacity(layout, num_seqs, num_tokens, max_seq_len);
   if (cap.decode_items > (1LL << 30) || cap.small_items > (1LL << 30))
     return fail(PA_ERR_INVALID, "step too large for one call");
-  const WsLayout lay = ws_layout(cap, layout->num_kv_heads, layout->head_size, group);
+  const WsLayout lay =
+      ws_layout(cap, layout->num_kv_heads, layout->head_size, group, small_rows(layout));
   if (workspace_bytes < lay.total)
     return fail(PA_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, lay.total);
   int num_sms = 0;

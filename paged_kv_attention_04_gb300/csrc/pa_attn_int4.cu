@@ -25,10 +25,13 @@
 //      a token's 32 dims, and one more MMA sums p d; v itself is rounded to f16.
 //
 // The tile: S^T = K Q^T and O^T += V^T P^T with the 16 keys of a block, then 16
-// head dims, as the MMA's M, and the query rows as N: 8 (decode: the G heads
-// that share a kv head) or 16 (few tokens: 16 / G positions x G heads).
+// head dims, as the MMA's M, and up to 8 query rows as N: the G heads that share a
+// kv head (decode) or 8 / G positions of them (few tokens).  Tiles of 16 rows in
+// two n-tiles unpack the codes half as often, but their registers leave 9 compute
+// warps an SM instead of 12: 48 requests of 2-8 tokens after 256-4096, 32/8 heads,
+// took VERIFY16 us instead of VERIFY8.
 // Lane (g, c) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 and rows 2c,
-// 2c + 1 of each n-tile, and O^T at dims (D/8) g + 2 mt, + 1 of m-tile mt: its
+// 2c + 1 and O^T at dims (D/8) g + 2 mt, + 1 of m-tile mt: its
 // V codes are one run of the page, all of one group.
 //
 // The softmax keeps a running maximum per row that moves only when a logit
@@ -56,16 +59,15 @@ namespace {
 constexpr unsigned long long kI4WaitNs = 2000000000ull;  // a wait gives up after two seconds
 constexpr float kI4Rescale = 8.f;  // base-2 logit growth that moves the running maximum
 
-template <int D, int G, int P, int NW, int NS, int BP>
+template <int D, int G, int P, int NW, int NS>
 struct I4Cfg {
   using Pg = I4Page<D>;
   static constexpr int kR = P * G;               // real query rows
-  static constexpr int kNT = (kR + 7) / 8;       // n-tiles of 8 query rows
   static constexpr int kGroups = D / 32;
   static constexpr int kMT = D / 16;             // m-tiles of O^T
   static constexpr int kThreads = (NW + 1) * 32;
   static constexpr int kBlockBytes = 2 * Pg::kBytes;  // K and V page of a block
-  static constexpr int kStageBytes = BP * kBlockBytes;
+  static constexpr int kStageBytes = 2 * kBlockBytes;
   static constexpr int kRingBytes = NW * NS * kStageBytes;
   // q buffer: rows of D f16, then per row 16 f16 (group sums) and a float factor
   static constexpr int kQRowBytes = D * 2;
@@ -84,7 +86,7 @@ struct I4Cfg {
   static constexpr int kSmemBytes = kBarOff + kNumBars * 8;
   static constexpr int kFit = (228 * 1024) / (kSmemBytes + 1024 + 64);
   static constexpr int kMinCtas = kFit < 3 ? kFit : 3;
-  static_assert(kR <= 16 && kGroups <= 4, "at most 16 query rows and 4 groups");
+  static_assert(kR <= 8 && kGroups <= 4, "at most 8 query rows and 4 groups");
   static_assert(kStageBytes % 16 == 0 && kQBufBytes % 16 == 0, "16-byte stages");
   static_assert(kNumBars <= kThreads, "one thread initialises each barrier");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
@@ -137,12 +139,12 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 
 }  // namespace
 
-template <int D, int G, int P, int NW, int NS, int BP>
-__global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D, G, P, NW, NS, BP>::kMinCtas)
+template <int D, int G, int P, int NW, int NS>
+__global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, P, NW, NS>::kMinCtas)
     attn_int4_kernel(const AttnParams p) {
-  using C = I4Cfg<D, G, P, NW, NS, BP>;
+  using C = I4Cfg<D, G, P, NW, NS>;
   using Pg = typename C::Pg;
-  constexpr int R = C::kR, NT = C::kNT, NG = C::kGroups, MT = C::kMT, NB = C::kNB;
+  constexpr int R = C::kR, NG = C::kGroups, MT = C::kMT, NB = C::kNB;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_abort;
 
@@ -186,7 +188,8 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
 
   if (warp == NW) {
     // ---------------------------------------------------------- scheduler warp
-    // (not through the read-only path, whose loads may be moved above the wait)
+    // (what the plan wrote is not read through the read-only path, whose loads may
+    // be moved above the wait)
     const int n_units = __ldcg(p.n_items) * Hkv;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
@@ -194,9 +197,9 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     // the block table.
     auto fetch_unit = [&](UnitMeta& m, int u) {
       const int k = u / Hkv;
-      const int item = p.order ? __ldg(p.order + k) : k;
+      const int item = p.order ? __ldcg(p.order + k) : k;
       const UnitRec* rec = p.recs + item;
-      const int4 ra = __ldg(&rec->a), rb = __ldg(&rec->b), rc = __ldg(&rec->c);
+      const int4 ra = __ldcg(&rec->a), rb = __ldcg(&rec->b), rc = __ldcg(&rec->c);
       const int32_t* row = p.block_tables + static_cast<long long>(ra.x) * p.max_blocks_per_seq;
       // a bad entry, and the one after an odd count, become -1: a block of zeros
       const int n = ra.w - ra.z;
@@ -423,13 +426,13 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
       iss_unit = k;
       iss_end = m.valid == 0;
       iss_n = m.valid ? m.b1 - m.b0 : 0;
-      iss_bl = BP * warp;
+      iss_bl = 2 * warp;
       iss_k = static_cast<const unsigned char*>(p.k_cache) + m.g * Pg::kBytes + lane * 16;
     }
     const uint32_t st = ring + iss_st * C::kStageBytes + lane * 16;
     const int32_t* bt = meta(iss_unit).bt + iss_bl;
 #pragma unroll
-    for (int b = 0; b < BP; ++b) {
+    for (int b = 0; b < 2; ++b) {
       const int phys = bt[b];
       const int bytes = phys >= 0 ? 16 : 0;
       const unsigned char* ks = iss_k + static_cast<unsigned long long>(static_cast<uint32_t>(max(phys, 0))) * block_stride;
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     }
     cp_async_commit();
     iss_st = iss_st + 1 == NS ? 0 : iss_st + 1;
-    iss_bl += BP * NW;
+    iss_bl += 2 * NW;
     ++in_flight;
     return true;
   };
@@ -521,52 +524,40 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     }
     const int nblk = cur.b1 - cur.b0;
     const int pos0 = cur.pos0, kv_hi = cur.kv_hi;
-    const int plain_end = min(pos0 + 1, kv_hi) - BP * kBlockSize;  // no mask up to this first key
+    const int plain_end = min(pos0 + 1, kv_hi) - 2 * kBlockSize;  // no mask up to this first key
     // q^T fragments, the group sums' and the rows' factors
-    // (q^T of one n-tile stays in registers; two are read again for every block,
-    // which leaves room for a third CTA on the SM)
-    constexpr bool kQRegs = NT == 1;
-    uint32_t qb[kQRegs ? NT : 1][NG][4], qrow[NT], zb[NT][2];
-    float rm[NT][2];
+    uint32_t qb[NG][4], zb[2];
+    float rm[2];
     {
       const unsigned char* buf = smem + C::kQOff + (k & 1) * C::kQBufBytes;
+      const int r = min(g, R - 1);  // (columns past the last row repeat it)
+      const uint32_t row = smem_u32(buf) + r * C::kQRowBytes + c4 * 16;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int r = min(8 * n + g, R - 1);  // (columns past the last row repeat it)
-        qrow[n] = smem_u32(buf) + r * C::kQRowBytes + c4 * 16;
-        if constexpr (kQRegs) {
-#pragma unroll
-          for (int e = 0; e < NG; ++e) lds_words<4>(qrow[n] + e * 64, qb[n][e]);
-        }
-        const uint32_t* zs = reinterpret_cast<const uint32_t*>(buf + R * C::kQRowBytes + r * 32);
-        zb[n][0] = zs[c4];
-        zb[n][1] = zs[4 + c4];
-        const float* fr = reinterpret_cast<const float*>(buf + R * (C::kQRowBytes + 32));
-        rm[n][0] = fr[min(8 * n + 2 * c4, R - 1)];
-        rm[n][1] = fr[min(8 * n + 2 * c4 + 1, R - 1)];
-      }
+      for (int e = 0; e < NG; ++e) lds_words<4>(row + e * 64, qb[e]);
+      const uint32_t* zs = reinterpret_cast<const uint32_t*>(buf + R * C::kQRowBytes + r * 32);
+      zb[0] = zs[c4];
+      zb[1] = zs[4 + c4];
+      const float* fr = reinterpret_cast<const float*>(buf + R * (C::kQRowBytes + 32));
+      rm[0] = fr[min(2 * c4, R - 1)];
+      rm[1] = fr[min(2 * c4 + 1, R - 1)];
     }
-    // running state per row: maximum (before the row factor), the value that
-    // moves it, minus the maximum's logit, sum; O^T and the sum of p d
-    float o[NT][MT][4], od[NT][4];
-    float m[NT][2], thr[NT][2], mneg[NT][2], l[NT][2];
+    // running state of rows 2 c4, 2 c4 + 1: maximum (before the row factor), the
+    // value that moves it, minus the maximum's logit, sum; O^T and the sum of p d
+    float o[MT][4], od[4] = {0.f, 0.f, 0.f, 0.f};
+    float m[2], thr[2], mneg[2], l[2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
-      od[n][0] = od[n][1] = od[n][2] = od[n][3] = 0.f;
-      m[n][0] = m[n][1] = thr[n][0] = thr[n][1] = -CUDART_INF_F;
-      mneg[n][0] = mneg[n][1] = l[n][0] = l[n][1] = 0.f;
-    }
-    for (int bl = BP * warp; bl < nblk; bl += BP * NW) {
+    for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    m[0] = m[1] = thr[0] = thr[1] = -CUDART_INF_F;
+    mneg[0] = mneg[1] = l[0] = l[1] = 0.f;
+    for (int bl = 2 * warp; bl < nblk; bl += 2 * NW) {
       if (in_flight == NS) cp_async_wait<NS - 1>(); else cp_async_wait<0>();
       __syncwarp();
       const uint32_t stage = ring + cur_st * C::kStageBytes;
       const int tok0 = (cur.b0 + bl) * kBlockSize;
       // S^T of keys g, g + 8 of both blocks
-      float s[BP][NT][4];
+      float s[2][4];
 #pragma unroll
-      for (int j = 0; j < BP; ++j) {
+      for (int j = 0; j < 2; ++j) {
         const uint32_t kp = stage + j * C::kBlockBytes;
         uint32_t kw[2][NG], sw[2][NG / 2], zw[2][1];  // codes, scales, the lane's pair of zeros
 #pragma unroll
@@ -577,46 +568,30 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
           lds_words<1>(kp + Pg::k_scale(g + 8 * h, 0) + 2 * NG + (NG == 4 ? (c4 & 1) * 4 : 0), zw[h]);
         }
         const uint32_t za[4] = {zw[0][0], zw[1][0], zw[0][0], zw[1][0]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16_zero(s[j][n], za, zb[n][0], zb[n][1]);
+        mma_f16_zero(s[j], za, zb[0], zb[1]);
 #pragma unroll
         for (int e = 0; e < NG; ++e) {
-          uint32_t a[4], b[4];
           const uint32_t k0 = kw[0][e] >> 8, k1 = kw[1][e] >> 8;
-          a[0] = kw[0][e] & 0x000f000fu;
-          a[1] = kw[1][e] & 0x000f000fu;
-          a[2] = k0 & 0x000f000fu;
-          a[3] = k1 & 0x000f000fu;
-          b[0] = kw[0][e] & 0x00f000f0u;
-          b[1] = kw[1][e] & 0x00f000f0u;
-          b[2] = k0 & 0x00f000f0u;
-          b[3] = k1 & 0x00f000f0u;
+          const uint32_t a[4] = {kw[0][e] & 0x000f000fu, kw[1][e] & 0x000f000fu, k0 & 0x000f000fu,
+                                 k1 & 0x000f000fu};
+          const uint32_t b[4] = {kw[0][e] & 0x00f000f0u, kw[1][e] & 0x00f000f0u, k0 & 0x00f000f0u,
+                                 k1 & 0x00f000f0u};
           const float2 f0 = half2_floats(sw[0][e / 2]), f1 = half2_floats(sw[1][e / 2]);
           const float s0 = (e & 1) ? f0.y : f0.x, s1 = (e & 1) ? f1.y : f1.x;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float acc[4];
-            uint32_t qf[4];
-            if constexpr (kQRegs) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) qf[x] = qb[n][e][x];
-            } else {
-              lds_words<4>(qrow[n] + e * 64, qf);
-            }
-            mma_f16_zero(acc, a, qf[0], qf[1]);
-            mma_f16(acc, b, qf[2], qf[3]);
-            s[j][n][0] = fmaf(acc[0], s0, s[j][n][0]);
-            s[j][n][1] = fmaf(acc[1], s0, s[j][n][1]);
-            s[j][n][2] = fmaf(acc[2], s1, s[j][n][2]);
-            s[j][n][3] = fmaf(acc[3], s1, s[j][n][3]);
-          }
+          float acc[4];
+          mma_f16_zero(acc, a, qb[e][0], qb[e][1]);
+          mma_f16(acc, b, qb[e][2], qb[e][3]);
+          s[j][0] = fmaf(acc[0], s0, s[j][0]);
+          s[j][1] = fmaf(acc[1], s0, s[j][1]);
+          s[j][2] = fmaf(acc[2], s1, s[j][2]);
+          s[j][3] = fmaf(acc[3], s1, s[j][3]);
         }
       }
       // V parameters: scales and zeros of tokens (2 c4, 2 c4 + 1) and
       // (2 c4 + 8, 2 c4 + 9), all in the group of the lane's run of dims
-      uint32_t vq[BP][4];
+      uint32_t vq[2][4];
 #pragma unroll
-      for (int j = 0; j < BP; ++j)
+      for (int j = 0; j < 2; ++j)
         lds_words<4>(stage + j * C::kBlockBytes + Pg::kBytes + Pg::kCodeBytes + (g * Pg::kRun / 32) * 64 +
                          c4 * 16,
                      vq[j]);
@@ -624,16 +599,14 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
         // causal edge, unwritten slots or no second block (K, V and parameters
         // there may be anything)
 #pragma unroll
-        for (int j = 0; j < BP; ++j) {
+        for (int j = 0; j < 2; ++j) {
           const int tj = tok0 + j * kBlockSize;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = tj + g + 8 * (e >> 1);
-              const int jj = (8 * n + 2 * c4 + (e & 1)) / G;
-              if (tok >= kv_hi || tok > pos0 + jj) s[j][n][e] = -CUDART_INF_F;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int tok = tj + g + 8 * (e >> 1);
+            const int jj = (2 * c4 + (e & 1)) / G;
+            if (tok >= kv_hi || tok > pos0 + jj) s[j][e] = -CUDART_INF_F;
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int left = kv_hi - (tj + 2 * c4 + 8 * h);  // written tokens of the pair
@@ -644,58 +617,45 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
         }
       }
       // online softmax
-      auto step_max = [&](int n, int e) {
-        float mx = fmaxf(s[0][n][e], s[0][n][2 + e]);
-#pragma unroll
-        for (int j = 1; j < BP; ++j) mx = fmaxf(mx, fmaxf(s[j][n][e], s[j][n][2 + e]));
-        return mx;
+      auto step_max = [&](int e) {
+        return fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e]));
       };
-      bool grew = false;
+      if (__any_sync(0xffffffffu, step_max(0) > thr[0] || step_max(1) > thr[1])) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(m[e], step_max(e));
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          grew |= step_max(n, e) > thr[n][e];
-      if (__any_sync(0xffffffffu, grew)) {
+          for (int o8 = 4; o8 < 32; o8 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o8));
+          if (mx > m[e]) {
+            const float corr = ex2_approx((m[e] - mx) * rm[e]);  // 0 before the first visible key
+            m[e] = mx;
+            thr[e] = mx + kI4Rescale / rm[e];
+            mneg[e] = -mx * rm[e];
+            l[e] *= corr;
+            od[e] *= corr;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(m[n][e], step_max(n, e));
-#pragma unroll
-            for (int o8 = 4; o8 < 32; o8 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o8));
-            if (mx > m[n][e]) {
-              const float corr = ex2_approx((m[n][e] - mx) * rm[n][e]);  // 0 before the first visible key
-              m[n][e] = mx;
-              thr[n][e] = mx + kI4Rescale / rm[n][e];
-              mneg[n][e] = -mx * rm[n][e];
-              l[n][e] *= corr;
-              od[n][e] *= corr;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                o[n][mt][e] *= corr;
-                o[n][mt][2 + e] *= corr;
-              }
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][e] *= corr;
+              o[mt][2 + e] *= corr;
             }
           }
-      }
-      uint32_t pb[BP][NT][2];
-#pragma unroll
-      for (int j = 0; j < BP; ++j)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float pr[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(fmaf(s[j][n][e], rm[n][e & 1], mneg[n][e & 1]));
-          l[n][0] += pr[0] + pr[2];
-          l[n][1] += pr[1] + pr[3];
-          // P^T as the B operand: an 8 x 8 transpose per half of the block's keys
-          pb[j][n][0] = movm_trans(pack_f16(pr[0], pr[1]));
-          pb[j][n][1] = movm_trans(pack_f16(pr[2], pr[3]));
         }
+      }
+      uint32_t pb[2][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(fmaf(s[j][e], rm[e & 1], mneg[e & 1]));
+        l[0] += pr[0] + pr[2];
+        l[1] += pr[1] + pr[3];
+        // P^T as the B operand: an 8 x 8 transpose per half of the block's keys
+        pb[j][0] = movm_trans(pack_f16(pr[0], pr[1]));
+        pb[j][1] = movm_trans(pack_f16(pr[2], pr[3]));
+      }
       // O^T += V^T P^T
 #pragma unroll
-      for (int j = 0; j < BP; ++j) {
+      for (int j = 0; j < 2; ++j) {
         const uint32_t vp = stage + j * C::kBlockBytes + Pg::kBytes;
         uint32_t vw[2][NG];
 #pragma unroll
@@ -706,8 +666,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
           // d of both token pairs in rows 0-7: row g's are of the lane's own group
           const uint32_t da[4] = {sub_half2(vq[j][2], fma_half2(s0, 0x4c004c00u, z0)), 0u,
                                   sub_half2(vq[j][3], fma_half2(s1, 0x4c004c00u, z1)), 0u};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(od[n], da, pb[j][n][0], pb[j][n][1]);
+          mma_f16(od, da, pb[j][0], pb[j][1]);
         }
 #pragma unroll
         for (int w = 0; w < NG; ++w) {
@@ -721,11 +680,8 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
           b[1] = fma_half2(code_plus_16(w0, mul4, sixteen), s0, z0);
           b[2] = fma_half2(code_plus_16(w1, mul64, sixteen), s1, z1);
           b[3] = fma_half2(code_plus_16(w1, mul4, sixteen), s1, z1);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma_f16(o[n][2 * w], a, pb[j][n][0], pb[j][n][1]);
-            mma_f16(o[n][2 * w + 1], b, pb[j][n][0], pb[j][n][1]);
-          }
+          mma_f16(o[2 * w], a, pb[j][0], pb[j][1]);
+          mma_f16(o[2 * w + 1], b, pb[j][0], pb[j][1]);
         }
       }
       __syncwarp();  // the stage has been read: the stream's next pair goes into it
@@ -740,24 +696,22 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS, BP>::kThreads, I4Cfg<D,
     float* cb = comb + (k % NB) * NW * R * D;
     float* cm = comb_ml + (k % NB) * NW * R * 2;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[n][e];
+      for (int o8 = 4; o8 < 32; o8 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o8);
+      const int row = 2 * c4 + e;
+      if (row < R) {
 #pragma unroll
-        for (int o8 = 4; o8 < 32; o8 <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o8);
-        const int row = 8 * n + 2 * c4 + e;
-        if (row < R) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            *reinterpret_cast<float2*>(cb + (warp * R + row) * D + (D / 8) * g + 2 * mt) =
-                make_float2(o[n][mt][e] + od[n][e], o[n][mt][2 + e] + od[n][e]);
-          if (g == 0) {
-            cm[(warp * R + row) * 2] = m[n][e] * rm[n][e];
-            cm[(warp * R + row) * 2 + 1] = sum;
-          }
+        for (int mt = 0; mt < MT; ++mt)
+          *reinterpret_cast<float2*>(cb + (warp * R + row) * D + (D / 8) * g + 2 * mt) =
+              make_float2(o[mt][e] + od[e], o[mt][2 + e] + od[e]);
+        if (g == 0) {
+          cm[(warp * R + row) * 2] = m[e] * rm[e];
+          cm[(warp * R + row) * 2 + 1] = sum;
         }
       }
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_full + (k % NB) * 8);
   }
@@ -768,20 +722,20 @@ namespace {
 
 // Launches the kernel, or with grid_only set only stores the grid size it
 // would use (CTAs per SM by occupancy x SMs).
-template <int D, int G, int P, int NW, int NS, int BP>
+template <int D, int G, int P, int NW, int NS>
 cudaError_t launch_i4(const AttnParams& p, int num_sms, cudaStream_t stream, int* grid_only) {
-  using C = I4Cfg<D, G, P, NW, NS, BP>;
+  using C = I4Cfg<D, G, P, NW, NS>;
   static int ctas_per_sm[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (ctas_per_sm[dev] == 0) {
-    e = cudaFuncSetAttribute(attn_int4_kernel<D, G, P, NW, NS, BP>,
+    e = cudaFuncSetAttribute(attn_int4_kernel<D, G, P, NW, NS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_int4_kernel<D, G, P, NW, NS, BP>, C::kThreads,
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_int4_kernel<D, G, P, NW, NS>, C::kThreads,
                                                       C::kSmemBytes);
     if (e != cudaSuccess) return e;
     ctas_per_sm[dev] = n > 0 ? n : 1;
@@ -802,21 +756,19 @@ cudaError_t launch_i4(const AttnParams& p, int num_sms, cudaStream_t stream, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.after_plan ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attn_int4_kernel<D, G, P, NW, NS, BP>, p);
+  return cudaLaunchKernelEx(&cfg, attn_int4_kernel<D, G, P, NW, NS>, p);
 }
 
-// CTAs of four compute warps, three to an SM at 128 registers a thread; few-token
-// tiles at head size 128 need more registers: three compute warps of 168 (four of
-// 128 spill: 48 requests of 2-8 tokens 173 us instead of 130).  Two stages of two
-// blocks (head size 64: four) keep 120 KB of pages per SM in flight or in use;
-// three stages and two CTAs, or four CTAs of three warps, were slower (long
+// CTAs of four compute warps, three to an SM at 128 registers a thread.  Two stages
+// of two blocks (head size 64: four) keep 120 KB of pages per SM in flight or in
+// use; three stages and two CTAs, or four CTAs of three warps, were slower (long
 // context: 375 and 347 us instead of 320).
 template <int D, int G>
 cudaError_t dispatch_positions_int4(const AttnParams& p, int positions, int num_sms,
                                     cudaStream_t stream, int* grid_only) {
   return positions == 1
-             ? launch_i4<D, G, 1, 4, D == 128 ? 2 : 4, 2>(p, num_sms, stream, grid_only)
-             : launch_i4<D, G, kSmallRows / G, D == 128 ? 3 : 4, 3, 1>(p, num_sms, stream, grid_only);
+             ? launch_i4<D, G, 1, 4, D == 128 ? 2 : 4>(p, num_sms, stream, grid_only)
+             : launch_i4<D, G, kSmallRowsInt4 / G, 4, D == 128 ? 2 : 4>(p, num_sms, stream, grid_only);
 }
 
 template <int D>

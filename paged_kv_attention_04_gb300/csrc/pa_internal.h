@@ -10,6 +10,7 @@ namespace pa {
 
 constexpr int kBlockSize = 16;        // tokens per KV block
 constexpr int kSmallRows = 16;        // query rows (positions x grouped heads) per few-token tile
+constexpr int kSmallRowsInt4 = 8;     // ... over a 4-bit cache
 constexpr int kMaxSplits = 64;        // KV splits per tile are kept at or below this ...
 constexpr int kMaxUnitBlocks = 256;   // ... unless a split would exceed this many blocks
 constexpr int kPrefillRows = 128;     // query rows per tensor-core prefill tile
@@ -144,7 +145,7 @@ struct AttnParams {
 int set_last_error(int code, const char* msg);
 
 // Workspace regions for a step with capacity cap (see pa_forward_workspace_size).
-WsLayout ws_layout(const Capacity& cap, int num_kv_heads, int head_size, int group);
+WsLayout ws_layout(const Capacity& cap, int num_kv_heads, int head_size, int group, int small_rows);
 
 // Kernel launchers (return cudaError_t of the launch).
 cudaError_t launch_cache_write(const void* k, const void* v, const int64_t* slot_mapping,

@@ -388,3 +388,68 @@ def test_captured_step_replays_with_new_inputs():
             torch.cuda.synchronize()
             for a, b in zip(got, (out, k, v)):
                 assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1e-30])
+def test_softmax_scale_zero_negative_tiny(scale):
+    """The sign of the scale is folded into the staged q; a scale of zero weighs all visible
+    keys alike."""
+    cpu, st, kc0, vc0, lay = make(spec([1, 1, 5, 3, 20], [33, 700, 300, 40, 130], seed=100))
+    kc0 = int4.store(kc0, wide(cpu.k), cpu.slot_mapping, 1.0, False)
+    vc0 = int4.store(vc0, wide(cpu.v), cpu.slot_mapping, 1.0, True)
+    cpu.scale = st.scale = scale
+    out, flags = forward(st, torch.from_numpy(kc0).cuda(), torch.from_numpy(vc0).cuda(), lay)
+    assert flags == 0
+    close(out, reference(cpu, kc0, vc0))
+
+
+@pytest.mark.parametrize("D,G,Hkv,q,s", [
+    (64, 8, 1, [1, 1], [40000, 9]),         # 20 and more splits of one tile, merged by a CTA
+    (128, 1, 3, [1, 4, 17], [9000, 5000, 4000]),
+    (64, 2, 5, [1, 15, 33], [300, 4100, 2100]),
+])
+def test_long_and_odd_heads(D, G, Hkv, q, s):
+    run(spec(q, s, G=G, Hkv=Hkv, D=D, seed=110 + D + Hkv))
+
+
+def test_two_steps_on_two_streams():
+    """Two steps with their own workspaces, one on each of two streams at once, give the bits
+    that they give alone."""
+    steps = []
+    for seed in (120, 121):
+        cpu, st, kc0, vc0, lay = make(spec([1] * 20 + [3, 7], [900] * 20 + [800, 500], seed=seed))
+        kc, vc = torch.from_numpy(kc0).cuda(), torch.from_numpy(vc0).cuda()
+        P.pa_cache_write(st.k, st.v, st.slot_mapping, kc, vc, lay)
+        alone, _ = forward(st, kc, vc, lay)
+        ws = P.alloc_workspace(lay, st.spec.num_seqs, st.spec.num_tokens, st.max_seq_len)
+        steps.append((st, kc, vc, lay, ws, torch.empty_like(alone), alone, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, kc, vc, lay, ws, out, alone, stream in steps:
+            P.pa_forward(st.q, kc, vc, st.block_tables, st.seq_lens, st.query_start_loc, st.max_query_len,
+                         st.max_seq_len, st.scale, out, ws, lay, stream=stream)
+    torch.cuda.synchronize()
+    for st, kc, vc, lay, ws, out, alone, stream in steps:
+        assert torch.equal(out.view(torch.int16), alone.view(torch.int16))
+
+
+def test_binding_refuses_what_would_run_out_of_bounds():
+    kc = torch.zeros(4, 2, 640, dtype=torch.uint8, device="cuda")
+    lay = P.layout_of(kc, 8)
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    with pytest.raises(P.PaError, match="rows"):
+        P.pa_cache_read(kc, kc, slots, k[:2].contiguous(), k, lay)
+    with pytest.raises(P.PaError, match="rows"):
+        P.pa_cache_read(kc, kc, slots, k, k.float(), lay)
+    with pytest.raises(P.PaError, match="slot_mapping"):
+        P.pa_cache_read(kc, kc, slots.int(), k, k.clone(), lay)
+    with pytest.raises(P.PaError, match="slots for"):
+        P.pa_cache_write(k, k, slots[:2].contiguous(), kc, kc.clone(), lay)
+    for wrong in (kc[:3].contiguous(), torch.zeros(4, 16, 2, 64, dtype=torch.uint8, device="cuda"), kc.to(torch.int32)):
+        for call in (lambda: P.pa_cache_write(k, k, slots, wrong, kc, lay),
+                     lambda: P.pa_cache_read(kc, wrong, slots, k, k.clone(), lay)):
+            with pytest.raises(P.PaError, match="4-bit cache"):
+                call()
+    with pytest.raises(P.PaError, match="not contiguous"):
+        P.pa_cache_read(kc, kc, slots, k.transpose(1, 2), k, lay)
