@@ -18,18 +18,15 @@
 //      applied to the float32 sums; the zeros term is one more MMA, z against
 //      the group sums of q 2^-20 split into f16 parts (to 2^-24, 2^-14 of the
 //      row's largest q).
-//   V  v = fma(16 + c, s, z') in f16 with z' = f16(z - 16 s), where 16 + c is the code
-//      placed in the top mantissa bits of 16.0: a shift (as a multiplication, on
-//      the other pipe), a masked OR and an FMA per two values.  What z' is off by,
-//      d = z - (16 s + z') <= 2^-12 of 1.6 times the group's range, is the same for
-//      a token's 32 dims, and one more MMA sums p d; v itself is rounded to f16.
+//   V  v = c s + z in f16, rounded once: a masked OR, an exact subtraction and an FMA
+//      per two values (pa_int4.cuh).
 //
 // The tile: S^T = K Q^T and O^T += V^T P^T with the 16 keys of a block, then 16
 // head dims, as the MMA's M, and up to 8 query rows as N: the G heads that share a
 // kv head (decode) or 8 / G positions of them (few tokens).  Tiles of 16 rows in
 // two n-tiles unpack the codes half as often, but their registers leave 9 compute
 // warps an SM instead of 12: 48 requests of 2-8 tokens after 256-4096, 32/8 heads,
-// took VERIFY16 us instead of VERIFY8.
+// took 130 us instead of 112 (kernel and plan).
 // Lane (g, c) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 and rows 2c,
 // 2c + 1 and O^T at dims (D/8) g + 2 mt, + 1 of m-tile mt: its
 // V codes are one run of the page, all of one group.
@@ -114,11 +111,6 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -404,7 +396,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
   // ------------------------------------------------------------ compute warps
   const int g = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * (NS * C::kStageBytes);
-  const uint32_t mul64 = opaque(64u), mul4 = opaque(4u), sixteen = opaque(0x4c004c00u);
+  const I4Magic magic;
 
   // ---- the stream of block pairs: this warp's share of unit k, then of unit k+1
   int iss_unit = -1;                // unit being issued
@@ -542,8 +534,8 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
       rm[1] = fr[min(2 * c4 + 1, R - 1)];
     }
     // running state of rows 2 c4, 2 c4 + 1: maximum (before the row factor), the
-    // value that moves it, minus the maximum's logit, sum; O^T and the sum of p d
-    float o[MT][4], od[4] = {0.f, 0.f, 0.f, 0.f};
+    // value that moves it, minus the maximum's logit, sum; O^T
+    float o[MT][4];
     float m[2], thr[2], mneg[2], l[2];
 #pragma unroll
     for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -632,7 +624,6 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
             thr[e] = mx + kI4Rescale / rm[e];
             mneg[e] = -mx * rm[e];
             l[e] *= corr;
-            od[e] *= corr;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               o[mt][e] *= corr;
@@ -660,26 +651,14 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
         uint32_t vw[2][NG];
 #pragma unroll
         for (int h = 0; h < 2; ++h) lds_words<NG>(vp + h * 4 * D + g * (D / 2) + c4 * Pg::kRun, vw[h]);
-        const uint32_t s0 = vq[j][0], s1 = vq[j][1];
-        const uint32_t z0 = fma_half2(s0, 0xcc00cc00u, vq[j][2]), z1 = fma_half2(s1, 0xcc00cc00u, vq[j][3]);
-        {
-          // d of both token pairs in rows 0-7: row g's are of the lane's own group
-          const uint32_t da[4] = {sub_half2(vq[j][2], fma_half2(s0, 0x4c004c00u, z0)), 0u,
-                                  sub_half2(vq[j][3], fma_half2(s1, 0x4c004c00u, z1)), 0u};
-          mma_f16(od, da, pb[j][0], pb[j][1]);
-        }
+        const uint32_t s0 = vq[j][0], s1 = vq[j][1], z0 = vq[j][2], z1 = vq[j][3];
 #pragma unroll
         for (int w = 0; w < NG; ++w) {
           const uint32_t w0 = vw[0][w] >> 8, w1 = vw[1][w] >> 8;
-          uint32_t a[4], b[4];
-          a[0] = fma_half2(code_plus_16(vw[0][w], mul64, sixteen), s0, z0);
-          a[1] = fma_half2(code_plus_16(vw[0][w], mul4, sixteen), s0, z0);
-          a[2] = fma_half2(code_plus_16(vw[1][w], mul64, sixteen), s1, z1);
-          a[3] = fma_half2(code_plus_16(vw[1][w], mul4, sixteen), s1, z1);
-          b[0] = fma_half2(code_plus_16(w0, mul64, sixteen), s0, z0);
-          b[1] = fma_half2(code_plus_16(w0, mul4, sixteen), s0, z0);
-          b[2] = fma_half2(code_plus_16(w1, mul64, sixteen), s1, z1);
-          b[3] = fma_half2(code_plus_16(w1, mul4, sixteen), s1, z1);
+          const uint32_t a[4] = {int4_values<0>(vw[0][w], s0, z0, magic), int4_values<1>(vw[0][w], s0, z0, magic),
+                                 int4_values<0>(vw[1][w], s1, z1, magic), int4_values<1>(vw[1][w], s1, z1, magic)};
+          const uint32_t b[4] = {int4_values<0>(w0, s0, z0, magic), int4_values<1>(w0, s0, z0, magic),
+                                 int4_values<0>(w1, s1, z1, magic), int4_values<1>(w1, s1, z1, magic)};
           mma_f16(o[2 * w], a, pb[j][0], pb[j][1]);
           mma_f16(o[2 * w + 1], b, pb[j][0], pb[j][1]);
         }
@@ -705,7 +684,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
           *reinterpret_cast<float2*>(cb + (warp * R + row) * D + (D / 8) * g + 2 * mt) =
-              make_float2(o[mt][e] + od[e], o[mt][2 + e] + od[e]);
+              make_float2(o[mt][e], o[mt][2 + e]);
         if (g == 0) {
           cm[(warp * R + row) * 2] = m[e] * rm[e];
           cm[(warp * R + row) * 2 + 1] = sum;

@@ -4,8 +4,8 @@
 // saturated at +-PA_INT4_LIMIT; z = f16(min y), s = f16((max y - min y) / 15);
 // code = (y - z) / s rounded and clamped to 0 .. 15.  All of it in float32
 // with IEEE division, so the codes are those of the definition.  The limit
-// keeps z - 16 s, which the attention kernels form in f16, and c s + z finite:
-// |z| + 16 s <= 16384 (1 + 32 / 15) < 65504.
+// keeps c s + z, which the attention kernels form in f16, finite whatever the
+// rounding of s and z: |z| + 15 s <= 3 x 16384 (1 + 2^-10) < 65504.
 //
 // Both kernels move 2 D + 10 D / 16 bytes per token, head and tensor and are bound
 // by HBM if a value costs few instructions:

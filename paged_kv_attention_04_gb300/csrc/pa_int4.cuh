@@ -50,24 +50,31 @@ struct I4Page {
   static_assert(kCodeBytes + kBlockSize * kRun == kBytes, "codes and parameters fill the page");
 };
 
-// A constant the compiler does not see through (it would turn a multiplication
-// by a power of two back into a shift).
+// A constant the compiler keeps in a register (an instruction takes one constant,
+// so a masked OR of two would become two instructions).
 __device__ __forceinline__ uint32_t opaque(uint32_t x) {
   asm volatile("mov.u32 %0, %0;\n" : "+r"(x));
   return x;
 }
-// 16 + c as f16 of the nibbles of both halves of w that `mul` moves to bits 6-9
-// (a multiplication leaves the integer pipe to the masks); sixteen = 16.0 in both
-// halves, in a register (an instruction takes one constant, so with two the
-// masked OR would be two).
-__device__ __forceinline__ uint32_t code_plus_16(uint32_t w, uint32_t mul, uint32_t sixteen) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;\n" : "=r"(r) : "r"(w * mul), "r"(sixteen));
-  return r;
-}
-__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+struct I4Magic {
+  uint32_t k1024, k64;  // 1024.0 and 64.0 in both halves
+  __device__ __forceinline__ I4Magic() : k1024(opaque(0x64006400u)), k64(opaque(0x54005400u)) {}
+};
+// Two values c s + z in f16 from the nibbles 0 (ODD = 0) or 1 of both halves of w,
+// rounded once.  The code in the low mantissa bits of 1024.0 (or from bit 4 on in
+// those of 64.0) makes 1024 + c (64 + c), and the subtraction is exact: a masked
+// OR, a subtraction and an FMA, without a shift.
+template <int ODD>
+__device__ __forceinline__ uint32_t int4_values(uint32_t w, uint32_t s, uint32_t z, const I4Magic& m) {
+  uint32_t x, r;
+  if constexpr (ODD) {
+    asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;\n" : "=r"(x) : "r"(w), "r"(m.k64));
+    asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(x) : "r"(x), "r"(0x54005400u));
+  } else {
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;\n" : "=r"(x) : "r"(w), "r"(m.k1024));
+    asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(x) : "r"(x), "r"(0x64006400u));
+  }
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(x), "r"(s), "r"(z));
   return r;
 }
 

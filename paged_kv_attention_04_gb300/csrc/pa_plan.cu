@@ -254,9 +254,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanParams p) {
   }
 
   // Few-token splits of a 4-bit cache: a quarter of a CTA's share of the tiles'
-  // blocks (their kernel takes ~4 times as long per byte, so a CTA left with a
-  // whole split more than the others shows: 48 requests of 2-8 tokens),
-  // within the same bounds.
+  // blocks, within the same bounds (a CTA has few of the longer splits that the
+  // other caches' kernels take, and one more than its neighbours shows).
   int bps_s = bps;
   if (p.num_ctas_small && s_tiles_s > 0) {
     const long long total_s = static_cast<long long>(s_blocks_s) * p.num_kv_heads;

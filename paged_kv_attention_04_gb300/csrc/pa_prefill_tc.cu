@@ -35,8 +35,7 @@
 // 16-token block per warp, while they work on the tile before; the products
 // run as kind::f16.
 // A 4-bit cache (pa_int4.cuh) goes the same way: a block's page is one bulk copy,
-// and widening turns codes into values, v = fma(16 + c, s, z - 16 s) in f16 (16 + c:
-// the code in the top mantissa bits of 16.0).  Its head dims come out of the words
+// and widening turns codes into values c s + z in f16.  Its head dims come out of the words
 // as 0, 4, 1, 5, 2, 6, 3, 7 of every eight; Q takes that order too, and the output's
 // columns are put back as they are written.
 // Hand-offs are mbarriers; every wait is bounded and a timeout makes the whole
@@ -333,23 +332,13 @@ __device__ __forceinline__ void widen_blocks(uint32_t src, uint32_t src_stride, 
     }
 }
 
-// The constants of code_plus_16, in registers.
-struct I4Consts {
-  uint32_t mul64, mul4, sixteen;
-};
-// z - 16 s of an f16 pair
-__device__ __forceinline__ uint32_t int4_offset(uint32_t s, uint32_t z) {
-  return fma_half2(s, 0xcc00cc00u, z);
-}
-// The values of w's nibbles 0 .. 3 of both halves (scale s, z16 = z - 16 s) to addr.
-__device__ __forceinline__ void st_shared_int4(uint32_t addr, uint32_t w, uint32_t s, uint32_t z16,
-                                               const I4Consts& c) {
+// The values of w's nibbles 0 .. 3 of both halves (scale s, zero z) to addr.
+__device__ __forceinline__ void st_shared_int4(uint32_t addr, uint32_t w, uint32_t s, uint32_t z,
+                                               const I4Magic& m) {
   const uint32_t w8 = w >> 8;
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr),
-               "r"(fma_half2(code_plus_16(w, c.mul64, c.sixteen), s, z16)),
-               "r"(fma_half2(code_plus_16(w, c.mul4, c.sixteen), s, z16)),
-               "r"(fma_half2(code_plus_16(w8, c.mul64, c.sixteen), s, z16)),
-               "r"(fma_half2(code_plus_16(w8, c.mul4, c.sixteen), s, z16))
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(int4_values<0>(w, s, z, m)),
+               "r"(int4_values<1>(w, s, z, m)), "r"(int4_values<0>(w8, s, z, m)),
+               "r"(int4_values<1>(w8, s, z, m))
                : "memory");
 }
 template <int N>
@@ -371,7 +360,7 @@ __device__ __forceinline__ void ld_shared_words(uint32_t addr, uint32_t (&w)[N])
 // stores (swizzled by row) then hit distinct banks.  The loop is not unrolled:
 // eight such warps hide each other's latency, and they have few registers.
 template <int D>
-__device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lane, const I4Consts& k) {
+__device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lane, const I4Magic& k) {
   using C = PfCfg<D>;
   using Pg = I4Page<D>;
   constexpr int NG = Pg::kGroups;
@@ -386,10 +375,10 @@ __device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lan
     for (int g = 0; g < NG; ++g) {
       const uint32_t sel = (g & 1) ? 0x3232u : 0x1010u;
       const uint32_t s = __byte_perm(q[g / 2], 0, sel);
-      const uint32_t z16 = __byte_perm(int4_offset(q[g / 2], q[NG / 2 + g / 2]), 0, sel);
+      const uint32_t z = __byte_perm(q[NG / 2 + g / 2], 0, sel);
       const int ch = 4 * g + c;  // 16-byte chunk of the row
       st_shared_int4(dst + h * C::kKGroupBytes + (ch >> 3) * 1024 + t * 128 + (((ch & 7) ^ t) << 4),
-                     w[g], s, z16, k);
+                     w[g], s, z, k);
     }
   }
 }
@@ -398,7 +387,7 @@ __device__ __forceinline__ void widen_k_int4(uint32_t src, uint32_t dst, int lan
 // `rows` on become zeros.  A lane takes one run of each token pair (2c, 2c + 1) + 8 h.
 template <int D>
 __device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int rows, int lane,
-                                             const I4Consts& k) {
+                                             const I4Magic& k) {
   using Pg = I4Page<D>;
   constexpr int NG = Pg::kGroups;
   const int e = lane >> 2, c = lane & 3;
@@ -411,17 +400,17 @@ __device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int row
     ld_shared_words<1>(par + 8, z1);
     const int t = 2 * c + 8 * h;
     const uint32_t keep = rows >= t + 2 ? 0xffffffffu : (rows == t + 1 ? 0x0000ffffu : 0u);
-    const uint32_t s2 = s1[0] & keep, z2 = int4_offset(s2, z1[0] & keep);
+    const uint32_t s2 = s1[0] & keep, z2 = z1[0] & keep;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const uint32_t sel = b ? 0x3232u : 0x1010u;
-      const uint32_t s = __byte_perm(s2, 0, sel), z16 = __byte_perm(z2, 0, sel);
+      const uint32_t s = __byte_perm(s2, 0, sel), z = __byte_perm(z2, 0, sel);
 #pragma unroll
       for (int i = 0; i < NG / 2; ++i) {
         const int ch = e * (NG / 2) + i;
         st_shared_int4(dst + (ch >> 3) * (kBlockSize * 128) + (t + b) * 128 +
                            (((ch & 7) ^ ((t + b) & 7)) << 4),
-                       __byte_perm(w[2 * i], w[2 * i + 1], b ? 0x7632u : 0x5410u), s, z16, k);
+                       __byte_perm(w[2 * i], w[2 * i + 1], b ? 0x7632u : 0x5410u), s, z, k);
       }
     }
   }
@@ -597,7 +586,7 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
     // and K(t + 2) for every tile t, behind the S that read the K buffer before.
     // V(t) goes into its buffer behind PV(t - 2).
     const int b = warp - kWidenWarp;    // the block of every tile this warp widens
-    const I4Consts kc4{opaque(64u), opaque(4u), opaque(0x4c004c00u)};
+    const I4Magic kc4;
     uint32_t kc = 0, vc = 0;            // K and V code tiles so far (staging buffer: & 1)
     uint32_t nk[2] = {0, 0}, nv[2] = {0, 0};  // tiles per K and V buffer so far
     bool ok = true;

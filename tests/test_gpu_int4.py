@@ -6,9 +6,9 @@ Tolerance of attention against fp64 over the same codes, |v| <= Vmax and a group
 (at most 8 and 10 for the N(0, 1) data here, times v_scale).  A rounding is off by at most
 half a step, relative 2^-8 in bf16 and 2^-11 in f16.
   output          2^-8 |o|
-  V values        z - 16 s to f16: 2^-11 x 1.6 R, the value to f16: 2^-11 Vmax
+  V values        c s + z to f16: 2^-11 Vmax (room for z - 16 s to f16 besides, 2^-11 x 1.6 R)
   P to f16        2^-11 Vmax (every weight off by 2^-11 of itself)
-  logits, chunks  K values rounded to f16 the same way: at most 2^-11 (1.6 R + Vmax) an element, close
+  logits, chunks  K values rounded to f16 the same way: at most 2^-11 (1.6 R + Vmax) an element, if
                   to uniform over z - 16 s's step, shared by a group's 32 dims; a logit is off by
                   sigma = sqrt(D) / sqrt(D) x 2^-11 x 1.6 R / sqrt(3) = 4.5e-3 rms for R = 10, and moves o
                   by that times sum p |v - o| <= 1; five sigma over the sampled outputs
