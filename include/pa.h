@@ -61,6 +61,9 @@ typedef enum {
 
 typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
 
+/* |x / scale| saturates here in a PA_INT4 cache (see pa_layout). */
+#define PA_INT4_LIMIT 16384
+
 /* Bits the kernels OR into the optional device status word. */
 #define PA_DEV_SLOT_RANGE 1   /* slot >= num_blocks*block_size: that token's write skipped */
 #define PA_DEV_BLOCK_RANGE 2  /* a used block-table entry outside [0,num_blocks): read as zeros */
@@ -127,7 +130,6 @@ typedef struct {
  *   stream        cudaStream_t
  * num_tokens == 0 is a no-op.
  */
-#define PA_INT4_LIMIT 16384
 int pa_cache_write(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
                    void* k_cache, void* v_cache, const pa_layout* layout, int32_t* status,
                    void* stream);
