@@ -74,8 +74,8 @@ struct PlanParams {
   int num_sms;          // SMs of the device
   int num_ctas;         // CTAs of the decode kernel's grid (the plan sizes splits from the
                         // step's KV per CTA)
-  int num_ctas_small;   // CTAs of the few-token kernel's grid if its splits are sized from its
-                        // own share per CTA (4-bit cache), else 0
+  int num_ctas_small;   // CTAs of the few-token kernel's grid if a small step's few-token splits
+                        // are sized from its share per CTA too (4-bit cache), else 0
   int small_positions;  // query positions per small-q tile
   int prefill_min_qlen; // requests with q_len >= this go to the tensor-core kernel
   int prefill_rows;     // query rows (positions x group) per prefill tile
