@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
     __syncwarp();
   };
 
-  if (I4 && warp >= kWidenWarp) {
-    if constexpr (I4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kWidenRegs));
+  // The roles.
+  auto widen_role = [&]() {
     // ------------------------------------------------------------ widening (4-bit)
     // Eight warps, a block of every tile each: K(0), K(1) of the unit, then V(t)
     // and K(t + 2) for every tile t, behind the S that read the K buffer before.
@@ -635,9 +635,8 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 8) {
-  if constexpr (I4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kCopyRegs));
-  if (warp == kKLoadWarp) {
+  };
+  auto k_role = [&]() {
     // ------------------------------------------------------------ units, Q, K
     // Work comes in chunks of pieces (PfItem), fetched from a counter: chunk
     // c is pieces starts[c] .. starts[c + 1] - 1 when the plan cut the unit
@@ -845,7 +844,8 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       }
     }
     __syncwarp();
-  } else if (warp == kVLoadWarp) {
+  };
+  auto v_role = [&]() {
     // ------------------------------------------------------------ V
     // per buffer parity: nv: V tiles (= kGo arrivals); gv: the last kGo phase
     // that carried a copy, plus one; nl: kVLand copies
@@ -940,7 +940,8 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
         if (gv[w] > 0) drain_wait(bar(kGo + w), (gv[w] - 1) & 1, kGoDrainLimit);
     }
     __syncwarp();
-  } else if (I4 && warp == kQWarp) {
+  };
+  auto q_role = [&]() {
     // ------------------------------------------------------------ Q (4-bit)
     for (int uc = 0;; ++uc) {
       const int slot = uc & 1;
@@ -952,7 +953,8 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       if (lane == 0) mbar_arrive(bar(kQFull));
       __syncwarp();
     }
-  } else {  // kMmaWarp
+  };
+  auto mma_role = [&]() {
     // ------------------------------------------------------------ MMA issue
     // Kept lean: every cycle this warp spends between products is tensor-core
     // idle time (the issue queue is shallow).  Counters live in registers,
@@ -1047,9 +1049,8 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       drain_wait(bar(kDrain), 0);
     }
     __syncwarp();
-  }
-  } else {
-    if constexpr (I4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+  };
+  auto softmax_role = [&]() {
     // ------------------------------------------------------------ softmax
     // Warpgroup w takes keys 64w .. 64w + 63 of every tile; thread i owns
     // query row i = TMEM lane i.  The two threads of a row trade their half
@@ -1330,6 +1331,28 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
         }
       }
     }
+  };
+  if constexpr (I4) {
+    // (a warpgroup's register share is set inside its branch: set before the
+    // branches, the compiler holds every role to the smallest)
+    if (warp >= kWidenWarp) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kWidenRegs));
+      widen_role();
+    } else if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kCopyRegs));
+      if (warp == kKLoadWarp) k_role();
+      else if (warp == kVLoadWarp) v_role();
+      else if (warp == kQWarp) q_role();
+      else mma_role();
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+      softmax_role();
+    }
+  } else {
+    if (warp == kKLoadWarp) k_role();
+    else if (warp == kVLoadWarp) v_role();
+    else if (warp == kMmaWarp) mma_role();
+    else softmax_role();
   }
 
   tc_fence_before();
