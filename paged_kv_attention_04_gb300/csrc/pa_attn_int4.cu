@@ -1,6 +1,5 @@
 // Attention over a 4-bit cache for decode and few-token tiles (bf16 q/out):
-// split-KV, warp-level f16 matrix products, bulk copies of whole pages, a fused
-// log-sum-exp merge.  Work lists, units and the merge are those of the bf16
+// split-KV, warp-level f16 matrix products, a fused log-sum-exp merge.  Work lists, units and the merge are those of the bf16
 // kernel (pa_attn_mma.cuh); the plan kernel writes them.
 //
 // What bounds it: the pages, 20 D bytes per block and kv head, from HBM: at its
@@ -28,21 +27,24 @@
 // warps an SM instead of 12: 48 requests of 2-8 tokens after 256-4096, 32/8 heads,
 // took 130 us instead of 112 (kernel and plan).
 // Lane (g, c) = (lane / 4, lane % 4) holds S^T at keys g, g + 8 and rows 2c,
-// 2c + 1 and O^T at dims (D/8) g + 2 mt, + 1 of m-tile mt: its
-// V codes are one run of the page, all of one group.
+// 2c + 1, and O^T at dims (D/8) g + 2 mt, + 1 of m-tile mt: its V codes are one
+// run of the page, all of one group.
 //
 // The softmax keeps a running maximum per row that moves only when a logit
 // exceeds it by 2^8 (base 2), found by a vote; most steps need no shuffle and
 // no rescaling.  P <= 2^8 in f16, sums in float32.
 //
 // A CTA has NW compute warps and one scheduler warp.  A compute warp takes pairs
-// of blocks w, w + NW, ... of a unit through a ring of NS stages (four bulk
-// copies and one mbarrier a stage, issued by four lanes) that runs on into the
-// next unit.  The scheduler warp claims and stages one unit ahead, and joins and
-// writes (or merges) the finished one; the roles meet on mbarriers only (unit
-// ready, warp states written, warp states read), so a warp that is done goes on.
-// Every wait is bounded: one that gives up flags PA_DEV_TIMEOUT and ends the CTA
-// after its copies have landed.
+// of blocks w, w + NW, ... of a unit through a ring of NS stages of 16-byte
+// asynchronous copies that runs on into the next unit.  (Whole pages by bulk copy
+// were slower: a warp's four are issued one lane after the other.)  The scheduler
+// warp claims and stages one unit ahead and joins the finished one; where that
+// completes a split tile, the merge goes to the compute warps as their next
+// unit.  The roles meet on mbarriers only (unit ready, warp states written, warp
+// states read), so a warp that is done goes on.  Every wait is bounded: one that
+// gives up flags PA_DEV_TIMEOUT and ends the CTA after its copies have landed.
+// Measured on Llama-3-8B heads: 256 requests of median 1024 keys 81 us (4 950 GB/s of
+// pages and the rest), 16 of 32768-131072 295 us with the plan (5 800 GB/s).
 #include <cuda_fp16.h>
 
 #include "pa_attn_mma.cuh"
