@@ -34,10 +34,14 @@
 // the V buffers themselves) and the softmax warps widen them to f16, one
 // 16-token block per warp, while they work on the tile before; the products
 // run as kind::f16.
-// A 4-bit cache (pa_int4.cuh) goes the same way: a block's page is one bulk copy,
-// and widening turns codes into values c s + z in f16.  Its head dims come out of the words
-// as 0, 4, 1, 5, 2, 6, 3, 7 of every eight; Q takes that order too, and the output's
-// columns are put back as they are written.
+// A 4-bit cache (pa_int4.cuh): a block's page is one bulk copy, K and V go to
+// staging buffers two tiles ahead, and eight warps of their own turn codes into
+// values c s + z in f16, a block of every tile each; one more converts Q.  Head
+// dims come out of the words as 0, 4, 1, 5, 2, 6, 3, 7 of every eight; Q takes that
+// order too, and the output's columns are put back as they are written.  What
+// bounds it is instruction issue (7000 warp instructions per 128-key tile, 62 % of
+// the slots): a 2048-token chunk over 8192 keys takes 300 us, 800 TFLOP/s; with the
+// widening left to the softmax warps it took 387.
 // Hand-offs are mbarriers; every wait is bounded and a timeout makes the whole
 // CTA stop (status PA_DEV_TIMEOUT), drain its copies and MMAs, and free TMEM.
 #include <cuda.h>
@@ -125,7 +129,8 @@ enum Bar : int {
   kSFull = 8,       // [2] S = Q K^T done (MMA commit); also frees the K buffer
   kGo = 10,         // [2] tile t: P written and S read (8 softmax warps), V of t landed
                     //     (V loader), K of t + 2 landed or none due (K loader); FP8 cache:
-                    //     the softmax warps alone, who also widen K of t + 2 and V of t
+                    //     the softmax warps alone, who also widen K of t + 2 and V of t;
+                    //     4-bit cache: softmax warps and widening warps (K of t + 2, V of t)
   kVLand = 12,      // [2] V tile landed, for a tile whose last block the V loader trims;
                     //     FP8 cache: V codes landed in V buffer 0 / 1
   kPVDone = 14,     // [2] O += P V done (MMA commit); frees the V buffer
@@ -483,9 +488,9 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       ph = -1;
     }
     if constexpr (I4) {
-      // the pages into the staging buffer at dst; a bad table entry leaves a page of zeros (its scales and zeros
-      // too), a block past the unit's keys what was there (K is masked, V rows
-      // past the last key are zeroed as they are widened)
+      // the pages into the staging buffer at dst; a bad table entry leaves a page of
+      // zeros (its scales and zeros too), a block past the unit's keys what was
+      // there (K is masked, V rows past the last key are zeroed as they are widened)
       const bool have = lane < kTileN / kBlockSize && ph >= 0;
       const bool bad = lane < kTileN / kBlockSize && lb_of(t) * kBlockSize < u.kv_end && !have;
       const uint32_t d = dst + lane * kCodeBlock;
