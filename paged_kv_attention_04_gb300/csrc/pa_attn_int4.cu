@@ -31,8 +31,10 @@
 // run of the page, all of one group.
 //
 // The softmax keeps a running maximum per row that moves only when a logit
-// exceeds it by 2^8 (base 2), found by a vote; most steps need no shuffle and
-// no rescaling.  P <= 2^8 in f16, sums in float32.
+// exceeds it by 2^4 (base 2), found by a vote; most steps need no shuffle and
+// no rescaling.  P is held as f16 of 2^11 P <= 2^15, so that a weight keeps its 11
+// bits down to 2^-25 of the largest (long contexts beside a dominant key live on
+// such weights); the factor cancels in the normalisation.  Sums in float32.
 //
 // A CTA has NW compute warps and one scheduler warp.  A compute warp takes pairs
 // of blocks w, w + NW, ... of a unit through a ring of NS stages of 16-byte
@@ -56,7 +58,8 @@ namespace pa {
 namespace {
 
 constexpr unsigned long long kI4WaitNs = 2000000000ull;  // a wait gives up after two seconds
-constexpr float kI4Rescale = 8.f;  // base-2 logit growth that moves the running maximum
+constexpr float kI4Rescale = 4.f;  // base-2 logit growth that moves the running maximum
+constexpr float kI4Lift = 11.f;    // P is held times 2^11: at most 2^15 in f16
 
 template <int D, int G, int P, int NW, int NS>
 struct I4Cfg {
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
       rm[1] = fr[min(2 * c4 + 1, R - 1)];
     }
     // running state of rows 2 c4, 2 c4 + 1: maximum (before the row factor), the
-    // value that moves it, minus the maximum's logit, sum; O^T
+    // value that moves it, the lift minus the maximum's logit, sum; O^T
     float o[MT][4];
     float m[2], thr[2], mneg[2], l[2];
 #pragma unroll
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
             const float corr = ex2_approx((m[e] - mx) * rm[e]);  // 0 before the first visible key
             m[e] = mx;
             thr[e] = mx + kI4Rescale / rm[e];
-            mneg[e] = -mx * rm[e];
+            mneg[e] = fmaf(-mx, rm[e], kI4Lift);
             l[e] *= corr;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -688,7 +691,8 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
           *reinterpret_cast<float2*>(cb + (warp * R + row) * D + (D / 8) * g + 2 * mt) =
               make_float2(o[mt][e], o[mt][2 + e]);
         if (g == 0) {
-          cm[(warp * R + row) * 2] = m[e] * rm[e];
+          // (the logit whose P is 1, so that the lift cancels in the merges)
+          cm[(warp * R + row) * 2] = m[e] == -CUDART_INF_F ? m[e] : -mneg[e];
           cm[(warp * R + row) * 2 + 1] = sum;
         }
       }

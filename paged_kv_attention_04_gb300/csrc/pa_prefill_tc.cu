@@ -74,7 +74,14 @@ constexpr int kWidenWarps = 8;
 constexpr int pf_threads(pa_dtype kv) { return kv == PA_INT4 ? 640 : 352; }
 constexpr int kSoftmaxRegs = 152, kCopyRegs = 80, kWidenRegs = 48;
 constexpr uint32_t kWaitLimit = 1u << 24;
-constexpr float kRescaleThreshold = 8.f;  // base-2 logit growth that forces a rescale
+// Base-2 logit growth that forces a rescale of a row, and the power of two that P is
+// held times: P <= 2^8 in bf16, whose exponent reaches every weight.  f16 ends at
+// 2^-14 (11 bits) and 2^-24, so there P is held times 2^11 and the maximum moves at
+// 2^4: at most 2^15, and a weight keeps its 11 bits down to 2^-25 of the largest (long
+// contexts beside a dominant key live on such weights).  The factor cancels in the
+// normalisation and, as part of the row's reference, in the merges.
+constexpr float rescale_threshold(pa_dtype kv) { return kv == PA_INT4 ? 4.f : 8.f; }
+constexpr float p_lift(pa_dtype kv) { return kv == PA_INT4 ? 11.f : 0.f; }
 
 template <int D>
 struct PfCfg {
@@ -1132,7 +1139,7 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
       const int jj = i / G;
       const bool row_ok = jj < u.npos;
       const int my_pos = u.pos0 + jj;
-      float m_used = -CUDART_INF_F, l_part = 0.f;
+      float m_used = -CUDART_INF_F, l_part = 0.f;  // the logit whose P is 1; row sum
       bool ok = true;
       for (int t = 0; t < u.n_kv; ++t) {  // t: place in the unit's order
         const int b = t & 1;
@@ -1188,12 +1195,13 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
         if (!wait_bar(bar(kMx + b), nb & 1, abort, p.status)) { ok = false; break; }
         mx = fmaxf(mx, s_mx[b][w ^ 1][i]);
         float f = 1.f;  // this tile's rescale of the row's earlier state
-        if (mx > m_used + kRescaleThreshold) {
-          f = ex2(m_used - mx);  // 0 while the row had no visible key
+        if (mx > m_used + (rescale_threshold(KV) + p_lift(KV))) {
+          const float m_new = mx - p_lift(KV);
+          f = ex2(m_used - m_new);  // 0 while the row had no visible key
           l_part *= f;
-          m_used = mx;
+          m_used = m_new;
         }
-        // P = exp2(logit - m) as bf16 pairs into columns 32w .. 32w + 31 of S
+        // P = exp2(logit - m) as bf16 (codes: f16) pairs into columns 32w .. 32w + 31 of S
         // buffer b (keys 64w .. 64w + 63 of the tile)
         {
           const float m_sub = m_used == -CUDART_INF_F ? 0.f : m_used;
