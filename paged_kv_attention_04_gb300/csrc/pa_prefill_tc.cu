@@ -80,8 +80,8 @@ constexpr uint32_t kWaitLimit = 1u << 24;
 // 2^4: at most 2^15, and a weight keeps its 11 bits down to 2^-25 of the largest (long
 // contexts beside a dominant key live on such weights).  The factor cancels in the
 // normalisation and, as part of the row's reference, in the merges.
-constexpr float rescale_threshold(pa_dtype kv) { return kv == PA_INT4 ? 4.f : 8.f; }
-constexpr float p_lift(pa_dtype kv) { return kv == PA_INT4 ? 11.f : 0.f; }
+constexpr float rescale_threshold(pa_dtype kv) { return kv == PA_BF16 ? 8.f : 4.f; }
+constexpr float p_lift(pa_dtype kv) { return kv == PA_BF16 ? 0.f : 11.f; }
 
 template <int D>
 struct PfCfg {

@@ -1,4 +1,5 @@
-"""Softmax weights far below a row's largest over the 4-bit cache.
+"""Softmax weights far below a row's largest over the caches whose weights are held in f16:
+4-bit and FP8 (whose K and V values are exact in f16).
 
 Every 32nd key has logit 0 and V = 0 (an attention sink); the others lie `a` nats below, +-0.5,
 with V of N(0, 1), so the output is made of the small weights alone and is judged relative to
@@ -23,9 +24,11 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import int4
+import oracle
+from oracle import fp8, int4
 import paged_kv_attention_04_gb300 as P
 
+from helpers import bits
 from test_gpu_int4 import forward, make, reference, spec, wide
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +80,18 @@ def test_small_weights_keep_their_bits(q, s, D, a):
     out, flags = forward(st, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay, q=cpu.q.cuda())
     assert flags == 0
     close_relative(out, reference(cpu, kc, vc), a, cpu.q)
+
+
+@pytest.mark.parametrize("a", [14, 18])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q,s", [([1, 1], [3000, 700]), ([5, 15], [2500, 1000]), ([16, 40], [3000, 1000])])
+def test_small_weights_keep_their_bits_fp8(q, s, D, a):
+    cpu, st, _, _, _ = make(spec(q, s, D=D, seed=150 + D + a + q[0]))
+    ks, vs = 0.0625, 0.03125
+    kc, vc = (fp8.encode(x / sc) for x, sc in zip(sinks(cpu, a), (ks, vs)))
+    lay = P.layout_of(torch.from_numpy(kc), cpu.spec.num_q_heads, k_scale=ks, v_scale=vs)
+    out, flags = forward(st, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay, q=cpu.q.cuda())
+    assert flags == 0
+    ref = oracle.paged_attention(bits(cpu.q), fp8.dequantize(kc, ks), fp8.dequantize(vc, vs), cpu.block_tables.numpy(),
+                                 cpu.spec.seq_lens, cpu.query_start_loc.numpy(), cpu.scale, cpu.spec.num_kv_heads)
+    close_relative(out, ref, a, cpu.q)
