@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
         fence_proxy_async_smem();  // before a later copy to this place
       }
       const int copies = __popc(__ballot_sync(0xffffffffu, have));
+      __syncwarp();  // the zeros of every lane come before lane 0's arrival
       if (lane == 0) mbar_arrive_expect_tx(full, copies * kCodeBlock);
       __syncwarp();
       if (have)

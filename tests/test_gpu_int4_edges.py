@@ -1,0 +1,41 @@
+"""Edges of the 4-bit cache: bad block-table entries in later tiles of a chunk, K values far from
+zero, pages issued across many short units.  Tolerances as in test_gpu_int4.py unless derived at
+the test."""
+import pytest
+import torch
+
+from oracle import int4
+import paged_kv_attention_04_gb300 as P
+
+from test_gpu_int4 import close, forward, make, reference, spec, wide
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_attention_04_gb300 import build
+    build.build()
+    P.lib()
+
+
+def filled(sp):
+    """A step whose new tokens are in the pools: (cpu step, gpu step, K pool, V pool, layout)."""
+    cpu, st, kc, vc, lay = make(sp)
+    kc = int4.store(kc, wide(cpu.k), cpu.slot_mapping, 1.0, False)
+    vc = int4.store(vc, wide(cpu.v), cpu.slot_mapping, 1.0, True)
+    return cpu, st, kc, vc, lay
+
+
+@pytest.mark.parametrize("q", [16, 300])
+def test_bad_block_ids_in_later_tiles_read_as_zeros(q):
+    """Several per 128-key tile, in tiles whose staging buffer held another tile's pages."""
+    cpu, st, kc, vc, lay = filled(spec([q], [1700], seed=160 + q))
+    bt = st.block_tables.clone()
+    zk, zv = kc.copy(), vc.copy()
+    for i, b in enumerate((1, 17, 18, 23, 40, 41, 42, 43, 44, 45, 46, 47, 70, 105)):
+        zk[cpu.block_tables[0, b]] = zv[cpu.block_tables[0, b]] = 0
+        bt[0, b] = (-1, lay.num_blocks, 1 << 30)[i % 3]
+    out, flags = forward(st, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay, bt=bt)
+    assert flags == P.PA_DEV_BLOCK_RANGE
+    close(out, reference(cpu, zk, zv))
