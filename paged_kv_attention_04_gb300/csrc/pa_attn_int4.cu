@@ -418,7 +418,9 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
     while (iss_bl >= iss_n) {
       if (iss_unit >= limit || iss_end) return false;
       const int k = iss_unit + 1;
-      if (!mbar_test(bar_unit + (k & 1) * 8, (k >> 1) & 1)) return false;
+      // (one answer for the warp: lanes that saw the unit at different steps would
+      // fill different stages)
+      if (!__all_sync(0xffffffffu, mbar_test(bar_unit + (k & 1) * 8, (k >> 1) & 1))) return false;
       const UnitMeta& m = meta(k);
       iss_unit = k;
       iss_end = m.valid == 0;

@@ -39,3 +39,18 @@ def test_bad_block_ids_in_later_tiles_read_as_zeros(q):
     out, flags = forward(st, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay, bt=bt)
     assert flags == P.PA_DEV_BLOCK_RANGE
     close(out, reference(cpu, zk, zv))
+
+
+@pytest.mark.parametrize("q", [1, 3])
+def test_units_shorter_than_the_ring(q):
+    """Requests of one to four blocks and a few longer ones: a warp's stream runs on into units
+    that are published while it asks for them; the results repeat to the bit."""
+    lens = [(7 * i) % 61 + q for i in range(700)] + [900, 2000]
+    cpu, st, kc, vc, lay = filled(spec([q] * len(lens), lens, D=64, seed=170 + q))
+    kc, vc = torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda()
+    a, flags = forward(st, kc, vc, lay)
+    assert flags == 0
+    close(a, reference(cpu, kc.cpu().numpy(), vc.cpu().numpy()))
+    for _ in range(10):
+        b, _ = forward(st, kc, vc, lay)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
