@@ -20,6 +20,7 @@ PA_DEV_SLOT_RANGE, PA_DEV_BLOCK_RANGE, PA_DEV_QSL, PA_DEV_LENGTHS, PA_DEV_CAPACI
 PA_DEV_TIMEOUT = 32
 
 _DTYPES = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
+_ELEM_BYTES = {PA_F32: 4, PA_BF16: 2}
 
 
 class pa_layout(ctypes.Structure):
@@ -120,6 +121,16 @@ def _int4_pages(layout: pa_layout, *caches) -> None:
                                           f"{tuple(c.shape)}")
 
 
+def _int64_slots(slot_mapping) -> None:
+    if slot_mapping.dtype != torch.int64:
+        raise PaError(PA_ERR_INVALID, f"slot_mapping is {slot_mapping.dtype}, expected torch.int64")
+
+
+def _rows_message(name: str, t, n: int, layout: pa_layout) -> str:
+    return (f"{name} is {t.dtype} {tuple(t.shape)}, expected {n} rows of {layout.num_kv_heads} x "
+            f"{layout.head_size} of the layout's dtype")
+
+
 # the current stream's handle without building a Stream object (about a microsecond a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -182,13 +193,23 @@ def layout_of(k_cache: torch.Tensor, num_q_heads: int, dtype=None, k_scale: floa
 
 def pa_cache_write(k, v, slot_mapping, k_cache, v_cache, layout: pa_layout,
                    status: torch.Tensor | None = None, stream=None) -> None:
-    """Write k[t], v[t] into slot slot_mapping[t] of the caches (in place)."""
+    """Write k[t], v[t] into slot slot_mapping[t] (int64) of the caches (in place); k's
+    first dimension counts the tokens."""
     dev = _on_one_device(k=k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache,
                          status=status)
     _int4_pages(layout, k_cache, v_cache)
-    if slot_mapping.numel() < k.shape[0]:
-        raise PaError(PA_ERR_INVALID, f"{slot_mapping.numel()} slots for {k.shape[0]} tokens")
-    _launch(lib().pa_cache_write, dev, stream, _ptr(k), _ptr(v), _ptr(slot_mapping), k.shape[0],
+    _int64_slots(slot_mapping)
+    n = k.shape[0]
+    if slot_mapping.numel() < n:
+        raise PaError(PA_ERR_INVALID, f"{slot_mapping.numel()} slots for {n} tokens")
+    elems = n * layout.num_kv_heads * layout.head_size
+    for name, t in (("k", k), ("v", v)):
+        # (an unquantised cache takes the rows' bits: any type of the same size will do)
+        typed = _DTYPES.get(t.dtype) == layout.dtype or (
+            layout.cache_dtype == layout.dtype and t.element_size() == _ELEM_BYTES.get(layout.dtype))
+        if not typed or t.numel() < elems or (t is k and t.numel() != elems):
+            raise PaError(PA_ERR_INVALID, _rows_message(name, t, n, layout))
+    _launch(lib().pa_cache_write, dev, stream, _ptr(k), _ptr(v), _ptr(slot_mapping), n,
             _ptr(k_cache), _ptr(v_cache), ctypes.byref(layout), _ptr(status))
 
 
@@ -206,14 +227,12 @@ def pa_cache_read(k_cache, v_cache, slot_mapping, k, v, layout: pa_layout,
     dev = _on_one_device(k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, k=k, v=v,
                          status=status)
     _int4_pages(layout, k_cache, v_cache)
+    _int64_slots(slot_mapping)
     n = slot_mapping.shape[0]
-    if slot_mapping.dtype != torch.int64:
-        raise PaError(PA_ERR_INVALID, f"slot_mapping is {slot_mapping.dtype}, expected torch.int64")
     elems = n * layout.num_kv_heads * layout.head_size
     for name, t in (("k", k), ("v", v)):
         if t.numel() != elems or _DTYPES.get(t.dtype) != layout.dtype:
-            raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, expected {n} rows of "
-                                          f"{layout.num_kv_heads} x {layout.head_size} of the layout's dtype")
+            raise PaError(PA_ERR_INVALID, _rows_message(name, t, n, layout))
     _launch(lib().pa_cache_read, dev, stream, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n,
             _ptr(k), _ptr(v), ctypes.byref(layout), _ptr(status))
 
