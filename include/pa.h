@@ -102,7 +102,13 @@ typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
  *           s of group g at 8 D + 64 g + 16 ((t%8)/2) + 4 (t/8) + 2 (t%2), z 8 bytes on.
  * Over a quantised cache (FP8 or 4-bit) attention takes q in f16: chunks of 16
  * and more tokens want |q| <= 65504, and below 2^-14 it is rounded to a multiple
- * of 2^-24; shorter queries over a 4-bit cache are scaled by a power of two first. */
+ * of 2^-24; shorter queries over a 4-bit cache are scaled by a power of two first.
+ * The softmax weights of a quantised cache are f16 too, scaled so that a weight
+ * keeps 11 bits down to 2^-25 of its row's largest; sums are float32.
+ * V values c * s + z of a 4-bit cache are rounded to f16 once, and so are the K
+ * values of chunks: off by up to 2^-11 |c * s + z|, which a logit of a chunk
+ * feels where |z| is many times s.  Shorter queries take K exactly, with the sums
+ * of q over a group (which multiply z) kept to 2^-15 of the row's largest |q|. */
 typedef struct {
   int num_q_heads;
   int num_kv_heads;

@@ -1,6 +1,7 @@
 """Edges of the 4-bit cache: bad block-table entries in later tiles of a chunk, K values far from
 zero, pages issued across many short units.  Tolerances as in test_gpu_int4.py unless derived at
 the test."""
+import numpy as np
 import pytest
 import torch
 
@@ -54,3 +55,32 @@ def test_units_shorter_than_the_ring(q):
     for _ in range(10):
         b, _ = forward(st, kc, vc, lay)
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q,s", [([1, 1], [2500, 300]), ([7, 15], [2500, 300]), ([40, 130], [2500, 300])])
+def test_keys_far_from_zero(q, s, D):
+    """K of 30 + N(0, 1): a group's zero is 90 of its steps.
+
+    Queries below 16 tokens use K as the codes say (z against the group sums of q, kept to 2^-15 of
+    the row's largest q; z differs by 0.4 between keys: under 1e-5 in a logit): tolerances unchanged.
+    Chunks round K to f16: half a step is 2^-7 below 32, 2^-6 above (2.3 % of the values), 4.7e-3 rms;
+    over D dims of q of N(0, 1) and a scale of 1 / sqrt(D) a logit is off by as much, and o by
+    that times |v - o|: sqrt(4.7e-3^2 + 2.4e-3^2) = 5.3e-3 in the 2-norm, an element by the
+    2^-11 x 10 and 2^-8 |o| of the other roundings and five sigma, 2.84e-2."""
+    cpu, st, kc, vc, lay = filled(spec(q, s, D=D, seed=180 + D + q[0]))
+    pool = 30 + cpu.k_cache.float().numpy()
+    bt = cpu.block_tables.numpy()
+    for r, n in enumerate(s):   # this step's tokens too
+        pos = np.arange(n - q[r], n)
+        pool[bt[r, pos // 16], pos % 16] = 30 + wide(cpu.k)[cpu.query_start_loc[r]:cpu.query_start_loc[r + 1]]
+    kc = int4.pack(pool, 1.0, False)
+    out, flags = forward(st, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay)
+    assert flags == 0
+    ref = reference(cpu, kc, vc)
+    if q[0] < 16:
+        close(out, ref)
+        return
+    err = np.abs(wide(out) - ref)
+    assert (err <= 2.84e-2 + 2.0 ** -8 * np.abs(ref)).all()
+    assert np.linalg.norm(err) <= 5.3e-3 * np.linalg.norm(ref)
