@@ -626,10 +626,13 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
 #pragma unroll
           for (int o8 = 4; o8 < 32; o8 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o8));
           if (mx > m[e]) {
-            const float corr = ex2_approx((m[e] - mx) * rm[e]);  // 0 before the first visible key
+            // (rounded down: at logits of 2^23, whose steps are 1, roundings to nearest
+            // could put P past f16's end)
+            const float mn = __fmaf_rd(-mx, rm[e], kI4Lift);
+            const float corr = m[e] == -CUDART_INF_F ? 0.f : ex2_approx(mn - mneg[e]);
             m[e] = mx;
-            thr[e] = mx + kI4Rescale / rm[e];
-            mneg[e] = fmaf(-mx, rm[e], kI4Lift);
+            thr[e] = __fadd_rd(mx, kI4Rescale / rm[e]);
+            mneg[e] = mn;
             l[e] *= corr;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {

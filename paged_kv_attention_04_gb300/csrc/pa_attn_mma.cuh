@@ -127,7 +127,8 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 // FP8 cache: P enters the f16 product times 2^15 (its largest is 1), so that a weight
 // keeps its 11 bits down to 2^-29 of the largest; the factor is part of the running
-// reference m, so it cancels in the merges and the normalisation.
+// reference m, so it cancels in the merges and the normalisation.  m is rounded up:
+// at logits of 2^24, whose steps are 2, a nearest m could put P past f16's end.
 constexpr float kF8Lift = 15.f;
 // Two E4M3 codes (low byte first) -> two f16 values, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes16) {
@@ -665,8 +666,8 @@ __global__ void __launch_bounds__(MmaCfg<D, G, P, NW, NS, F8, SW>::kThreads,
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o8));
           }
           if constexpr (F8) {  // m: the logit whose P is 1
-            mx0 -= kF8Lift;
-            mx1 -= kF8Lift;
+            mx0 = __fadd_ru(mx0, -kF8Lift);
+            mx1 = __fadd_ru(mx1, -kF8Lift);
           }
           const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
           float corr0 = 1.f, corr1 = 1.f, pr[4];
@@ -873,7 +874,7 @@ __global__ void __launch_bounds__(MmaCfg<D, G, P, NW, NS, F8, SW>::kThreads,
             }
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          if constexpr (F8) mx -= kF8Lift;  // m: the logit whose P is 1
+          if constexpr (F8) mx = __fadd_ru(mx, -kF8Lift);  // m: the logit whose P is 1
           const float mn = fmaxf(mA, mx);
           float corr = 1.f;
           if (mn != -CUDART_INF_F) {
@@ -903,7 +904,7 @@ __global__ void __launch_bounds__(MmaCfg<D, G, P, NW, NS, F8, SW>::kThreads,
               }
             mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
             mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-            if constexpr (F8) mxb -= kF8Lift;
+            if constexpr (F8) mxb = __fadd_ru(mxb, -kF8Lift);
             const float mnb = fmaxf(mB, mxb);
             if (mnb != -CUDART_INF_F) {
               corrB = ex2_approx(mB - mnb);

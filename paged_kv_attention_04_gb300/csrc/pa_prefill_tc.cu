@@ -79,9 +79,15 @@ constexpr uint32_t kWaitLimit = 1u << 24;
 // 2^-14 (11 bits) and 2^-24, so there P is held times 2^11 and the maximum moves at
 // 2^4: at most 2^15, and a weight keeps its 11 bits down to 2^-25 of the largest (long
 // contexts beside a dominant key live on such weights).  The factor cancels in the
-// normalisation and, as part of the row's reference, in the merges.
+// normalisation and, as part of the row's reference, in the merges.  For f16 the maximum
+// and the reference are rounded up and the border down: at logits of 2^23, whose steps are
+// 1, roundings to nearest could put P past f16's end.
 constexpr float rescale_threshold(pa_dtype kv) { return kv == PA_BF16 ? 8.f : 4.f; }
 constexpr float p_lift(pa_dtype kv) { return kv == PA_BF16 ? 0.f : 11.f; }
+template <pa_dtype KV>
+__device__ __forceinline__ float scaled_max(float mx, float scale) {
+  return KV == PA_BF16 ? mx * scale : __fmul_ru(mx, scale);
+}
 
 template <int D>
 struct PfCfg {
@@ -1180,12 +1186,12 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
 #pragma unroll
               for (int c = 4; c < 64; c += 2)
                 m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-              mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+              mx = scaled_max<KV>(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), sl2);
             } else {
 #pragma unroll
               for (int c = 4; c < 64; c += 2)
                 m4[(c >> 1) & 3] = min3(m4[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-              mx = fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3])) * sl2;
+              mx = scaled_max<KV>(fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3])), sl2);
             }
           }
         }
@@ -1196,8 +1202,9 @@ __global__ void __launch_bounds__(pf_threads(KV), 1)
         if (!wait_bar(bar(kMx + b), nb & 1, abort, p.status)) { ok = false; break; }
         mx = fmaxf(mx, s_mx[b][w ^ 1][i]);
         float f = 1.f;  // this tile's rescale of the row's earlier state
-        if (mx > m_used + (rescale_threshold(KV) + p_lift(KV))) {
-          const float m_new = mx - p_lift(KV);
+        constexpr float kBorder = rescale_threshold(KV) + p_lift(KV);
+        if (mx > (CODES ? __fadd_rd(m_used, kBorder) : m_used + kBorder)) {
+          const float m_new = CODES ? __fadd_ru(mx, -p_lift(KV)) : mx;
           f = ex2(m_used - m_new);  // 0 while the row had no visible key
           l_part *= f;
           m_used = m_new;
