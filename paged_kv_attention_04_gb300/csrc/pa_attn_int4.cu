@@ -274,11 +274,12 @@ __global__ void __launch_bounds__(I4Cfg<D, G, P, NW, NS>::kThreads, I4Cfg<D, G, 
             sum -= __half2float(part);
           }
         }
-        if (c == 0)  // base-2 logit = (accumulated sum) x factor; kept positive
+        if (c == 0) {  // base-2 logit = (accumulated sum) x factor; kept positive and finite
+          const float f = fabsf(p.scale_log2) * 1048576.f *
+                          __uint_as_float(static_cast<uint32_t>(ex - 10 + 127) << 23);
           *reinterpret_cast<float*>(qb + R * (C::kQRowBytes + 32) + row * 4) =
-              fmaxf(fabsf(p.scale_log2) * 1048576.f *
-                        __uint_as_float(static_cast<uint32_t>(ex - 10 + 127) << 23),
-                    1e-37f);
+              fminf(fmaxf(f, 1e-37f), 3e38f);
+        }
       }
     };
     auto publish = [&](int k, int u) {  // unit k of the sequence is unit u of the list

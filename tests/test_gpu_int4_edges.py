@@ -84,3 +84,17 @@ def test_keys_far_from_zero(q, s, D):
     err = np.abs(wide(out) - ref)
     assert (err <= 2.84e-2 + 2.0 ** -8 * np.abs(ref)).all()
     assert np.linalg.norm(err) <= 5.3e-3 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("q,s", [([1, 1], [700, 40]), ([5, 3], [700, 40]), ([16, 20], [700, 40])])
+def test_a_k_scale_beyond_the_data_gives_keys_of_zero(q, s):
+    """K of N(0, 1) over a scale of 1e37 has codes, scales and zeros of 0: all keys weigh alike.
+    The scale itself times the largest q is past float32."""
+    cpu, st, _, vc, lay = filled(spec(q, s, seed=200 + q[0]))
+    x = cpu.k_cache.float().numpy()
+    x.reshape(-1, *x.shape[2:])[cpu.slot_mapping.numpy()] = wide(cpu.k)
+    kc = int4.pack(x, 1e37, False)
+    lay.k_scale = 1e37
+    out, flags = forward(st, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay)
+    assert flags == 0
+    close(out, reference(cpu, kc, vc, ks=1e37))
