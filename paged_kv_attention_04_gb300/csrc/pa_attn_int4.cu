@@ -1,6 +1,7 @@
 // Attention over a 4-bit cache for decode and few-token tiles (bf16 q/out):
-// split-KV, warp-level f16 matrix products, a fused log-sum-exp merge.  Work lists, units and the merge are those of the bf16
-// kernel (pa_attn_mma.cuh); the plan kernel writes them.
+// split-KV, warp-level f16 matrix products, a fused log-sum-exp merge.  Work lists
+// and units are those of the bf16 kernel (pa_attn_mma.cuh); the plan kernel writes
+// them.
 //
 // What bounds it: the pages, 20 D bytes per block and kv head, from HBM: at its
 // copy rate an SM takes one 2560-byte block (D = 128) per ~110 clocks, so each
@@ -12,11 +13,12 @@
 //      of each half) or c 2^-20 (nibbles 1), exact as a matrix operand, so 8
 //      codes take 4 ANDs and a shift.  q is staged in f16, scaled by a power of
 //      two per row (largest |q| in [2^10, 2^11)) and by 16 more for the dims
-//      whose codes are the c 2^-24: exact but for q below 2^-34 of the row's
-//      largest.  Each group accumulates by itself (two MMAs) and the scales are
+//      whose codes are the c 2^-24: exact down to 2^-27 of the row's largest (a bf16
+//      q has 8 bits and f16 ends at 2^-24), below it off by 2^-35 of the largest at
+//      most.  Each group accumulates by itself (two MMAs) and the scales are
 //      applied to the float32 sums; the zeros term is one more MMA, z against
-//      the group sums of q 2^-20 split into f16 parts (to 2^-24, 2^-14 of the
-//      row's largest q).
+//      the group sums of q 2^-20 split into f16 parts (off by 2^-25 at most, 2^-15 of
+//      the row's largest q).
 //   V  v = c s + z in f16, rounded once: a masked OR, an exact subtraction and an FMA
 //      per two values (pa_int4.cuh).
 //

@@ -26,7 +26,8 @@
 //     warpgroup w takes its keys 64w .. 64w + 63, thread i owns query row i
 //     = TMEM lane i.  The two threads of a row trade their half maxima, so
 //     both scale by one running maximum, which moves only when the row's
-//     maximum grows by more than 2^8 (base-2 logits): O is rescaled rarely.
+//     maximum grows by more than 2^8 (base-2 logits; 2^4 where P is f16): O is
+//     rescaled rarely.
 //     Each writes its half of P (bf16) over the first half of the tile's S,
 //     which both have read by then.  At the end of the unit the two halves'
 //     row sums are added and each warpgroup writes half of O's columns.
@@ -436,12 +437,14 @@ __device__ __forceinline__ void widen_v_int4(uint32_t src, uint32_t dst, int row
 
 }  // namespace
 
-// KV: the cache's type.  CODES: it holds FP8 or 4-bit codes.  K codes are copied into two
-// staging buffers, two tiles ahead, V codes into the V tile buffers they are
-// widened in; both are widened to f16 (exactly) in the K / V tile buffers, a
-// unit's first two K tiles by the K loader and every other tile by the
-// softmax warps, one block each.  Q is converted from bf16 to f16 in place
-// once per unit, and the two products run as kind::f16 with f16 operands (P
+// KV: the cache's type.  CODES: it holds FP8 or 4-bit codes.  FP8: K codes are
+// copied into two staging buffers, two tiles ahead, V codes into the V tile
+// buffers they are widened in; both are widened to f16 (exactly) in the K / V
+// tile buffers, a unit's first two K tiles by the K loader and every other tile
+// by the softmax warps, one block each.  4-bit: K and V pages have two staging
+// buffers each, and warps 12-19 widen every tile (c s + z, rounded to f16 once).
+// Q is converted from bf16 to f16 in place once per unit (FP8: by the K loader,
+// 4-bit: by warp 11), and the two products run as kind::f16 with f16 operands (P
 // in f16).  The K scale is folded into the softmax scale and the V scale
 // into the normalisation.
 template <int D, int G, pa_dtype KV>
