@@ -98,3 +98,30 @@ def test_a_k_scale_beyond_the_data_gives_keys_of_zero(q, s):
     out, flags = forward(st, torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay)
     assert flags == 0
     close(out, reference(cpu, kc, vc, ks=1e37))
+
+
+def test_pages_past_4_gib_and_off_alignment():
+    """Blocks whose pages lie more than 2^32 bytes into the cache, in caches that start 16 bytes off a
+    larger alignment: write, every attention path and read-back give what a small pool gives."""
+    cpu, st, kc, vc, lay = make(spec([1, 1, 5, 40], [700, 20, 90, 300], Hkv=8, seed=210))
+    nb = lay.num_blocks
+    big = (1 << 32) // (8 * 1280) + 2 * nb
+    ids = torch.randperm(nb) + big - nb   # block i of the small pool is block ids[i] of the large one
+
+    def step(kc, vc, lay, bt, slots):
+        P.pa_cache_write(st.k, st.v, slots, kc, vc, lay)
+        out, flags = forward(st, kc, vc, lay, bt=bt)
+        k, v = torch.empty_like(st.k), torch.empty_like(st.v)
+        P.pa_cache_read(kc, vc, slots, k, v, lay)
+        assert flags == 0
+        return out, k, v
+
+    want = step(torch.from_numpy(kc).cuda(), torch.from_numpy(vc).cuda(), lay, st.block_tables, st.slot_mapping)
+    large = [torch.empty(16 + big * 8 * 1280, dtype=torch.uint8, device="cuda")[16:].view(big, 8, 1280) for _ in range(2)]
+    for c, small in zip(large, (kc, vc)):
+        c[ids.cuda()] = torch.from_numpy(small).cuda()
+    bt, slots = cpu.block_tables.long(), cpu.slot_mapping
+    bt = torch.where(bt < 0, bt, ids[bt.clamp(min=0)]).int().cuda()
+    got = step(*large, P.layout_of(large[0], st.spec.num_q_heads), bt, (ids[slots // 16] * 16 + slots % 16).cuda())
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
