@@ -6,7 +6,17 @@
  *   pa_cache_write  writes each new token's K and V into its paged slot;
  *   pa_forward      runs attention for every new token over its request's
  *                   KV, read through the request's block table.
- * Beside them, pa_cache_read reads slots of a cache back.
+ * Beside them, pa_cache_read reads slots of a cache back, and
+ * pa_rope_cache_write is pa_cache_write with the position rotation of q and k
+ * applied on the way.
+ *
+ * Models that keep one latent vector a token for all heads have a cache and a
+ * step of their own:
+ *   pa_latent_write     normalises, rotates and writes each new token's latent;
+ *   pa_latent_read      reads slots back;
+ *   pa_latent_forward   attention over the latents (absorbed form);
+ *   pa_expanded_forward attention over keys and values of each head's own,
+ *                       computed from the latents (expanded form, prompts).
  *
  * Sources (page title, section):
  *   "Inside vLLM: Anatomy of a High-Throughput LLM Inference System",
@@ -71,6 +81,7 @@ typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
 #define PA_DEV_LENGTHS 8      /* q_len < 1, q_len > seq_len, or a host upper bound exceeded */
 #define PA_DEV_CAPACITY 16    /* the workspace was sized for a smaller step */
 #define PA_DEV_TIMEOUT 32     /* a tensor-core wait gave up; that kernel stopped early */
+#define PA_DEV_POSITION 64    /* position outside [0, max_position): that token skipped */
 
 /* Model-side shape of the KV cache. Supported: block_size 16; head_size 64
  * or 128; num_q_heads / num_kv_heads in {1, 2, 4, 8}.
@@ -283,6 +294,153 @@ int pa_forward_noalloc(const void* q, const void* k_cache, const void* v_cache,
                        int num_seqs, int num_tokens, int max_query_len, int max_seq_len,
                        float scale, void* out, const pa_layout* layout, int32_t* status,
                        void* stream);
+
+/*
+ * Position rotation.  At position p the first n = rope_size dims of a head are
+ * turned in pairs by the table's row cos_sin[p] (float32, n / 2 cosines c, then
+ * n / 2 sines s): (a, b) becomes (a c - b s, b c + a s), in float32 with every
+ * product rounded, then rounded to layout->dtype once.  Dims from n on are unchanged.
+ * Pair i is (x_i, x_(i + n/2)) for PA_ROPE_HALVES, (x_2i, x_(2i+1)) for PA_ROPE_PAIRS.
+ *   positions     device int64 [num_tokens]
+ *   cos_sin       device float32 [max_position][rope_size], 16-byte aligned
+ *   rope_size     a multiple of 16, at most the head's size
+ * A token whose position is outside [0, max_position) is skipped whole and sets
+ * PA_DEV_POSITION.  (The pages do not say where a model's rotation happens.)
+ */
+typedef enum { PA_ROPE_HALVES = 0, PA_ROPE_PAIRS = 1 } pa_rope_style;
+typedef struct {
+  const int64_t* positions;
+  const float* cos_sin;
+  int max_position;
+  int rope_size;
+  pa_rope_style style;
+} pa_rope;
+
+/*
+ * pa_cache_write of rotated keys: q and k of every token are rotated, the
+ * rotated q goes to q_out and the rotated k (rounded to layout->dtype) and v to
+ * the caches as by pa_cache_write (slots, cache types and status bits as there:
+ * the caches get the bits that rotating first and calling pa_cache_write would give).
+ * q, k and v may be slices of one projection: token t starts at q + t * q_stride,
+ * k + t * k_stride, v + t * v_stride (strides in elements), its heads contiguous.
+ *   q, k, v       device, layout->dtype, 16-byte aligned, strides multiples of 16 bytes
+ *   q_out         device, contiguous [num_tokens][num_q_heads][head_size], 16-byte
+ *                 aligned; may be q itself (then q_stride = num_q_heads * head_size), else
+ *                 must not overlap it.  q and q_out NULL: only k and v are written.
+ * A token with a slot < 0 still has its q rotated.
+ */
+int pa_rope_cache_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const pa_rope* rope,
+                        const int64_t* slot_mapping, int num_tokens, void* q_out, void* k_cache,
+                        void* v_cache, const pa_layout* layout, int32_t* status, void* stream);
+
+/* A cache of latents: [num_blocks][16][latent_size + rope_size] of dtype, for every
+ * token a latent vector and a rotated key part that all num_heads query heads share.
+ * Supported: block_size 16; latent_size 256 or 512; rope_size 64; num_heads 1 .. 256;
+ * dtype PA_BF16 (tensor cores) or PA_F32 (plain CUDA cores). */
+typedef struct {
+  int num_heads;
+  int latent_size;
+  int rope_size;
+  int block_size;
+  int num_blocks;
+  pa_dtype dtype;
+} pa_latent_layout;
+
+/*
+ * Append to a latent cache.  For every token t, with s = slot_mapping[t]:
+ *   row s of the cache becomes [c', k'], c' the latent c[t] (norm_weight NULL: its
+ *   bits) or c[t] / sqrt(mean(c[t]^2) + eps) * norm_weight, k' the rotated k_rope[t];
+ *   q_out[t][h] becomes the rotated q[t][h] (rope_size numbers) for every head.
+ * float32 throughout, rounded to dtype once.  Tokens with s < 0 write no row;
+ * s >= num_blocks*block_size sets PA_DEV_SLOT_RANGE.  Slots must be distinct.
+ * Token t of c, k_rope starts at c + t * c_stride, k_rope + t * k_stride; head h of
+ * token t of q (q_out) at q + t * q_stride + h * q_head_stride (qo_ likewise), all in elements.
+ * So q may be the last rope_size numbers of every head of a projection and q_out
+ * those of pa_latent_forward's q.  q_out may be q with the same strides, else must not
+ * overlap it; q and q_out NULL: only the cache is written.
+ * Pointers are 16-byte aligned, strides multiples of 16 bytes.  rope->rope_size is the
+ * layout's.
+ *   norm_weight   device [latent_size] of dtype, or NULL (eps then unused); eps finite, >= 0
+ */
+int pa_latent_write(const void* c, int64_t c_stride, const void* k_rope, int64_t k_stride,
+                    const void* norm_weight, float eps, const void* q, int64_t q_stride,
+                    int64_t q_head_stride, const pa_rope* rope, const int64_t* slot_mapping,
+                    int num_tokens, void* q_out, int64_t qo_stride, int64_t qo_head_stride,
+                    void* cache, const pa_latent_layout* layout, int32_t* status, void* stream);
+
+/*
+ * The reverse: c[t] and k_rope[t] (contiguous [num_tokens][latent_size] and
+ * [num_tokens][rope_size]) receive the bits of slot s = slot_mapping[t] >= 0, for
+ * computing the expanded form's keys and values.  Other rows are left as they were;
+ * s >= num_blocks*block_size sets PA_DEV_SLOT_RANGE.  A slot may be named any number
+ * of times.
+ */
+int pa_latent_read(const void* cache, const int64_t* slot_mapping, int num_tokens, void* c,
+                   void* k_rope, const pa_latent_layout* layout, int32_t* status, void* stream);
+
+/* Bytes of device workspace pa_latent_forward needs for a step within these
+ * bounds; 0 on bad arguments (see pa_last_error). */
+size_t pa_latent_workspace_size(const pa_latent_layout* layout, int num_seqs, int num_tokens,
+                                int max_query_len, int max_seq_len);
+
+/*
+ * Attention over a latent cache, absorbed form.  Steps are described as for
+ * pa_forward (query_start_loc, seq_lens, block_tables, bounds, workspace, status, skipped
+ * requests, early reading of seq_lens and query_start_loc).  With L_p and K_p the latent and
+ * the key part of position p,
+ *   out[t][h] = sum_p softmax_p(scale * q[t][h] . [L_p, K_p]) L_p
+ *   q    device [num_tokens][num_heads][latent_size + rope_size], contiguous, 16-byte aligned
+ *   out  device [num_tokens][num_heads][latent_size], contiguous, 16-byte aligned
+ * bf16: products on the tensor cores with float32 sums, softmax weights rounded to bf16 for
+ * the second product.  NaN or infinity in a slot within a request's length reaches
+ * the rows that see it, and may reach (as NaN) rows of the same request that do not.
+ * Results do not depend on timing: the work is cut by lengths alone and joined in order.
+ */
+int pa_latent_forward(const void* q, const void* cache, const int32_t* block_tables,
+                      int max_blocks_per_seq, const int32_t* seq_lens,
+                      const int32_t* query_start_loc, int num_seqs, int num_tokens,
+                      int max_query_len, int max_seq_len, float scale, void* out, void* workspace,
+                      size_t workspace_bytes, const pa_latent_layout* layout, int32_t* status,
+                      void* stream);
+
+/* Sizes and strides (in elements) of pa_expanded_forward's tensors: element d of head h of
+ * token t of q is q[t * q_stride + h * q_head_stride + d], of k_nope and v likewise, of the
+ * shared key part k_rope[t * kr_stride + d].  Supported: head_size (of k_nope, v and out) 64
+ * or 128; rope_size 64; num_heads 1 .. 256; dtype PA_BF16 (tensor cores) or PA_F32. */
+typedef struct {
+  int num_heads;
+  int head_size;
+  int rope_size;
+  pa_dtype dtype;
+  int64_t q_stride, q_head_stride;
+  int64_t k_stride, k_head_stride;
+  int64_t kr_stride;
+  int64_t v_stride, v_head_stride;
+} pa_expanded_layout;
+
+/*
+ * Attention, expanded form.  Request r owns rows query_start_loc[r] ..
+ * query_start_loc[r+1]-1 of q and out (L of them) and kv_start_loc[r] ..
+ * kv_start_loc[r+1]-1 of k_nope, k_rope and v (S of them, its earlier tokens first).
+ * Row j attends to its request's keys 0 .. S - L + j:
+ *   out[t][h] = sum_p softmax_p(scale * q[t][h] . [k_nope[p][h], k_rope[p]]) v[p][h]
+ *   q          [num_tokens][num_heads][head_size + rope_size], strided
+ *   k_nope, v  [num_kv_tokens][num_heads][head_size], strided;  k_rope [num_kv_tokens][rope_size]
+ *   out        [num_tokens][num_heads][head_size], contiguous
+ *   query_start_loc, kv_start_loc  device int32 [num_seqs + 1], 0-based, nondecreasing, ending
+ *              at num_tokens and at num_kv_tokens
+ *   max_query_len, max_kv_len  host upper bounds of L and S
+ * Pointers are 16-byte aligned, strides multiples of 16 bytes.  Requests with L < 1,
+ * L > S or above a bound set PA_DEV_LENGTHS and their rows are left unwritten; bad start arrays
+ * set PA_DEV_QSL and nothing is written.  No workspace.  Rounding, NaN and early reads (of
+ * both start arrays) as for pa_latent_forward.
+ */
+int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                        const int32_t* query_start_loc, const int32_t* kv_start_loc, int num_seqs,
+                        int num_tokens, int num_kv_tokens, int max_query_len, int max_kv_len,
+                        float scale, void* out, const pa_expanded_layout* layout, int32_t* status,
+                        void* stream);
 
 /* Message of the last failing call on this thread ("" if none). */
 const char* pa_last_error(void);

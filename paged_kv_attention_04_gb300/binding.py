@@ -18,6 +18,8 @@ PA_F32, PA_BF16, PA_FP8_E4M3, PA_INT4 = 0, 1, 2, 3
 PA_INT4_LIMIT = 16384  # |x / scale| saturates here in a 4-bit cache
 PA_DEV_SLOT_RANGE, PA_DEV_BLOCK_RANGE, PA_DEV_QSL, PA_DEV_LENGTHS, PA_DEV_CAPACITY = 1, 2, 4, 8, 16
 PA_DEV_TIMEOUT = 32
+PA_DEV_POSITION = 64
+PA_ROPE_HALVES, PA_ROPE_PAIRS = 0, 1
 
 _DTYPES = {torch.float32: PA_F32, torch.bfloat16: PA_BF16}
 _ELEM_BYTES = {PA_F32: 4, PA_BF16: 2}
@@ -29,6 +31,24 @@ class pa_layout(ctypes.Structure):
                 ("num_blocks", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("cache_dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float)]
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("max_position", ctypes.c_int), ("rope_size", ctypes.c_int), ("style", ctypes.c_int)]
+
+
+class pa_latent_layout(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int), ("latent_size", ctypes.c_int),
+                ("rope_size", ctypes.c_int), ("block_size", ctypes.c_int),
+                ("num_blocks", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class pa_expanded_layout(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int), ("head_size", ctypes.c_int),
+                ("rope_size", ctypes.c_int), ("dtype", ctypes.c_int)] + [
+                    (n, ctypes.c_int64) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride",
+                                                  "kr_stride", "v_stride", "v_head_stride")]
 
 
 class PaError(RuntimeError):
@@ -54,6 +74,23 @@ def lib() -> ctypes.CDLL:
         L.pa_cache_write.restype = i32
         L.pa_cache_read.argtypes = [vp, vp, vp, i32, vp, vp, lp, vp, vp]
         L.pa_cache_read.restype = i32
+        i64, f32, rp = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(pa_rope)
+        llp, elp = ctypes.POINTER(pa_latent_layout), ctypes.POINTER(pa_expanded_layout)
+        L.pa_rope_cache_write.argtypes = [vp, i64, vp, i64, vp, i64, rp, vp, i32, vp, vp, vp, lp, vp, vp]
+        L.pa_rope_cache_write.restype = i32
+        L.pa_latent_write.argtypes = [vp, i64, vp, i64, vp, f32, vp, i64, i64, rp, vp, i32, vp, i64, i64,
+                                      vp, llp, vp, vp]
+        L.pa_latent_write.restype = i32
+        L.pa_latent_read.argtypes = [vp, vp, i32, vp, vp, llp, vp, vp]
+        L.pa_latent_read.restype = i32
+        L.pa_latent_workspace_size.argtypes = [llp, i32, i32, i32, i32]
+        L.pa_latent_workspace_size.restype = sz
+        L.pa_latent_forward.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, f32, vp, vp, sz, llp,
+                                        vp, vp]
+        L.pa_latent_forward.restype = i32
+        L.pa_expanded_forward.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, elp,
+                                          vp, vp]
+        L.pa_expanded_forward.restype = i32
         L.pa_forward_workspace_size.argtypes = [lp, i32, i32, i32]
         L.pa_forward_workspace_size.restype = sz
         L.pa_forward.argtypes = [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float,
@@ -89,17 +126,17 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _on_one_device(**tensors) -> int:
-    """Every tensor argument must be a contiguous CUDA tensor, all on one
-    device (a host pointer would reach the kernels unchecked).  Returns the
-    device's index."""
+def _on_one_device(strided=(), **tensors) -> int:
+    """Every tensor argument must be a CUDA tensor, contiguous unless its name is
+    in `strided`, all on one device (a host pointer would reach the kernels
+    unchecked).  Returns the device's index."""
     dev = None
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise PaError(PA_ERR_INVALID, f"{name} is not a CUDA tensor")
-        if not t.is_contiguous():
+        if name not in strided and not t.is_contiguous():
             raise PaError(PA_ERR_INVALID, f"{name} is not contiguous")
         d = t.get_device()
         if dev is None:
@@ -315,3 +352,231 @@ def alloc_workspace(layout: pa_layout, num_seqs: int, num_tokens: int, max_seq_l
     """Caller-owned workspace for pa_forward (torch's allocator aligns to >= 256 bytes)."""
     n = pa_forward_workspace_size(layout, num_seqs, num_tokens, max_seq_len)
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------- rotation and latent attention
+
+def _want(name: str, t, dtype, shape, strided: int | None = None) -> None:
+    """t must have this type and shape; with `strided`, its last `strided` dimensions
+    must lie side by side (the ones before may have any stride)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+    if strided is not None:
+        step = 1
+        for n, s in zip(reversed(t.shape[-strided:]), reversed(t.stride()[-strided:])):
+            if n != 1 and s != step:
+                raise PaError(PA_ERR_INVALID, f"{name}: its last {strided} dimensions must be contiguous, "
+                                              f"strides {t.stride()}")
+            step *= n
+
+
+def _torch_dtype(code: int):
+    return torch.float32 if code == PA_F32 else torch.bfloat16
+
+
+def _stride(t, dim: int, least: int) -> int:
+    """Stride of a dimension; of one that is never stepped over, one that passes."""
+    return t.stride(dim) if t.shape[dim] > 1 else least
+
+
+def _rope(positions, cos_sin, tokens: int, pairs: bool) -> pa_rope:
+    if positions.dtype != torch.int64:
+        raise PaError(PA_ERR_INVALID, f"positions is {positions.dtype}, expected torch.int64")
+    if positions.numel() < tokens:
+        raise PaError(PA_ERR_INVALID, f"{positions.numel()} positions for {tokens} tokens")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise PaError(PA_ERR_INVALID, f"cos_sin is {cos_sin.dtype} {tuple(cos_sin.shape)}, expected float32 "
+                                      "[max_position, rope_size]")
+    return pa_rope(positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                   PA_ROPE_PAIRS if pairs else PA_ROPE_HALVES)
+
+
+def _slots_for(slot_mapping, n: int) -> None:
+    _int64_slots(slot_mapping)
+    if slot_mapping.numel() < n:
+        raise PaError(PA_ERR_INVALID, f"{slot_mapping.numel()} slots for {n} tokens")
+
+
+def _cache_rows(layout: pa_layout, *caches) -> None:
+    """The caches of an unquantised or FP8 layout."""
+    want = torch.uint8 if layout.cache_dtype == PA_FP8_E4M3 else _torch_dtype(layout.dtype)
+    for c in caches:
+        if c.dtype != want or tuple(c.shape) != cache_shape(layout):
+            raise PaError(PA_ERR_INVALID, f"a cache is {c.dtype} {tuple(c.shape)}, expected {want} "
+                                          f"{cache_shape(layout)}")
+
+
+def pa_rope_cache_write(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
+                        layout: pa_layout, pairs: bool = False, status: torch.Tensor | None = None,
+                        stream=None) -> None:
+    """Rotate q [T, Hq, D] into q_out and k [T, Hkv, D] on its way into the caches, with v
+    as it is, at slot_mapping's slots (int64).  The first n = cos_sin.shape[1] dims
+    of a head are rotated by row positions[t] (int64) of cos_sin [max_position, n]
+    (float32: n / 2 cosines, then n / 2 sines), in pairs (x_i, x_(i + n/2)), or with
+    `pairs` (x_2i, x_(2i+1)).  q, k and v may be slices of one projection (any token
+    stride, heads contiguous); q_out may be q.  q and q_out None: only k and v."""
+    dev = _on_one_device(strided=("q", "k", "v"), q=q, k=k, v=v, positions=positions, cos_sin=cos_sin,
+                         slot_mapping=slot_mapping, q_out=q_out, k_cache=k_cache, v_cache=v_cache,
+                         status=status)
+    if layout.cache_dtype == PA_INT4:
+        _int4_pages(layout, k_cache, v_cache)
+    else:
+        _cache_rows(layout, k_cache, v_cache)
+    n, d, dt = k.shape[0], layout.head_size, _torch_dtype(layout.dtype)
+    kv = (n, layout.num_kv_heads, d)
+    _want("k", k, dt, kv, 2)
+    _want("v", v, dt, kv, 2)
+    if (q is None) != (q_out is None):
+        raise PaError(PA_ERR_INVALID, "q and q_out must both be given, or neither")
+    if q is not None:
+        _want("q", q, dt, (n, layout.num_q_heads, d), 2)
+        _want("q_out", q_out, dt, (n, layout.num_q_heads, d))
+    _slots_for(slot_mapping, n)
+    rope = _rope(positions, cos_sin, n, pairs)
+    q_row, kv_row = layout.num_q_heads * d, layout.num_kv_heads * d
+    _launch(lib().pa_rope_cache_write, dev, stream, _ptr(q), 0 if q is None else _stride(q, 0, q_row),
+            _ptr(k), _stride(k, 0, kv_row), _ptr(v), _stride(v, 0, kv_row), ctypes.byref(rope),
+            _ptr(slot_mapping), n, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), ctypes.byref(layout),
+            _ptr(status))
+
+
+def make_latent_layout(num_heads: int, latent_size: int, num_blocks: int, dtype=torch.bfloat16,
+                       rope_size: int = 64, block_size: int = 16) -> pa_latent_layout:
+    """Layout of a latent cache and the heads that attend over it."""
+    code = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return pa_latent_layout(num_heads, latent_size, rope_size, block_size, num_blocks, code)
+
+
+def latent_cache_shape(layout: pa_latent_layout) -> tuple:
+    """Shape of a latent cache: [num_blocks, block_size, latent_size + rope_size]."""
+    return (layout.num_blocks, layout.block_size, layout.latent_size + layout.rope_size)
+
+
+def latent_layout_of(cache: torch.Tensor, num_heads: int, rope_size: int = 64) -> pa_latent_layout:
+    """Layout of a latent cache tensor [num_blocks][block_size][latent_size + rope_size]."""
+    nb, bs, row = cache.shape
+    return make_latent_layout(num_heads, row - rope_size, nb, cache.dtype, rope_size, bs)
+
+
+def _latent_cache(layout: pa_latent_layout, cache) -> None:
+    _want("cache", cache, _torch_dtype(layout.dtype), latent_cache_shape(layout))
+
+
+def pa_latent_write(c, k_rope, q, positions, cos_sin, slot_mapping, q_out, cache,
+                    layout: pa_latent_layout, norm_weight=None, eps: float = 1e-6,
+                    pairs: bool = False, status: torch.Tensor | None = None, stream=None) -> None:
+    """Write [c[t], rotated k_rope[t]] into slot slot_mapping[t] (int64) of the latent cache and the
+    rotated q[t] (the heads' parts [T, H, rope_size] that meet the key part) into q_out.  With
+    norm_weight [latent_size], c is divided by its root mean square (eps inside the root) and
+    weighted first.  positions, cos_sin and pairs as for pa_rope_cache_write.  c [T, latent_size],
+    k_rope [T, rope_size], q and q_out may be slices (last dimension contiguous); q_out may be
+    q.  q and q_out None: only the cache is written."""
+    dev = _on_one_device(strided=("c", "k_rope", "q", "q_out"), c=c, k_rope=k_rope, q=q, positions=positions,
+                         cos_sin=cos_sin, slot_mapping=slot_mapping, q_out=q_out, cache=cache,
+                         norm_weight=norm_weight, status=status)
+    _latent_cache(layout, cache)
+    n, dt, rs = c.shape[0], _torch_dtype(layout.dtype), layout.rope_size
+    _want("c", c, dt, (n, layout.latent_size), 1)
+    _want("k_rope", k_rope, dt, (n, rs), 1)
+    if norm_weight is not None:
+        _want("norm_weight", norm_weight, dt, (layout.latent_size,))
+    if (q is None) != (q_out is None):
+        raise PaError(PA_ERR_INVALID, "q and q_out must both be given, or neither")
+    strides = [0] * 4
+    if q is not None:
+        for i, (name, t) in enumerate((("q", q), ("q_out", q_out))):
+            _want(name, t, dt, (n, layout.num_heads, rs), 1)
+            strides[2 * i + 1] = _stride(t, 1, rs)
+            strides[2 * i] = _stride(t, 0, strides[2 * i + 1] * layout.num_heads)
+    _slots_for(slot_mapping, n)
+    rope = _rope(positions, cos_sin, n, pairs)
+    _launch(lib().pa_latent_write, dev, stream, _ptr(c), _stride(c, 0, layout.latent_size), _ptr(k_rope),
+            _stride(k_rope, 0, rs), _ptr(norm_weight), float(eps), _ptr(q), strides[0], strides[1],
+            ctypes.byref(rope), _ptr(slot_mapping), n, _ptr(q_out), strides[2], strides[3], _ptr(cache),
+            ctypes.byref(layout), _ptr(status))
+
+
+def pa_latent_read(cache, slot_mapping, c, k_rope, layout: pa_latent_layout,
+                   status: torch.Tensor | None = None, stream=None) -> None:
+    """Read slot slot_mapping[t] of the latent cache into c[t], k_rope[t] (in place)."""
+    dev = _on_one_device(cache=cache, slot_mapping=slot_mapping, c=c, k_rope=k_rope, status=status)
+    _latent_cache(layout, cache)
+    _int64_slots(slot_mapping)
+    n, dt = slot_mapping.shape[0], _torch_dtype(layout.dtype)
+    _want("c", c, dt, (n, layout.latent_size))
+    _want("k_rope", k_rope, dt, (n, layout.rope_size))
+    _launch(lib().pa_latent_read, dev, stream, _ptr(cache), _ptr(slot_mapping), n, _ptr(c), _ptr(k_rope),
+            ctypes.byref(layout), _ptr(status))
+
+
+def pa_latent_workspace_size(layout: pa_latent_layout, num_seqs: int, num_tokens: int,
+                             max_query_len: int, max_seq_len: int) -> int:
+    n = lib().pa_latent_workspace_size(ctypes.byref(layout), int(num_seqs), int(num_tokens),
+                                       int(max_query_len), int(max_seq_len))
+    if n == 0:
+        raise PaError(PA_ERR_INVALID, last_error())
+    return int(n)
+
+
+def alloc_latent_workspace(layout: pa_latent_layout, num_seqs: int, num_tokens: int,
+                           max_query_len: int, max_seq_len: int, device="cuda") -> torch.Tensor:
+    """Caller-owned workspace for pa_latent_forward."""
+    n = pa_latent_workspace_size(layout, num_seqs, num_tokens, max_query_len, max_seq_len)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _int32(**arrays) -> None:
+    for name, t in arrays.items():
+        if t.dtype != torch.int32:
+            raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype}, expected torch.int32")
+
+
+def pa_latent_forward(q, cache, block_tables, seq_lens, query_start_loc, max_query_len: int,
+                      max_seq_len: int, scale: float, out, workspace, layout: pa_latent_layout,
+                      status: torch.Tensor | None = None, stream=None) -> None:
+    """Attention over a latent cache (absorbed form): q [T, H, latent_size + rope_size], out
+    [T, H, latent_size], the rest as for pa_forward."""
+    dev = _on_one_device(q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens,
+                         query_start_loc=query_start_loc, out=out, workspace=workspace, status=status)
+    _latent_cache(layout, cache)
+    _int32(block_tables=block_tables, seq_lens=seq_lens, query_start_loc=query_start_loc)
+    n, b, dt = q.shape[0], seq_lens.shape[0], _torch_dtype(layout.dtype)
+    _want("q", q, dt, (n, layout.num_heads, layout.latent_size + layout.rope_size))
+    _want("out", out, dt, (n, layout.num_heads, layout.latent_size))
+    if query_start_loc.numel() != b + 1 or block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise PaError(PA_ERR_INVALID, f"{b} requests, but query_start_loc {tuple(query_start_loc.shape)} and "
+                                      f"block_tables {tuple(block_tables.shape)}")
+    _launch(lib().pa_latent_forward, dev, stream, _ptr(q), _ptr(cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(seq_lens), _ptr(query_start_loc), b, n, int(max_query_len),
+            int(max_seq_len), float(scale), _ptr(out), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), ctypes.byref(layout), _ptr(status))
+
+
+def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max_query_len: int,
+                        max_kv_len: int, scale: float, out, status: torch.Tensor | None = None,
+                        stream=None) -> None:
+    """Attention in the expanded form: q [T, H, D + 64] against the keys [k_nope [Tk, H, D], k_rope
+    [Tk, 64] (shared by the heads)] and values v [Tk, H, D] of ragged requests, causal
+    from the bottom right; out [T, H, D].  q, k_nope, k_rope and v may be slices (last
+    dimension contiguous)."""
+    dev = _on_one_device(strided=("q", "k_nope", "k_rope", "v"), q=q, k_nope=k_nope, k_rope=k_rope, v=v,
+                         query_start_loc=query_start_loc, kv_start_loc=kv_start_loc, out=out, status=status)
+    _int32(query_start_loc=query_start_loc, kv_start_loc=kv_start_loc)
+    if q.dim() != 3 or k_nope.dim() != 3 or q.dtype not in _DTYPES:
+        raise PaError(PA_ERR_INVALID, f"q is {q.dtype} {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}: expected "
+                                      "[tokens, heads, size] of float32 or bfloat16")
+    (n, h, _), (tk, _, d), b = q.shape, k_nope.shape, query_start_loc.numel() - 1
+    rs = k_rope.shape[-1]
+    _want("q", q, q.dtype, (n, h, d + rs), 1)
+    _want("k_nope", k_nope, q.dtype, (tk, h, d), 1)
+    _want("k_rope", k_rope, q.dtype, (tk, rs), 1)
+    _want("v", v, q.dtype, (tk, h, d), 1)
+    _want("out", out, q.dtype, (n, h, d))
+    if b < 0 or kv_start_loc.numel() != b + 1:
+        raise PaError(PA_ERR_INVALID, f"query_start_loc has {b + 1} entries, kv_start_loc {kv_start_loc.numel()}")
+    layout = pa_expanded_layout(h, d, rs, _DTYPES[q.dtype], _stride(q, 0, h * (d + rs)), _stride(q, 1, d + rs),
+                                _stride(k_nope, 0, h * d), _stride(k_nope, 1, d), _stride(k_rope, 0, rs),
+                                _stride(v, 0, h * d), _stride(v, 1, d))
+    _launch(lib().pa_expanded_forward, dev, stream, _ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v),
+            _ptr(query_start_loc), _ptr(kv_start_loc), b, n, tk, int(max_query_len), int(max_kv_len),
+            float(scale), _ptr(out), ctypes.byref(layout), _ptr(status))

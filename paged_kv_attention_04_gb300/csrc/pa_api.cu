@@ -219,6 +219,21 @@ int set_last_error(int code, const char* msg) {
   return code;
 }
 
+int sms_of_current_device(int* out) { return num_sms_of_current_device(out); }
+
+int check_rope(const pa_rope* r) {
+  if (!r) return fail(PA_ERR_INVALID, "rope is NULL");
+  if (r->style != PA_ROPE_HALVES && r->style != PA_ROPE_PAIRS)
+    return fail(PA_ERR_INVALID, "rope style %d", static_cast<int>(r->style));
+  if (r->rope_size <= 0 || r->rope_size % 16)
+    return fail(PA_ERR_INVALID, "rope_size %d is not a positive multiple of 16", r->rope_size);
+  if (r->max_position <= 0) return fail(PA_ERR_INVALID, "max_position %d < 1", r->max_position);
+  if (!r->positions || !r->cos_sin) return fail(PA_ERR_INVALID, "null positions or cos_sin");
+  if (!aligned(r->positions, 8) || !aligned(r->cos_sin, 16))
+    return fail(PA_ERR_INVALID, "positions must be 8-byte and cos_sin 16-byte aligned");
+  return PA_OK;
+}
+
 WsLayout ws_layout(const Capacity& cap, int Hkv, int D, int group, int small_rows) {
   WsLayout w{};
   size_t off = 0;
@@ -257,7 +272,7 @@ extern "C" {
 
 const char* pa_last_error(void) { return g_last_error.c_str(); }
 
-int pa_version(void) { return 300; }
+int pa_version(void) { return 400; }
 
 int pa_set_profile_events(void* start, void* stop) {
   g_prof_start = static_cast<cudaEvent_t>(start);
@@ -302,6 +317,37 @@ int pa_cache_write(const void* k, const void* v, const int64_t* slot_mapping, in
                                            static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e, "cache write launch");
   return PA_OK;
+}
+
+int pa_rope_cache_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const pa_rope* rope,
+                        const int64_t* slot_mapping, int num_tokens, void* q_out, void* k_cache,
+                        void* v_cache, const pa_layout* layout, int32_t* status, void* stream) {
+  g_last_error.clear();
+  if (int rc = check_layout(layout)) return rc;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID, "num_tokens %d < 0", num_tokens);
+  if (num_tokens == 0) return PA_OK;
+  if (int rc = check_rope(rope)) return rc;
+  if (rope->rope_size > layout->head_size)
+    return fail(PA_ERR_INVALID, "rope_size %d > head_size %d", rope->rope_size, layout->head_size);
+  if (int rc = check_slot_call(k, v, slot_mapping, k_cache, v_cache, status)) return rc;
+  if (!q != !q_out) return fail(PA_ERR_INVALID, "q and q_out must both be given, or neither");
+  if (!aligned(q, 16) || !aligned(q_out, 16)) return fail(PA_ERR_INVALID, "q and q_out must be 16-byte aligned");
+  const int64_t unit = 16 / elem_bytes(layout->dtype);
+  const int64_t q_row = static_cast<int64_t>(layout->num_q_heads) * layout->head_size;
+  const int64_t kv_row = static_cast<int64_t>(layout->num_kv_heads) * layout->head_size;
+  if ((q && q_stride % unit) || k_stride % unit || v_stride % unit)
+    return fail(PA_ERR_INVALID, "token strides must be multiples of 16 bytes");
+  if ((q && q_stride < q_row) || k_stride < kv_row || v_stride < kv_row)
+    return fail(PA_ERR_INVALID, "a token stride is smaller than the token's heads");
+  if (q && q == q_out && q_stride != q_row)
+    return fail(PA_ERR_INVALID, "q_out may be q only where q is contiguous");
+  if (static_cast<long long>(num_tokens) * (layout->num_q_heads + 2LL * layout->num_kv_heads) > 0x7fffffffLL)
+    return fail(PA_ERR_INVALID, "too many rows for one call");
+  const RopeWriteArgs a{q, k, v, q_stride, k_stride, v_stride, rope, slot_mapping, num_tokens,
+                        q_out, k_cache, v_cache, status};
+  const cudaError_t e = launch_rope_write(a, *layout, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? static_cast<int>(PA_OK) : fail_cuda(e, "rotating cache write launch");
 }
 
 int pa_cache_read(const void* k_cache, const void* v_cache, const int64_t* slot_mapping,

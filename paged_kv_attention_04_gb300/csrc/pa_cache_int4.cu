@@ -27,6 +27,7 @@
 #include "pa_device.cuh"
 #include "pa_int4.cuh"
 #include "pa_internal.h"
+#include "pa_rope.cuh"
 
 namespace pa {
 
@@ -177,16 +178,60 @@ struct Place {
   }
 };
 
-template <int D>
+// What the rotating write adds: the rotation, and token strides of k and v (in 16-byte words).
+struct Turned {
+  RopeParams rope;
+  long long k_stride, v_stride;
+};
+
+// 8 dims from d of a row of k, rotated by the table row: each lane loads the
+// group that holds the partners of its own too.
+__device__ __forceinline__ uint4 load_turned(const uint4* row, int d, const float* table,
+                                             const RopeParams& r) {
+  Eight<__nv_bfloat16> own, other;
+  own.w = __ldg(row + d / 8);
+  if (d >= r.size) return own.w;
+  const int half = r.size / 2;
+  if (r.pairs) {
+    // (the group's four pairs: the lower or upper half of the 16 numbers of thread d / 16)
+    float x[8], c[8], s[8];
+    own.get(x);
+    load8(table + (d / 16) * 8, c);
+    load8(table + half + (d / 16) * 8, s);
+    const bool up = (d / 8) & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], up ? c[4 + i] : c[i], up ? s[4 + i] : s[i]);
+    own.set(x);
+    return own.w;
+  }
+  const bool up = d >= half;
+  other.w = __ldg(row + (up ? d - half : d + half) / 8);
+  const int j = (up ? d - half : d) / 8;
+  if (up) {
+    rope_turn(other, own, table, j, r.size, false);
+  } else {
+    rope_turn(own, other, table, j, r.size, false);
+  }
+  return own.w;
+}
+
+// TURN: k is rotated as it is read.
+template <int D, bool TURN>
 __global__ void __launch_bounds__(kThreads) cache_write_int4_kernel(
     const uint4* __restrict__ k, const uint4* __restrict__ v, const int64_t* __restrict__ slots,
     int num_tokens, unsigned char* __restrict__ k_cache, unsigned char* __restrict__ v_cache,
-    int num_kv_heads, long long num_slots, TensorScale ks, TensorScale vs, int32_t* status) {
+    int num_kv_heads, long long num_slots, TensorScale ks, TensorScale vs, int32_t* status,
+    const Turned turned) {
   using Pg = I4Page<D>;
   using Pl = Place<D>;
   launch_dependents();  // a following plan kernel may start; it waits for this grid
   const Pl at;
   int64_t s = at.token < num_tokens ? __ldg(slots + at.token) : -1;
+  const float* table = nullptr;
+  if constexpr (TURN) {
+    if (at.token < num_tokens) table = rope_row(turned.rope, static_cast<int>(at.token), at.d == 0, status);
+    if (!table) s = -1;
+  }
   if (s >= num_slots) {
     if (at.d == 0) flag_error(status, PA_DEV_SLOT_RANGE);
     s = -1;
@@ -197,12 +242,13 @@ __global__ void __launch_bounds__(kThreads) cache_write_int4_kernel(
   const bool joined = s >= 0 && (s & 1) == odd && other == s + (odd ? -1 : 1);
   const int row = static_cast<int>(s & (kBlockSize - 1)), g = at.d / 32;
   const int step = gridDim.y * Pl::kHeads;
-  const uint4* kr = k + at.token * num_kv_heads * Pl::kLanes + at.d / 8;
-  const uint4* vr = v + at.token * num_kv_heads * Pl::kLanes + at.d / 8;
+  const uint4* kr = k + at.token * (TURN ? turned.k_stride : num_kv_heads * Pl::kLanes) + (TURN ? 0 : at.d / 8);
+  const uint4* vr = v + at.token * (TURN ? turned.v_stride : num_kv_heads * Pl::kLanes) + at.d / 8;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   auto load = [&](int head, uint4& kw, uint4& vw) {
     const bool ok = s >= 0 && head < num_kv_heads;
-    kw = ok ? __ldg(kr + head * Pl::kLanes) : zero;
+    if constexpr (TURN) kw = ok ? load_turned(kr + head * Pl::kLanes, at.d, table, turned.rope) : zero;
+    else kw = ok ? __ldg(kr + head * Pl::kLanes) : zero;
     vw = ok ? __ldg(vr + head * Pl::kLanes) : zero;
   };
   uint4 kw, vw, kw1, vw1;  // this head's values, the next one's
@@ -308,10 +354,23 @@ cudaError_t launch_cache_write_int4(const void* k, const void* v, const int64_t*
     kernel<<<grid_for(num_tokens, num_kv_heads, head_size), kThreads, 0, stream>>>(
         static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping, num_tokens,
         static_cast<unsigned char*>(k_cache), static_cast<unsigned char*>(v_cache), num_kv_heads,
-        num_slots, tensor_scale(k_scale), tensor_scale(v_scale), status);
+        num_slots, tensor_scale(k_scale), tensor_scale(v_scale), status, Turned{});
     return cudaGetLastError();
   };
-  return head_size == 64 ? go(cache_write_int4_kernel<64>) : go(cache_write_int4_kernel<128>);
+  return head_size == 64 ? go(cache_write_int4_kernel<64, false>) : go(cache_write_int4_kernel<128, false>);
+}
+
+cudaError_t launch_rope_write_int4(const RopeWriteArgs& a, const pa_layout& L, cudaStream_t stream) {
+  const Turned turned{rope_params(a.rope), a.k_stride / 8, a.v_stride / 8};
+  auto go = [&](auto kernel) {
+    kernel<<<grid_for(a.num_tokens, L.num_kv_heads, L.head_size), kThreads, 0, stream>>>(
+        static_cast<const uint4*>(a.k), static_cast<const uint4*>(a.v), a.slots, a.num_tokens,
+        static_cast<unsigned char*>(a.k_cache), static_cast<unsigned char*>(a.v_cache),
+        L.num_kv_heads, static_cast<long long>(L.num_blocks) * kBlockSize, tensor_scale(L.k_scale),
+        tensor_scale(L.v_scale), a.status, turned);
+    return cudaGetLastError();
+  };
+  return L.head_size == 64 ? go(cache_write_int4_kernel<64, true>) : go(cache_write_int4_kernel<128, true>);
 }
 
 cudaError_t launch_cache_read_int4(const void* k_cache, const void* v_cache,

@@ -143,6 +143,9 @@ struct AttnParams {
 
 // Sets the message pa_last_error() returns on this thread; returns code.
 int set_last_error(int code, const char* msg);
+// PA_OK, or an error that pa_last_error() describes.
+int sms_of_current_device(int* out);
+int check_rope(const pa_rope* r);
 
 // Workspace regions for a step with capacity cap (see pa_forward_workspace_size).
 WsLayout ws_layout(const Capacity& cap, int num_kv_heads, int head_size, int group, int small_rows);
@@ -161,6 +164,19 @@ cudaError_t launch_cache_write_int4(const void* k, const void* v, const int64_t*
                                     int num_tokens, void* k_cache, void* v_cache, int num_kv_heads,
                                     int head_size, long long num_slots, float k_scale,
                                     float v_scale, int32_t* status, cudaStream_t stream);
+// The slot write with the position rotation on the way (strides in elements).
+struct RopeWriteArgs {
+  const void *q, *k, *v;  // q null: k and v only
+  long long q_stride, k_stride, v_stride;
+  const pa_rope* rope;
+  const int64_t* slots;
+  int num_tokens;
+  void *q_out, *k_cache, *v_cache;
+  int32_t* status;
+};
+cudaError_t launch_rope_write(const RopeWriteArgs& a, const pa_layout& L, cudaStream_t stream);
+// ... its k and v for a 4-bit cache.
+cudaError_t launch_rope_write_int4(const RopeWriteArgs& a, const pa_layout& L, cudaStream_t stream);
 // Read-back of slots: by copy (row_bytes a cache row), from an FP8 cache
 // (row_bytes the bf16 row) and from a 4-bit cache.
 cudaError_t launch_cache_read(const void* k_cache, const void* v_cache, const int64_t* slot_mapping,

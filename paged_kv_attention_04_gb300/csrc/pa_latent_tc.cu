@@ -1,0 +1,791 @@
+// Attention over a latent cache (absorbed form) on the 5th-generation tensor cores.
+//
+// All heads of a token read the same row [L, K] of a key (R + 64 numbers, 1152 bytes at
+// R = 512), whose first R numbers are the value too: 2 (2 R + 64) flops per head and key
+// on 2 (R + 64) bytes, 60 flop/byte at 32 heads, so decode is bound by HBM up to about 128 query
+// rows a key.  Every key is staged once and used for both products.
+//
+// The products are taken transposed, with the keys as M, so that few query rows do not
+// pad a tile to 128 rows: S' = [L, K] q' (M = 64 keys, N rows, K = R + 64) and
+// O' += L' P' (M = 128 numbers of the latent, R / 128 of them, N rows, K = 64 keys).  N is
+// 16, 32 or 64 query rows, a row being a (token, head) of a request.  O' takes R / 128 x N
+// columns of tensor memory: 64 rows of 512 are half of it.
+// The 64-key tile lies in shared memory as four 16-token pages, each one TMA box:
+//   [8-key group][64-number slice][8 keys][128 bytes], 128-byte swizzle.
+// Read with the keys as rows (K-major) it is A of the first product, with the numbers
+// as rows (MN-major) A of the second, so there is one copy of it.
+//
+// Roles: warps 0-3 softmax and output, warp 4 units and copies, warp 5 MMA issue.
+// S' has a key per TMEM lane (16 of every 32) and is read as matrix fragments: column maxima by
+// shuffles over lanes and a trade between the four warps in shared memory.  The reference
+// of a column moves only when its maximum grows by more than 2^8; P is written transposed
+// to shared memory by stmatrix as B of the second product.
+//
+// Work: units (request, N rows) lie on a line, each as long as its keys' tiles plus a
+// constant; every CTA takes an equal stretch, computed by itself from the lengths.  Units
+// cut by a border leave partial states (at most two a CTA) that a second kernel joins in order.
+#include <math_constants.h>
+
+#include "pa_latent.h"
+#include "pa_tc_util.cuh"
+
+namespace pa {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kKeys = 64;           // keys of a tile
+constexpr int kPages = kKeys / kBlockSize;
+constexpr int kCopyWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kSoftThreads = 128;
+constexpr float kGrowth = 8.f;      // base-2 growth of a maximum that moves the reference
+constexpr int kUnitCost = 2;        // what a unit costs beside its tiles, in tiles
+constexpr uint32_t kPollLimit = 1u << 26;
+constexpr int kMinStretch = 4;      // shortest stretch of the line for a CTA
+
+template <int R, int N>
+struct Cfg {
+  static constexpr int kSlices = (R + kLatentRope) / 64;
+  static constexpr int kGroupBytes = kSlices * 1024;       // 8 keys
+  static constexpr int kPageBytes = 2 * kGroupBytes;
+  static constexpr int kTileBytes = kPages * kPageBytes;
+  static constexpr int kQBytes = N * (R + kLatentRope) * 2;  // [slice][N rows][128 bytes]
+  static constexpr int kPBytes = N * kKeys * 2;              // [N rows][128 bytes]
+  static constexpr bool kTight = R == 512 && N == 64;
+  static constexpr int kBufs = R == 512 ? 2 : 4;   // tiles
+  static constexpr int kQs = N == 64 ? 1 : 2;
+  static constexpr int kPs = kTight ? 1 : 2;
+  static constexpr int kQOff = kBufs * kTileBytes;
+  static constexpr int kPOff = kQOff + kQs * kQBytes;
+  static constexpr int kSmallOff = kPOff + kPs * kPBytes;
+  static constexpr int kSmemBytes = kSmallOff + 3072;
+  static constexpr int kBlocks = R / 128;          // of 128 latent numbers
+  static constexpr int kTmemS = 256;               // S of even and odd tiles behind O
+  static_assert(kBlocks * N <= 256, "O fits beside S");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
+};
+
+struct Unit {
+  int r;        // request; < 0: no more units
+  int row0;     // first row of q and out
+  int rows;     // rows of the unit
+  int first;    // first row's index in the request (token x heads + head)
+  int prior;    // S - L
+  int seq;      // S
+  int t0, n;    // key tiles
+  int slot;     // partial state, -1: the whole unit
+};
+
+enum Bar : int {
+  kUnitFull = 0,   // [2]
+  kUnitEmpty = 2,  // [2] (4 softmax warps, MMA)
+  kQFull = 4,      // [2] TMA
+  kQEmpty = 6,     // [2] the unit's last S done
+  kKFull = 8,      // [4] TMA
+  kKEmpty = 12,    // [4] O += of the tile done: frees the tile and its P
+  kSFull = 16,     // [2] S done
+  kPFull = 18,     // [2] S read, P written, O rescaled (4 warps)
+  kTrade = 20,     // the softmax warps meet (4 warps)
+  kDrain = 21,
+  kNumBars = 22
+};
+
+struct Small {
+  uint64_t bars[kNumBars];
+  Unit units[2];
+  float mx[2][4][64];   // per warp: column maxima, by tile parity (and row sums)
+  float f[64];          // factors of a moved reference; 1 / sum
+  uint32_t tmem;
+  int abort;
+  int start_r;
+  int bad;
+  long long start_pos, total;
+};
+static_assert(sizeof(Small) <= 3072, "small shared memory");
+
+// The line: what request r (rows a .. a + L - 1 of the step, S keys) takes of it.
+struct Span {
+  int a, L, S, units, len;  // units of this way, each len long
+};
+
+struct Shape {
+  int ways, way;     // a request's row tiles are dealt to `ways` CTAs that read the same keys
+  int groups, group; // stretches of the line
+};
+
+template <int N>
+__device__ __forceinline__ int span_of(const LatentParams& p, const Shape& sh, int r, Span& s) {
+  s.a = __ldg(p.qsl + r);
+  const int b = __ldg(p.qsl + r + 1);
+  s.S = __ldg(p.seq_lens + r);
+  s.L = b - s.a;
+  s.units = s.len = 0;
+  if (s.L < 0 || s.a < 0 || b > p.num_tokens || (r == 0 && s.a != 0) ||
+      (r == p.num_seqs - 1 && b != p.num_tokens))
+    return PA_DEV_QSL;
+  if (s.L < 1 || s.L > s.S || s.S > p.max_seq_len || s.L > p.max_query_len) return PA_DEV_LENGTHS;
+  const int tiles = static_cast<int>((static_cast<long long>(s.L) * p.num_heads + N - 1) / N);
+  s.units = (tiles + sh.ways - 1) / sh.ways;
+  s.len = (s.S + kKeys - 1) / kKeys + kUnitCost;
+  return 0;
+}
+
+// The stretch that position x of the line belongs to.
+__device__ __forceinline__ int group_of(long long x, long long total, int groups) {
+  return static_cast<int>(((x + 1) * groups - 1) / total);
+}
+
+}  // namespace
+
+template <int R, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_tc_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kmap, const int ways) {
+  using C = Cfg<R, N>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Small& sm = *reinterpret_cast<Small*>(smem + C::kSmallOff);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &sm.abort;
+  auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t n = 1;
+      if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 5;
+      if (i == kPFull || i == kPFull + 1 || i == kTrade) n = 4;
+      mbar_init(bar(i), n);
+    }
+    // (the swizzled tiles need the alignment that the declaration asks for)
+    sm.abort = (sbase & 1023) != 0;
+    if (sbase & 1023) flag_error(p.status, PA_DEV_TIMEOUT);
+    sm.bad = 0;
+    sm.start_r = -1;
+    mbar_fence_init();
+  }
+  if (warp == 0) tmem_alloc(smem_u32(&sm.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  // ---- this CTA's stretch of the line: [lo, hi), beginning in request start_r
+  Shape sh;
+  sh.ways = ways;
+  sh.way = blockIdx.x % ways;
+  sh.group = blockIdx.x / ways;
+  sh.groups = gridDim.x / ways;
+  long long lo = 0, hi = 0, total = 0;
+  {
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int ra = min(tid * per, p.num_seqs), rb = min(ra + per, p.num_seqs);
+    long long mine = 0;
+    int err = 0;
+    for (int r = ra; r < rb; ++r) {
+      Span s;
+      err |= span_of<N>(p, sh, r, s);
+      mine += static_cast<long long>(s.units) * s.len;
+    }
+    if (err) {
+      if (blockIdx.x == 0) flag_error(p.status, err);
+      if (err & PA_DEV_QSL) sm.bad = 1;
+    }
+    long long before = mine;  // inclusive scan over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    long long* sums = reinterpret_cast<long long*>(&sm.mx[0][0][0]);
+    if (lane == 31) sums[warp] = before;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    before -= mine;
+    if (sm.bad) total = 0;
+    const long long most = total / kMinStretch;
+    sh.groups = static_cast<int>(min(static_cast<long long>(sh.groups), most < 1 ? 1 : most));
+    if (sh.group < sh.groups) {
+      lo = total * sh.group / sh.groups;
+      hi = total * (sh.group + 1) / sh.groups;
+    }
+    if (lo < hi && before <= lo && lo < before + mine) {
+      long long pos = before;
+      for (int r = ra; r < rb; ++r) {
+        Span s;
+        span_of<N>(p, sh, r, s);
+        const long long len = static_cast<long long>(s.units) * s.len;
+        if (lo < pos + len) {
+          sm.start_r = r;
+          sm.start_pos = pos;
+          break;
+        }
+        pos += len;
+      }
+    }
+    __syncthreads();
+  }
+  wait_prior_grid();
+
+  if (warp == kCopyWarp) {
+    // ------------------------------------------------------------ units and copies
+    if (lane == 0) p.recs[blockIdx.x * kLatentRecWords + 3] = 0;
+    int uc = 0;        // units published
+    uint32_t g = 0;    // tiles copied
+    bool ok = !*abort;
+    auto publish = [&](const Unit& u) {
+      const int slot = uc & 1;
+      if (uc >= 2 && !wait_bar(bar(kUnitEmpty + slot), ((uc >> 1) - 1) & 1, abort, p.status)) return false;
+      if (lane == 0) {
+        sm.units[slot] = u;
+        mbar_arrive(bar(kUnitFull + slot));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto run = [&](const Unit& u) {
+      if (!publish(u)) return false;
+      const int qs = uc % C::kQs;
+      if (uc >= C::kQs && !wait_bar(bar(kQEmpty + qs), (uc / C::kQs - 1) & 1, abort, p.status)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(bar(kQFull + qs), C::kQBytes);
+      __syncwarp();
+      if (lane < C::kSlices)
+        tma_load_2d(sbase + C::kQOff + qs * C::kQBytes + lane * N * 128, &qmap, lane * 64, u.row0,
+                    bar(kQFull + qs));
+      ++uc;
+      const int32_t* table = p.block_tables + static_cast<long long>(u.r) * p.max_blocks_per_seq;
+      auto entry = [&](int t) {  // block of page `lane` of tile t, -1 past the request's keys
+        const int b = t * kPages + lane;
+        return lane < kPages && b * kBlockSize < u.seq ? __ldg(table + b) : -1;
+      };
+      int ph = entry(u.t0);
+      for (int t = 0; t < u.n; ++t, ++g) {
+        const int b = g % C::kBufs;
+        int cur = ph;
+        if (t + 1 < u.n) ph = entry(u.t0 + t + 1);
+        if (g >= C::kBufs && !wait_bar(bar(kKEmpty + b), (g / C::kBufs - 1) & 1, abort, p.status)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + b), C::kTileBytes);
+        __syncwarp();
+        if (lane < kPages) {
+          // a page past the keys or with a bad table entry is read out of bounds: zeros
+          if (cur < 0 || cur >= p.num_blocks) {
+            if (((u.t0 + t) * kPages + lane) * kBlockSize < u.seq) flag_error(p.status, PA_DEV_BLOCK_RANGE);
+            cur = p.num_blocks;
+          }
+          tma_load_5d(sbase + b * C::kTileBytes + lane * C::kPageBytes, &kmap, 0, 0, 0, 0, cur, bar(kKFull + b));
+        }
+      }
+      return true;
+    };
+    if (ok && sm.start_r >= 0) {
+      long long pos = sm.start_pos;
+      for (int r = sm.start_r; ok && r < p.num_seqs && pos < hi; ++r) {
+        Span s;
+        span_of<N>(p, sh, r, s);
+        const long long skip = s.len && lo > pos ? (lo - pos) / s.len : 0;
+        for (int j = static_cast<int>(skip); ok && j < s.units; ++j) {
+          const long long ua = pos + static_cast<long long>(j) * s.len;
+          if (ua >= hi) break;
+          const long long m = static_cast<long long>(j) * sh.ways + sh.way;
+          const long long first = m * N;
+          const long long rows = static_cast<long long>(s.L) * p.num_heads - first;
+          if (rows <= 0) continue;
+          Unit u;
+          u.r = r;
+          u.rows = static_cast<int>(min(rows, static_cast<long long>(N)));
+          u.first = static_cast<int>(first);
+          u.row0 = static_cast<int>(static_cast<long long>(s.a) * p.num_heads + first);
+          u.prior = s.S - s.L;
+          u.seq = s.S;
+          // tiles that some row of the unit sees
+          const int seen = u.prior + (u.first + u.rows - 1) / p.num_heads + 1;
+          const int nk = (seen + kKeys - 1) / kKeys;
+          const long long f = ua + kUnitCost;  // the first tile's place
+          u.t0 = static_cast<int>(max(0LL, lo - f));
+          const int t1 = static_cast<int>(min(static_cast<long long>(nk), hi - f));
+          if (u.t0 >= t1) continue;
+          u.n = t1 - u.t0;
+          u.slot = u.n == nk ? -1 : static_cast<int>(blockIdx.x) * 2 + (u.t0 == 0);
+          if (u.slot >= 0 && u.t0 == 0 && lane == 0) {
+            int* rec = p.recs + blockIdx.x * kLatentRecWords;
+            rec[0] = u.row0;
+            rec[1] = u.rows;
+            rec[2] = ways;
+            rec[3] = group_of(f + nk - 1, total, sh.groups) - sh.group + 1;
+          }
+          ok = run(u);
+        }
+        pos += static_cast<long long>(s.units) * s.len;
+      }
+    }
+    Unit end{};
+    end.r = -1;
+    if (ok) publish(end);
+    if (*abort) {  // let every copy issued land before the CTA ends
+      for (uint32_t i = g > C::kBufs ? g - C::kBufs : 0; i < g; ++i)
+        drain_wait(bar(kKFull + i % C::kBufs), (i / C::kBufs) & 1);
+      for (int i = uc > C::kQs ? uc - C::kQs : 0; i < uc; ++i)
+        drain_wait(bar(kQFull + i % C::kQs), (i / C::kQs) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t kIdS = idesc_bf16(kKeys, N, 0);
+    constexpr uint32_t kIdO = idesc_bf16(128, N, 0) | (1u << 15);  // A MN-major
+    const uint64_t dk = smem_desc_sw128(sbase, 16, C::kGroupBytes);
+    const uint64_t dv = smem_desc_sw128(sbase, 1024, C::kGroupBytes);
+    const uint64_t dq = smem_desc_sw128(sbase + C::kQOff, 16, 1024);
+    const uint64_t dp = smem_desc_sw128(sbase + C::kPOff, 16, 1024);
+    auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
+    auto ready = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
+    };
+    // S of the next tile and O += of the oldest are issued as what they need arrives, S at
+    // most one tile ahead (two S buffers): waiting for either would hold up the other.
+    int uc = -1;            // unit of the next S
+    int left = 0;           // its tiles without an S
+    bool fresh = false;     // its Q has not been waited for
+    bool ends = false;
+    uint32_t gs = 0, gp = 0;
+    uint32_t firsts = 0;    // bit g & 1: tile g is its unit's first
+    uint32_t idle = 0;      // polls without progress
+    while (!(ends && gp == gs)) {
+      bool moved = false;
+      if (!ends && gs - gp < 2) {
+        if (left == 0) {
+          const int slot = (uc + 1) & 1;
+          if (ready(bar(kUnitFull + slot), ((uc + 1) >> 1) & 1)) {
+            ++uc;
+            const int r = sm.units[slot].r;
+            left = sm.units[slot].n;
+            warp_arrive(bar(kUnitEmpty + slot));
+            if (r < 0) {
+              ends = true;
+              left = 0;
+            }
+            fresh = true;
+            moved = true;
+          }
+        } else if (ready(bar(kKFull + gs % C::kBufs), (gs / C::kBufs) & 1) &&
+                   (!fresh || ready(bar(kQFull + uc % C::kQs), (uc / C::kQs) & 1))) {
+          const uint32_t b = gs % C::kBufs;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t kb = adv(dk, b * C::kTileBytes), qb = adv(dq, (uc % C::kQs) * C::kQBytes);
+            const uint32_t d = tmem + C::kTmemS + (gs & 1) * N;
+#pragma unroll
+            for (int i = 0; i < C::kSlices * 4; ++i)
+              tc_mma_f16(d, adv(kb, (i >> 2) * 1024 + (i & 3) * 32), adv(qb, (i >> 2) * (N * 128) + (i & 3) * 32),
+                         kIdS, i > 0);
+            tc_commit(bar(kSFull + (gs & 1)));
+            if (left == 1) tc_commit(bar(kQEmpty + uc % C::kQs));
+          }
+          __syncwarp();
+          firsts = fresh ? firsts | (1u << (gs & 1)) : firsts & ~(1u << (gs & 1));
+          fresh = false;
+          --left;
+          ++gs;
+          moved = true;
+        }
+      }
+      if (gp < gs && ready(bar(kPFull + (gp & 1)), (gp >> 1) & 1)) {
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t b = gp % C::kBufs;
+          const uint64_t vb = adv(dv, b * C::kTileBytes), pb = adv(dp, (gp % C::kPs) * C::kPBytes);
+          const bool first = (firsts >> (gp & 1)) & 1;
+#pragma unroll
+          for (int pg = 0; pg < kPages; ++pg)
+#pragma unroll
+            for (int m = 0; m < C::kBlocks; ++m)
+              tc_mma_f16(tmem + m * N, adv(vb, pg * C::kPageBytes + m * 2048), adv(pb, pg * 32), kIdO,
+                         !first || pg > 0);
+          tc_commit(bar(kKEmpty + b));
+        }
+        __syncwarp();
+        ++gp;
+        moved = true;
+      }
+      idle = moved ? 0 : idle + 1;
+      if (__any_sync(0xffffffffu, *abort != 0)) break;
+      if (idle > kPollLimit) {
+        if (lane == 0) {
+          *abort = 1;
+          flag_error(p.status, PA_DEV_TIMEOUT);
+        }
+        __syncwarp();
+        break;
+      }
+    }
+    if (*abort) {  // nothing may still run on tensor memory when it is freed
+      if (lane == 0) tc_commit(bar(kDrain));
+      __syncwarp();
+      drain_wait(bar(kDrain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and output
+    constexpr int F = N / 8;  // column groups of a fragment
+    const int c0 = 2 * (lane & 3);
+    const int key0 = warp * 16 + (lane >> 2);
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t g = 0;
+    bool ok = !*abort;
+    // phase of tile i's "O += done"
+    auto wait_o = [&](uint32_t i) {
+      return wait_bar(bar(kKEmpty + i % C::kBufs), (i / C::kBufs) & 1, abort, p.status);
+    };
+    uint32_t trades = 0;
+    auto meet = [&]() {
+      warp_arrive(bar(kTrade));
+      return wait_bar(bar(kTrade), trades++ & 1, abort, p.status);
+    };
+    for (int uc = 0; ok; ++uc) {
+      if (!wait_bar(bar(kUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
+      const Unit u = sm.units[uc & 1];
+      warp_arrive(bar(kUnitEmpty + (uc & 1)));
+      if (u.r < 0) break;
+      float m[F][2], l[F][2];  // reference and this lane's part of the sum, by column
+#pragma unroll
+      for (int i = 0; i < F; ++i) m[i][0] = m[i][1] = -CUDART_INF_F, l[i][0] = l[i][1] = 0.f;
+      // keys up to here are seen by every row
+      const int low = u.prior + u.first / p.num_heads;
+      for (int t = 0; t < u.n; ++t, ++g) {
+        const int k0 = (u.t0 + t) * kKeys;
+        if (!wait_bar(bar(kSFull + (g & 1)), (g >> 1) & 1, abort, p.status)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t raw[F * 4];
+        tmem_ld_frag(tmem + C::kTmemS + (g & 1) * N + lanes, raw);
+        tmem_wait_ld();
+        float x[F][4];
+#pragma unroll
+        for (int i = 0; i < F * 4; ++i) x[i >> 2][i & 3] = __uint_as_float(raw[i]) * p.scale_log2;
+        if (k0 + kKeys - 1 > low) {
+          const int a = k0 + key0;
+#pragma unroll
+          for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int last = u.prior + (u.first + 8 * i + c0 + j) / p.num_heads;
+              if (a > last) x[i][j] = -CUDART_INF_F;
+              if (a + 8 > last) x[i][j + 2] = -CUDART_INF_F;
+            }
+          // slots behind the last key hold anything: zeros, so that a weight of zero meets no NaN
+          const int end = u.seq - k0;  // rows of the tile that hold keys
+          if (end < kKeys && (end & (kBlockSize - 1))) {
+            const uint32_t page = sbase + (g % C::kBufs) * C::kTileBytes + (end / kBlockSize) * C::kPageBytes;
+            const int r0 = end & (kBlockSize - 1);
+            constexpr int kPer = R / 8;
+            for (int i = tid; i < (kBlockSize - r0) * kPer; i += kSoftThreads) {
+              const int row = r0 + i / kPer, c = i % kPer;
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(
+                               page + (row >> 3) * C::kGroupBytes + (c >> 3) * 1024 + (row & 7) * 128 + (c & 7) * 16),
+                           "r"(0u)
+                           : "memory");
+            }
+          }
+        }
+        // column maxima: over the warp's 16 keys, then the four warps
+        float mx[F][2];
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float y = fmaxf(x[i][j], x[i][j + 2]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+            mx[i][j] = y;
+          }
+        if (lane < 4) {
+#pragma unroll
+          for (int i = 0; i < F; ++i)
+            *reinterpret_cast<float2*>(&sm.mx[g & 1][warp][8 * i + c0]) = make_float2(mx[i][0], mx[i][1]);
+        }
+        if (!meet()) { ok = false; break; }
+        bool moved = false;
+        float f[F][2];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          float2 y[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) y[w] = *reinterpret_cast<const float2*>(&sm.mx[g & 1][w][8 * i + c0]);
+          mx[i][0] = fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x));
+          mx[i][1] = fmaxf(fmaxf(y[0].y, y[1].y), fmaxf(y[2].y, y[3].y));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            f[i][j] = 1.f;
+            if (mx[i][j] > m[i][j] + kGrowth) {  // (also the first finite maximum: m = -inf)
+              f[i][j] = ex2(m[i][j] - mx[i][j]);
+              m[i][j] = mx[i][j];
+              l[i][j] *= f[i][j];
+              moved = true;
+            }
+          }
+        }
+        moved = __any_sync(0xffffffffu, moved);
+        // P and this lane's sums
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // (no key seen yet: every logit is -inf, every weight 0)
+            const float ref = m[i][j & 1] == -CUDART_INF_F ? 0.f : m[i][j & 1];
+            x[i][j] = ex2(x[i][j] - ref);
+            l[i][j & 1] += x[i][j];
+          }
+        // O' of earlier tiles takes the new references, once it is there
+        if (moved && t > 0) {
+          if (warp == 0 && lane < 4) {
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+              *reinterpret_cast<float2*>(&sm.f[8 * i + c0]) = make_float2(f[i][0], f[i][1]);
+          }
+          if (!meet() || !wait_o(g - 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < C::kBlocks * N; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tmem + lanes + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.f[(c & (N - 1)) + i]);
+            tmem_st16(tmem + lanes + c, o);
+          }
+          tmem_wait_st();
+        } else if (g >= C::kPs) {
+          if (!wait_o(g - C::kPs)) { ok = false; break; }  // P's buffer is free
+        }
+        const uint32_t pbuf = sbase + C::kPOff + (g % C::kPs) * C::kPBytes;
+#pragma unroll
+        for (int i = 0; i < F; i += 2) {
+          const int row = 8 * (i + (lane >> 4)) + (lane & 7), chunk = 2 * warp + ((lane >> 3) & 1);
+          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(
+                           pbuf + row * 128 + ((chunk ^ (row & 7)) << 4)),
+                       "r"(pack_bf16(x[i][0], x[i][1])), "r"(pack_bf16(x[i][2], x[i][3])),
+                       "r"(pack_bf16(x[i + 1][0], x[i + 1][1])), "r"(pack_bf16(x[i + 1][2], x[i + 1][3]))
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(bar(kPFull + (g & 1)));
+      }
+      if (!ok) break;
+
+      // ---- the unit's output: O' / sum, or its partial state
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[i][j] += __shfl_xor_sync(0xffffffffu, l[i][j], o);
+      if (!meet()) break;  // the last tile's maxima are read
+      if (lane < 4) {
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+          *reinterpret_cast<float2*>(&sm.mx[0][warp][8 * i + c0]) = make_float2(l[i][0], l[i][1]);
+        if (warp == 0 && u.slot >= 0) {
+#pragma unroll
+          for (int i = 0; i < F; ++i)
+            *reinterpret_cast<float2*>(&sm.mx[1][0][8 * i + c0]) = make_float2(m[i][0], m[i][1]);
+        }
+      }
+      if (!meet()) break;
+      if (tid < N) {
+        const float sum = sm.mx[0][0][tid] + sm.mx[0][1][tid] + sm.mx[0][2][tid] + sm.mx[0][3][tid];
+        sm.f[tid] = u.slot >= 0 ? 1.f : 1.f / sum;
+        if (u.slot >= 0)
+          reinterpret_cast<float2*>(p.part_ml)[static_cast<long long>(u.slot) * N + tid] =
+              make_float2(sm.mx[1][0][tid], sum);
+      }
+      if (!meet() || !wait_o(g - 1)) break;
+      tc_fence_after();
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(u.row0) * R;
+      float* part = p.part_acc + static_cast<long long>(u.slot) * N * R;
+#pragma unroll 1
+      for (int c = 0; c < C::kBlocks * N; c += 16) {
+        const int n0 = c & (N - 1);                        // rows n0 .. n0 + 15
+        const int d = (c / N) * 128 + warp * 32 + lane;    // this lane's number
+        if (n0 >= u.rows) continue;
+        uint32_t o[16];
+        tmem_ld16(tmem + lanes + c, o);
+        tmem_wait_ld();
+        if (u.slot >= 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (n0 + i < u.rows) part[(n0 + i) * R + d] = __uint_as_float(o[i]);
+        } else {
+          // lanes of a pair trade: the even one writes both numbers of row i, the odd one of row i + 1
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float a = __uint_as_float(o[i]) * sm.f[n0 + i], b = __uint_as_float(o[i + 1]) * sm.f[n0 + i + 1];
+            const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+            const int row = n0 + i + (lane & 1);
+            const uint32_t w = (lane & 1) ? pack_bf16(other, b) : pack_bf16(a, other);
+            if (row < u.rows) *reinterpret_cast<uint32_t*>(out + row * R + (d & ~1)) = w;
+          }
+        }
+      }
+      tc_fence_before();
+      if (!meet()) break;  // the shared factors are read
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of units that a border cut, in the order of their keys.  The CTA that
+// holds a unit's first piece has left a record; 8 CTAs a record.  A warp joins a row's pieces
+// one after the other where they are few; else a CTA's warps take every eighth piece of a row.
+template <int R, int N>
+__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) {
+  constexpr int kVec = R / 128;  // float4 of a lane
+  __shared__ float4 acc_s[8][R / 4];
+  __shared__ float2 ml_s[8];
+  wait_prior_grid();
+  const int* rec = p.recs + blockIdx.x * kLatentRecWords;
+  const int pieces = rec[3];
+  if (pieces == 0) return;
+  const int row0 = rec[0], rows = rec[1], ways = rec[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // piece k: the first CTA's slot 1, then slot 0 of the following ones
+  auto slot = [&](int k) {
+    return (static_cast<long long>(blockIdx.x + k * ways) * 2 + (k == 0)) * N;
+  };
+  const bool few = pieces <= 8;
+  const int step = few ? 64 : 8;
+  for (int n = few ? blockIdx.y * 8 + warp : blockIdx.y; n < rows; n += step) {
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 acc[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 ml, const float4 (&x)[kVec]) {
+      if (ml.y == 0.f) return;  // a piece whose keys the row does not see
+      const float nm = fmaxf(m, ml.x);
+      const float fa = m == nm ? 1.f : ex2(m - nm), fb = ml.x == nm ? 1.f : ex2(ml.x - nm);
+      m = nm;
+      l = l * fa + ml.y * fb;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        acc[i].x = acc[i].x * fa + x[i].x * fb;
+        acc[i].y = acc[i].y * fa + x[i].y * fb;
+        acc[i].z = acc[i].z * fa + x[i].z * fb;
+        acc[i].w = acc[i].w * fa + x[i].w * fb;
+      }
+    };
+#pragma unroll 2
+    for (int k = few ? 0 : warp; k < pieces; k += few ? 1 : 8) {
+      const long long row = slot(k) + n;
+      const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[row];
+      const float4* src = reinterpret_cast<const float4*>(p.part_acc + row * R);
+      float4 x[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = src[i * 32 + lane];
+      add(ml, x);
+    }
+    if (!few) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc_s[warp][i * 32 + lane] = acc[i];
+      if (lane == 0) ml_s[warp] = make_float2(m, l);
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < 8; ++w) {
+          float4 x[kVec];
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) x[i] = acc_s[w][i * 32 + lane];
+          add(ml_s[w], x);
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    const float inv = 1.f / l;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(row0 + n) * R);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      out[i * 32 + lane] = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+  }
+}
+
+namespace {
+
+template <int R, int N>
+cudaError_t launch_latent(const LatentParams& p, int num_sms, cudaStream_t stream) {
+  using C = Cfg<R, N>;
+  constexpr int W = R + kLatentRope;
+  static bool configured[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(latent_tc_kernel<R, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  CUtensorMap qmap, kmap;
+  {
+    const cuuint64_t dims[2] = {W, static_cast<cuuint64_t>(p.num_tokens) * p.num_heads};
+    const cuuint64_t strides[1] = {W * 2};
+    const cuuint32_t box[2] = {64, N};
+    if (!encode_bf16(&qmap, p.q, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[5] = {64, 8, C::kSlices, 2, static_cast<cuuint64_t>(p.num_blocks)};
+    const cuuint64_t strides[4] = {W * 2, 128, 8 * W * 2, kBlockSize * W * 2};
+    const cuuint32_t box[5] = {64, 8, C::kSlices, 2, 1};
+    if (!encode_bf16(&kmap, p.cache, 5, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  // decodes of more heads than a unit's rows: CTAs side by side take the row tiles of
+  // the same keys, so that all but the first read them from L2
+  int ways = p.max_query_len == 1 ? (p.num_heads + N - 1) / N : 1;
+  const int ctas = (num_sms < kLatentMaxCtas ? num_sms : kLatentMaxCtas) / ways * ways;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_tc_kernel<R, N>, p, qmap, kmap, ways);
+  if (e != cudaSuccess || p.max_seq_len <= kKeys) return e;  // (units of one tile are never cut)
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, latent_join_kernel<R, N>, p);
+}
+
+}  // namespace
+
+// Query rows of a unit: the smallest tile that holds a request's rows.
+static int unit_rows(int num_heads, int max_query_len) {
+  const long long rows = static_cast<long long>(num_heads) * max_query_len;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+size_t latent_tc_partial_rows(int num_heads, int max_query_len) {
+  return static_cast<size_t>(2) * kLatentMaxCtas * unit_rows(num_heads, max_query_len);
+}
+
+cudaError_t launch_latent_tc(const LatentParams& p, int latent_size, int num_sms, cudaStream_t stream) {
+  const int n = unit_rows(p.num_heads, p.max_query_len);
+  if (latent_size == 512)
+    return n == 16 ? launch_latent<512, 16>(p, num_sms, stream)
+         : n == 32 ? launch_latent<512, 32>(p, num_sms, stream)
+                   : launch_latent<512, 64>(p, num_sms, stream);
+  return n == 16 ? launch_latent<256, 16>(p, num_sms, stream)
+       : n == 32 ? launch_latent<256, 32>(p, num_sms, stream)
+                 : launch_latent<256, 64>(p, num_sms, stream);
+}
+
+}  // namespace pa
