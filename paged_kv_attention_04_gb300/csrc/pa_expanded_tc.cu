@@ -1,4 +1,670 @@
+// Latent attention in the expanded form on the 5th-generation tensor cores: ragged requests whose heads
+// have keys [k_nope (D), k_rope (64, shared by the heads)] and values (D) of their own, causal
+// from the bottom right.
+//
+// A (query, key) pair costs 2 (2 D + 64) flops and no bytes worth counting, so the tensor cores
+// bound it.  A unit is 256 rows of one head of a request, two tiles of 128 that read every
+// staged K and V tile; while one tile's softmax runs, the tensor cores work on the other's
+// products: S = Q K' (Q and K in shared memory) and O += P V (P in tensor memory, over the S
+// it came from).  The two S and the two O fill tensor memory at D = 128.
+// Shared memory: the two Q tiles, the rest a ring of 16 KB slots, each 128 keys x 64 numbers of K or
+// V (128-byte swizzle).  K takes D / 64 + 1 slots and V D / 64; slots are freed in the order they
+// are filled, so 8 slots (D = 128) keep the loads about one tile ahead of both products.
+//
+// Roles: warps 0-3 and 4-7 softmax and output of one tile each, a thread a row: no
+// trade between threads; O is rescaled only when a row's maximum grows by more than 2^8.  Warp 8
+// units and copies, warp 9 MMA issue.  A thread holds a row's 128 logits, so the softmax warps take
+// 208 registers of the 168 that the launch gives every thread, the others 88.
+//
+// Work: units lie on a line in request, head, row order, each as long as its key tiles plus a
+// constant; a CTA takes the units whose middle lies in its equal stretch.
+#include <math_constants.h>
+
 #include "pa_latent.h"
+#include "pa_tc_util.cuh"
+
 namespace pa {
-cudaError_t launch_expanded_tc(const ExpandedParams&, int, int, cudaStream_t) { return cudaErrorNotSupported; }
+
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128, kUnitRows = 256, kKeys = 128;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;
+constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
+constexpr int kSlotBytes = kKeys * 128;
+constexpr int kItems = 8;          // barriers of K and V tiles in the ring
+constexpr float kGrowth = 8.f;
+constexpr int kUnitCost = 2;       // what a unit costs beside its key tiles
+
+template <int D>
+struct ECfg {
+  static constexpr int kQSlices = D / 64 + 1, kVSlices = D / 64;
+  static constexpr int kQBytes = kQSlices * kSlotBytes;  // a tile of 128 rows
+  static constexpr int kSlots = D == 128 ? 8 : 10;
+  static constexpr int kRingOff = 2 * kQBytes;
+  static constexpr int kSmallOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kSmemBytes = kSmallOff + 1024;
+  static constexpr int kTmemO = 256;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
+};
+
+struct EUnit {
+  int r;       // < 0: no more units
+  int head;
+  int row0;    // first row of the step
+  int rows;    // valid rows (up to 256)
+  int pos0;    // key position of the first row
+  int key0;    // first key of the request in the step
+  int seq;     // keys of the request
+  int n[2];    // key tiles of each row tile
+};
+
+enum EBar : int {
+  eUnitFull = 0,   // [2]
+  eUnitEmpty = 2,  // [2] (8 softmax warps, MMA)
+  eQFull = 4,      // [2] TMA, by row tile
+  eQEmpty = 6,     // [2] the unit's last S of the row tile done
+  eSFull = 8,      // [2] S done, by row tile (and everything issued before it)
+  ePFull = 10,     // [2] S read, P written, O rescaled (4 warps)
+  eOFull = 12,     // [2] the unit's last O += done
+  eFull = 14,      // [8] K or V tile landed
+  eEmpty = 22,     // [8] ... and read
+  eVLand = 30,     // a V tile whose last rows are zeroed landed
+  eDrain = 31,
+  eNumBars = 32
+};
+
+struct ESmall {
+  uint64_t bars[eNumBars];
+  EUnit units[2];
+  long long sums[kThreads / 32];
+  long long start_pos;
+  uint32_t tmem;
+  int abort, bad, start_r;
+};
+static_assert(sizeof(ESmall) <= 1024, "small shared memory");
+
+struct ESpan {
+  int a, L, ka, S, tiles;  // rows, keys, row units of a head
+  long long head_len;      // line length of one head
+};
+
+// key tiles that rows up to position `last` see
+__device__ __forceinline__ int tiles_to(int last) { return last / kKeys + 1; }
+__device__ __forceinline__ int unit_len(const ESpan& s, int m) {
+  return tiles_to(s.S - s.L + min((m + 1) * kUnitRows, s.L) - 1) + kUnitCost;
+}
+
+__device__ __forceinline__ int span_of(const ExpandedParams& p, int r, ESpan& s) {
+  s.a = __ldg(p.qsl + r);
+  s.ka = __ldg(p.kvsl + r);
+  const int b = __ldg(p.qsl + r + 1), kb = __ldg(p.kvsl + r + 1);
+  s.L = b - s.a;
+  s.S = kb - s.ka;
+  s.tiles = 0;
+  s.head_len = 0;
+  if (s.L < 0 || s.a < 0 || b > p.num_tokens || s.S < 0 || s.ka < 0 || kb > p.num_kv_tokens ||
+      (r == 0 && (s.a != 0 || s.ka != 0)) ||
+      (r == p.num_seqs - 1 && (b != p.num_tokens || kb != p.num_kv_tokens)))
+    return PA_DEV_QSL;
+  if (s.L < 1 || s.L > s.S || s.S > p.max_kv_len || s.L > p.max_query_len) return PA_DEV_LENGTHS;
+  s.tiles = (s.L + kUnitRows - 1) / kUnitRows;
+  for (int m = 0; m < s.tiles; ++m) s.head_len += unit_len(s, m);
+  return 0;
+}
+
+struct EMaps {
+  CUtensorMap q, k, kr, v;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (a0, a1) = (a0, a1) * b + c in one instruction
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b, float c) {
+  asm("{\n .reg .b64 ra, rb, rc;\n mov.b64 ra, {%0, %1};\n mov.b64 rb, {%2, %2};\n"
+      " mov.b64 rc, {%3, %3};\n fma.rn.f32x2 ra, ra, rb, rc;\n mov.b64 {%0, %1}, ra;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n .reg .b64 ra, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rd, {%0, %1};\n"
+      " add.rn.f32x2 rd, rd, ra;\n mov.b64 {%0, %1}, rd;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    expanded_tc_kernel(const ExpandedParams p, const __grid_constant__ EMaps maps) {
+  using C = ECfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  ESmall& sm = *reinterpret_cast<ESmall*>(smem + C::kSmallOff);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &sm.abort;
+  auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
+
+  if (tid == 0) {
+    for (int i = 0; i < eNumBars; ++i) {
+      uint32_t n = 1;
+      if (i == eUnitEmpty || i == eUnitEmpty + 1) n = 9;
+      if (i == ePFull || i == ePFull + 1) n = 4;
+      mbar_init(bar(i), n);
+    }
+    // (the swizzled tiles need the alignment that the declaration asks for)
+    sm.abort = (sbase & 1023) != 0;
+    if (sbase & 1023) flag_error(p.status, PA_DEV_TIMEOUT);
+    sm.bad = 0;
+    sm.start_r = -1;
+    mbar_fence_init();
+  }
+  if (warp == 0) tmem_alloc(smem_u32(&sm.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  // ---- this CTA's stretch of the line, beginning in request start_r
+  long long lo = 0, hi = 0;
+  {
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int ra = min(tid * per, p.num_seqs), rb = min(ra + per, p.num_seqs);
+    long long mine = 0, total = 0;
+    int err = 0;
+    for (int r = ra; r < rb; ++r) {
+      ESpan s;
+      err |= span_of(p, r, s);
+      mine += s.head_len * p.num_heads;
+    }
+    if (err) {
+      if (blockIdx.x == 0) flag_error(p.status, err);
+      if (err & PA_DEV_QSL) sm.bad = 1;
+    }
+    long long before = mine;  // inclusive scan over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) sm.sums[warp] = before;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sm.sums[w];
+      total += sm.sums[w];
+    }
+    before -= mine;
+    if (sm.bad) total = 0;
+    lo = total * blockIdx.x / gridDim.x;
+    hi = total * (blockIdx.x + 1) / gridDim.x;
+    if (lo < hi && before <= lo && lo < before + mine) {
+      long long pos = before;
+      for (int r = ra; r < rb; ++r) {
+        ESpan s;
+        span_of(p, r, s);
+        const long long len = s.head_len * p.num_heads;
+        if (lo < pos + len) {
+          sm.start_r = r;
+          sm.start_pos = pos;
+          break;
+        }
+        pos += len;
+      }
+    }
+    __syncthreads();
+  }
+  wait_prior_grid();
+
+  if (warp >= kCopyWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+      // ------------------------------------------------------------ units and copies
+      int uc = 0;                    // units published
+      uint32_t it = 0, freed = 0;    // ring items filled, and known to be read
+      int used = 0, slot = 0;        // ring slots of items freed .. it - 1; next slot
+      uint32_t nq[2] = {0, 0};       // Q tiles copied
+      uint32_t nland = 0;
+      bool landing = false, ok = !*abort;
+      auto slots_of = [](uint32_t item) { return (item & 1) ? C::kVSlices : C::kQSlices; };
+      auto publish = [&](const EUnit& u) {
+        const int s = uc & 1;
+        if (uc >= 2 && !wait_bar(bar(eUnitEmpty + s), ((uc >> 1) - 1) & 1, abort, p.status)) return false;
+        if (lane == 0) {
+          sm.units[s] = u;
+          mbar_arrive(bar(eUnitFull + s));
+        }
+        __syncwarp();
+        ++uc;
+        return true;
+      };
+      auto load_q = [&](const EUnit& u, int w) {
+        if (u.n[w] == 0) return true;
+        if (nq[w] > 0 && !wait_bar(bar(eQEmpty + w), (nq[w] - 1) & 1, abort, p.status)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(eQFull + w), C::kQBytes);
+#pragma unroll
+          for (int s = 0; s < C::kQSlices; ++s)
+            tma_load_3d(sbase + w * C::kQBytes + s * kSlotBytes, &maps.q, s * 64, u.head, u.row0 + w * kRows,
+                        bar(eQFull + w));
+        }
+        __syncwarp();
+        ++nq[w];
+        return true;
+      };
+      // room in the ring for the next item
+      auto room = [&]() {
+        while (used + slots_of(it) > C::kSlots || it - freed >= kItems) {
+          if (!wait_bar(bar(eEmpty + freed % kItems), (freed / kItems) & 1, abort, p.status)) return false;
+          used -= slots_of(freed);
+          ++freed;
+        }
+        return true;
+      };
+      auto take = [&](int n) {  // the item's slots
+        used += n;
+        const int s = slot;
+        slot = (slot + n) % C::kSlots;
+        return s;
+      };
+      auto load_k = [&](const EUnit& u, int t) {
+        if (!room()) return false;
+        const int s0 = take(C::kQSlices);
+        const uint32_t full = bar(eFull + it % kItems);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, C::kQSlices * kSlotBytes);
+          const int key = u.key0 + t * kKeys;
+#pragma unroll
+          for (int s = 0; s < C::kQSlices; ++s) {
+            const uint32_t dst = sbase + C::kRingOff + (s0 + s) % C::kSlots * kSlotBytes;
+            if (s < C::kVSlices) tma_load_3d(dst, &maps.k, s * 64, u.head, key, full);
+            else tma_load_2d(dst, &maps.kr, 0, key, full);
+          }
+        }
+        __syncwarp();
+        ++it;
+        return true;
+      };
+      auto load_v = [&](const EUnit& u, int t) {
+        if (!room()) return false;
+        const int s0 = take(C::kVSlices);
+        // rows behind the request's last key hold another's values or nothing: zeros, so that
+        // a weight of zero meets no NaN
+        const int rows = u.seq - t * kKeys;
+        const bool trim = rows < kKeys;
+        const uint32_t full = bar(eFull + it % kItems), land = trim ? bar(eVLand) : full;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(land, C::kVSlices * kSlotBytes);
+#pragma unroll
+          for (int s = 0; s < C::kVSlices; ++s)
+            tma_load_3d(sbase + C::kRingOff + (s0 + s) % C::kSlots * kSlotBytes, &maps.v, s * 64, u.head,
+                        u.key0 + t * kKeys, land);
+        }
+        __syncwarp();
+        if (trim) {
+          landing = true;
+          if (!wait_bar(land, nland & 1, abort, p.status)) return false;
+          landing = false;
+          ++nland;
+          for (int i = lane; i < (kKeys - rows) * C::kVSlices * 8; i += 32) {
+            const int c = i % 8, s = i / 8 % C::kVSlices, row = rows + i / (8 * C::kVSlices);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(
+                             sbase + C::kRingOff + (s0 + s) % C::kSlots * kSlotBytes + row * 128 + c * 16),
+                         "r"(0u)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          warp_arrive(full);
+        }
+        ++it;
+        return true;
+      };
+      auto run = [&](const EUnit& u) {
+        const int n = max(u.n[0], u.n[1]);
+        if (!publish(u) || !load_q(u, 0) || !load_k(u, 0) || !load_q(u, 1)) return false;
+        for (int t = 0; t < n; ++t) {
+          if (!load_v(u, t)) return false;
+          if (t + 1 < n && !load_k(u, t + 1)) return false;
+        }
+        return true;
+      };
+      if (ok && sm.start_r >= 0) {
+        long long pos = sm.start_pos;
+        for (int r = sm.start_r; ok && r < p.num_seqs && pos < hi; ++r) {
+          ESpan s;
+          span_of(p, r, s);
+          if (s.tiles == 0) continue;
+          int h = lo > pos ? static_cast<int>((lo - pos) / s.head_len) : 0;
+          for (; ok && h < p.num_heads; ++h) {
+            long long at = pos + h * s.head_len;
+            if (at >= hi) break;
+            for (int m = 0; ok && m < s.tiles; ++m) {
+              const int len = unit_len(s, m);
+              const long long middle = at + len / 2;
+              at += len;
+              if (middle < lo) continue;
+              if (middle >= hi) break;
+              EUnit u;
+              u.r = r;
+              u.head = h;
+              u.row0 = s.a + m * kUnitRows;
+              u.rows = min(kUnitRows, s.L - m * kUnitRows);
+              u.pos0 = s.S - s.L + m * kUnitRows;
+              u.key0 = s.ka;
+              u.seq = s.S;
+              u.n[0] = tiles_to(u.pos0 + min(kRows, u.rows) - 1);
+              u.n[1] = u.rows > kRows ? tiles_to(u.pos0 + u.rows - 1) : 0;
+              ok = run(u);
+            }
+          }
+          pos += s.head_len * p.num_heads;
+        }
+      }
+      EUnit end{};
+      end.r = -1;
+      if (ok) publish(end);
+      if (*abort) {  // let every copy issued land before the CTA ends
+        for (uint32_t i = freed; i < it; ++i) drain_wait(bar(eFull + i % kItems), (i / kItems) & 1);
+        if (landing) drain_wait(bar(eVLand), nland & 1);
+        for (int w = 0; w < 2; ++w)
+          if (nq[w] > 0) drain_wait(bar(eQFull + w), (nq[w] - 1) & 1);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------ MMA issue
+      constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, 0);
+      constexpr uint32_t kIdO = idesc_bf16(kRows, D, 1), kIdHalf = idesc_bf16(kRows, 64, 1);
+      const uint64_t dq = smem_desc_sw128(sbase, 16, 1024);
+      const uint64_t dk = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sbase + C::kRingOff, kSlotBytes, 1024);
+      auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
+      int uc = 0;               // units read
+      int n[2] = {0, 0}, t = 0; // the current step: tile t of a unit
+      uint32_t step = 0;        // its number: K is item 2 step, V item 2 step + 1
+      int ks = 0;               // first ring slot of the next K
+      uint32_t np[2] = {0, 0};  // P tiles taken
+      uint32_t nq[2] = {0, 0};  // Q tiles taken
+      bool ok = !*abort;
+      auto fetch = [&](int (&m)[2]) {  // the next unit's tiles; 0, 0 at the end
+        const int s = uc & 1;
+        if (!wait_bar(bar(eUnitFull + s), (uc >> 1) & 1, abort, p.status)) return false;
+        const bool end = sm.units[s].r < 0;
+        m[0] = end ? 0 : sm.units[s].n[0];
+        m[1] = end ? 0 : sm.units[s].n[1];
+        warp_arrive(bar(eUnitEmpty + s));
+        ++uc;
+        return true;
+      };
+      auto wait_item = [&](uint32_t i) {
+        return wait_bar(bar(eFull + i % kItems), (i / kItems) & 1, abort, p.status);
+      };
+      // S of row tile w for tile tt of a unit with m tiles, K item `item` at slot s0
+      auto issue_s = [&](int w, int tt, int m, uint32_t item, int s0) {
+        if (tt == 0) {
+          if (!wait_bar(bar(eQFull + w), nq[w] & 1, abort, p.status)) return false;
+          ++nq[w];
+        }
+        if (!wait_item(item)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int s = 0; s < C::kQSlices; ++s) {
+            const uint64_t kb = adv(dk, (s0 + s) % C::kSlots * kSlotBytes);
+            const uint64_t qb = adv(dq, w * C::kQBytes + s * kSlotBytes);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tc_mma_f16(tmem + w * kKeys, adv(qb, i * 32), adv(kb, i * 32), kIdS, s + i > 0);
+          }
+          tc_commit(bar(eSFull + w));
+          if (tt == m - 1) tc_commit(bar(eQEmpty + w));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_o = [&](int w, int s0) {
+        if (!wait_bar(bar(ePFull + w), np[w] & 1, abort, p.status)) return false;
+        ++np[w];
+        if (!wait_item(2 * step + 1)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t d = tmem + C::kTmemO + w * D, a = tmem + w * kKeys;
+          if (D == 64 || s0 + 1 < C::kSlots) {
+            const uint64_t vb = adv(dv, s0 * kSlotBytes);
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+              tc_mma_f16_ts(d, a + i * 8, adv(vb, i * 2048), kIdO, t > 0 || i > 0);
+          } else {  // V's two slots are the ring's last and first: each half of O by itself
+#pragma unroll
+            for (int s = 0; s < C::kVSlices; ++s)
+#pragma unroll
+              for (int i = 0; i < kKeys / 16; ++i)
+                tc_mma_f16_ts(d + s * 64, a + i * 8, adv(dv, (s0 + s) % C::kSlots * kSlotBytes + i * 2048), kIdHalf,
+                              t > 0 || i > 0);
+          }
+          if (t == n[w] - 1) tc_commit(bar(eOFull + w));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto free_item = [&](uint32_t i) {
+        if (lane == 0) tc_commit(bar(eEmpty + i % kItems));
+        __syncwarp();
+      };
+      ok = ok && fetch(n);
+      if (ok && n[0] + n[1] > 0) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (ok && n[w] > 0) ok = issue_s(w, 0, n[w], 0, 0);
+        if (ok) free_item(0);
+        ks = C::kQSlices;  // (the V of the step comes next)
+        while (ok) {
+          const int vs = ks % C::kSlots;
+          const int k1 = (vs + C::kVSlices) % C::kSlots;
+          int m[2] = {n[0], n[1]}, t1 = t + 1;
+          if (t1 >= max(n[0], n[1])) {
+            t1 = 0;
+            if (!fetch(m)) { ok = false; break; }
+          }
+          const bool more = m[0] + m[1] > 0;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (ok && t < n[w]) ok = issue_o(w, vs);
+            if (ok && w == 1) free_item(2 * step + 1);
+            if (ok && more && t1 < m[w]) ok = issue_s(w, t1, m[w], 2 * step + 2, k1);
+          }
+          if (!ok || !more) break;
+          free_item(2 * step + 2);
+          ks = k1 + C::kQSlices;
+          ++step;
+          n[0] = m[0];
+          n[1] = m[1];
+          t = t1;
+        }
+      }
+      if (*abort) {  // nothing may still run on tensor memory when it is freed
+        if (lane == 0) tc_commit(bar(eDrain));
+        __syncwarp();
+        drain_wait(bar(eDrain), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+    // ------------------------------------------------------------ softmax and output
+    const int w = warp >> 2, i = tid & 127;  // row tile, row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + w * kKeys + lanes, to = tmem + C::kTmemO + w * D + lanes;
+    // maxima are taken of logits that grow with S: a negative scale turns S over
+    const bool minus = p.scale_log2 < 0.f;
+    const float scale = fabsf(p.scale_log2);
+    uint32_t ns = 0, no = 0;  // S tiles and units of this row tile so far
+    bool ok = !*abort;
+    for (int uc = 0; ok; ++uc) {
+      if (!wait_bar(bar(eUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
+      const EUnit u = sm.units[uc & 1];
+      warp_arrive(bar(eUnitEmpty + (uc & 1)));
+      if (u.r < 0) break;
+      const int n = w ? u.n[1] : u.n[0];
+      if (n == 0) continue;
+      const int pos = u.pos0 + w * kRows + i;  // keys up to here are seen
+      float m = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+      for (int t = 0; t < n; ++t, ++ns) {
+        if (!wait_bar(bar(eSFull + w), ns & 1, abort, p.status)) { ok = false; break; }
+        tc_fence_after();
+        float x[128];
+        {
+          uint32_t(&r)[128] = reinterpret_cast<uint32_t(&)[128]>(x);
+          PA_TMEM_LD32(ts, (r + 0));
+          PA_TMEM_LD32(ts + 32, (r + 32));
+          PA_TMEM_LD32(ts + 64, (r + 64));
+          PA_TMEM_LD32(ts + 96, (r + 96));
+          tmem_wait_ld();
+        }
+        if (minus) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) x[j] = -x[j];
+        }
+        if ((t + 1) * kKeys - 1 > u.pos0 + w * kRows) {
+          const int last = pos - t * kKeys;
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (j > last) x[j] = -CUDART_INF_F;
+        }
+        float mx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(x[j], x[j + 4]);
+#pragma unroll
+        for (int j = 8; j < 128; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        float f = 1.f;
+        if (top > m + kGrowth) {  // (also the first finite maximum: m = -inf)
+          f = ex2(m - top);
+          m = top;
+          l0 *= f;
+          l1 *= f;
+        }
+        // O of earlier tiles takes the new reference (S done: so is every product before it)
+        if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(to + c, o);
+          }
+        }
+        const float ref = m == -CUDART_INF_F ? 0.f : -m;  // (no key seen yet: every weight 0)
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float &a = x[c + j], &b = x[c + j + 1];
+            fma2(a, b, scale, ref);
+            a = ex2(a);
+            b = ex2(b);
+            add2(l0, l1, a, b);
+            pk[j / 2] = pack_bf16(a, b);
+          }
+          tmem_st16(ts + c / 2, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar(ePFull + w));
+      }
+      if (!ok) break;
+      if (!wait_bar(bar(eOFull + w), no & 1, abort, p.status)) break;
+      ++no;
+      tc_fence_after();
+      const float inv = 1.f / (l0 + l1);
+      const int row = w * kRows + i;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                           (static_cast<long long>(u.row0 + row) * p.num_heads + u.head) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        PA_TMEM_LD32(to + c, o);
+        tmem_wait_ld();
+        if (row < u.rows) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[j + e]) * inv;
+            *reinterpret_cast<uint4*>(out + c + j) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                                pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+          }
+        }
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+namespace {
+
+template <int D>
+cudaError_t launch_expanded(const ExpandedParams& args, int num_sms, cudaStream_t stream) {
+  using C = ECfg<D>;
+  static bool configured[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(expanded_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  ExpandedParams p = args;
+  // (a scale of zero would make NaN of the masked logits' -inf)
+  if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;
+  EMaps maps;
+  const cuuint32_t box3[3] = {64, 1, 128}, box2[2] = {64, 128};
+  auto rows3 = [&](CUtensorMap* m, const void* base, int size, long long head_stride, long long stride, int n) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(size), static_cast<cuuint64_t>(p.num_heads),
+                                static_cast<cuuint64_t>(n)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(stride) * 2};
+    return encode_bf16(m, base, 3, dims, strides, box3);
+  };
+  const cuuint64_t dims2[2] = {kLatentRope, static_cast<cuuint64_t>(p.num_kv_tokens)};
+  const cuuint64_t strides2[1] = {static_cast<cuuint64_t>(p.kr_stride) * 2};
+  if (!rows3(&maps.q, p.q, D + kLatentRope, p.q_head_stride, p.q_stride, p.num_tokens) ||
+      !rows3(&maps.k, p.k, D, p.k_head_stride, p.k_stride, p.num_kv_tokens) ||
+      !rows3(&maps.v, p.v, D, p.v_head_stride, p.v_stride, p.num_kv_tokens) ||
+      !encode_bf16(&maps.kr, p.kr, 2, dims2, strides2, box2))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, expanded_tc_kernel<D>, p, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_expanded_tc(const ExpandedParams& p, int head_size, int num_sms, cudaStream_t stream) {
+  return head_size == 128 ? launch_expanded<128>(p, num_sms, stream) : launch_expanded<64>(p, num_sms, stream);
+}
+
 }  // namespace pa
