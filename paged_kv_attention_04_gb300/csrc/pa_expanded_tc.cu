@@ -411,14 +411,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!wait_item(item)) return false;
         tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
+        if (elect_one()) {
+          // (slices one by one: unrolled, the descriptors of all of them spill, and an MMA waits for its own)
+          uint64_t qb = adv(dq, w * C::kQBytes);
+          uint32_t k = s0;
+#pragma unroll 1
           for (int s = 0; s < C::kQSlices; ++s) {
-            const uint64_t kb = adv(dk, (s0 + s) % C::kSlots * kSlotBytes);
-            const uint64_t qb = adv(dq, w * C::kQBytes + s * kSlotBytes);
+            const uint64_t kb = adv(dk, k * kSlotBytes);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              tc_mma_f16(tmem + w * kKeys, adv(qb, i * 32), adv(kb, i * 32), kIdS, s + i > 0);
+              tc_mma_f16(tmem + w * kKeys, adv(qb, i * 32), adv(kb, i * 32), kIdS, s > 0 || i > 0);
+            qb = adv(qb, kSlotBytes);
+            k = k + 1 == C::kSlots ? 0 : k + 1;
           }
           tc_commit(bar(eSFull + w));
           if (tt == m - 1) tc_commit(bar(eQEmpty + w));
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++np[w];
         if (!wait_item(2 * step + 1)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t d = tmem + C::kTmemO + w * D, a = tmem + w * kKeys;
           if (D == 64 || s0 + 1 < C::kSlots) {
             const uint64_t vb = adv(dv, s0 * kSlotBytes);
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kKeys / 16; ++i)
               tc_mma_f16_ts(d, a + i * 8, adv(vb, i * 2048), kIdO, t > 0 || i > 0);
           } else {  // V's two slots are the ring's last and first: each half of O by itself
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < C::kVSlices; ++s)
 #pragma unroll
               for (int i = 0; i < kKeys / 16; ++i)
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       auto free_item = [&](uint32_t i) {
-        if (lane == 0) tc_commit(bar(eEmpty + i % kItems));
+        if (elect_one()) tc_commit(bar(eEmpty + i % kItems));
         __syncwarp();
       };
       ok = ok && fetch(n);
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (*abort) {  // nothing may still run on tensor memory when it is freed
-        if (lane == 0) tc_commit(bar(eDrain));
+        if (elect_one()) tc_commit(bar(eDrain));
         __syncwarp();
         drain_wait(bar(eDrain), 0);
       }

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    (!fresh || ready(bar(kQFull + uc % C::kQs), (uc / C::kQs) & 1))) {
           const uint32_t b = gs % C::kBufs;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint64_t kb = adv(dk, b * C::kTileBytes), qb = adv(dq, (uc % C::kQs) * C::kQBytes);
             const uint32_t d = tmem + C::kTmemS + (gs & 1) * N;
 #pragma unroll
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (gp < gs && ready(bar(kPFull + (gp & 1)), (gp >> 1) & 1)) {
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t b = gp % C::kBufs;
           const uint64_t vb = adv(dv, b * C::kTileBytes), pb = adv(dp, (gp % C::kPs) * C::kPBytes);
           const bool first = (firsts >> (gp & 1)) & 1;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       idle = moved ? 0 : idle + 1;
       if (__any_sync(0xffffffffu, *abort != 0)) break;
       if (idle > kPollLimit) {
-        if (lane == 0) {
+        if (elect_one()) {
           *abort = 1;
           flag_error(p.status, PA_DEV_TIMEOUT);
         }
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (*abort) {  // nothing may still run on tensor memory when it is freed
-      if (lane == 0) tc_commit(bar(kDrain));
+      if (elect_one()) tc_commit(bar(kDrain));
       __syncwarp();
       drain_wait(bar(kDrain), 0);
     }

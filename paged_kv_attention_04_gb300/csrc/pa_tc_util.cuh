@@ -38,6 +38,15 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitLimit; ++i)
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
 }
+// One lane of a converged warp, the same one each time.  MMAs are issued under this and not under
+// lane == 0: the compiler then knows that one thread runs them and takes their descriptors to uniform
+// registers once, where a lane's own cost 46 cycles an MMA, whatever its shape (an MMA of 64 x 32 x 16
+// takes 24, 128 x 32 40, 128 x 128 64, measured in a row of 384).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 // One arrival per warp, after every lane's preceding work.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
