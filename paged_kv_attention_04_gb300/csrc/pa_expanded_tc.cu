@@ -7,13 +7,14 @@
 // staged K and V tile; while one tile's softmax runs, the tensor cores work on the other's
 // products: S = Q K' (Q and K in shared memory) and O += P V (P in tensor memory, over the S
 // it came from).  The two S and the two O fill tensor memory at D = 128.
-// Shared memory: the two Q tiles, the rest a ring of 16 KB slots, each 128 keys x 64 numbers of K or
-// V (128-byte swizzle).  K takes D / 64 + 1 slots and V D / 64; slots are freed in the order they
-// are filled, so 8 slots (D = 128) keep the loads about one tile ahead of both products.
+// Shared memory holds the two Q tiles and K and V of two key tiles (four at D = 64), in slices of 64
+// numbers (128-byte swizzle).  Key tiles are of 96 keys so that two fit at D = 128: S costs 56 cycles an
+// MMA instead of 48 for it, but with 128 keys, whose K and V fit one and a half times, the products
+// waited for their loads (4400 cycles a step of 128 keys, ideal 2560).
 //
 // Roles: warps 0-3 and 4-7 softmax and output of one tile each, a thread a row: no
 // trade between threads; O is rescaled only when a row's maximum grows by more than 2^8.  Warp 8
-// units and copies, warp 9 MMA issue.  A thread holds a row's 128 logits, so the softmax warps take
+// units and copies, warp 9 MMA issue.  A thread holds a row's 96 logits, so the softmax warps take
 // 208 registers of the 168 that the launch gives every thread, the others 88.
 //
 // Work: units lie on a line in request, head, row order, each as long as its key tiles plus a
@@ -29,22 +30,22 @@ namespace {
 
 using namespace tc;
 
-constexpr int kRows = 128, kUnitRows = 256, kKeys = 128;
+constexpr int kRows = 128, kUnitRows = 256, kKeys = 96;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 384;
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
-constexpr int kSlotBytes = kKeys * 128;
-constexpr int kItems = 8;          // barriers of K and V tiles in the ring
+constexpr int kQSlice = kRows * 128, kKSlice = kKeys * 128;  // bytes of 64 numbers of a tile
 constexpr float kGrowth = 8.f;
 constexpr int kUnitCost = 2;       // what a unit costs beside its key tiles
 
 template <int D>
 struct ECfg {
   static constexpr int kQSlices = D / 64 + 1, kVSlices = D / 64;
-  static constexpr int kQBytes = kQSlices * kSlotBytes;  // a tile of 128 rows
-  static constexpr int kSlots = D == 128 ? 8 : 10;
-  static constexpr int kRingOff = 2 * kQBytes;
-  static constexpr int kSmallOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kQBytes = kQSlices * kQSlice;
+  static constexpr int kKBytes = kQSlices * kKSlice, kVBytes = kVSlices * kKSlice;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kKOff = 2 * kQBytes, kVOff = kKOff + kStages * kKBytes;
+  static constexpr int kSmallOff = kVOff + kStages * kVBytes;
   static constexpr int kSmemBytes = kSmallOff + 1024;
   static constexpr int kTmemO = 256;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
@@ -67,13 +68,16 @@ enum EBar : int {
   eQFull = 4,      // [2] TMA, by row tile
   eQEmpty = 6,     // [2] the unit's last S of the row tile done
   eSFull = 8,      // [2] S done, by row tile (and everything issued before it)
-  ePFull = 10,     // [2] S read, P written, O rescaled (4 warps)
-  eOFull = 12,     // [2] the unit's last O += done
-  eFull = 14,      // [8] K or V tile landed
-  eEmpty = 22,     // [8] ... and read
-  eVLand = 30,     // a V tile whose last rows are zeroed landed
-  eDrain = 31,
-  eNumBars = 32
+  ePFull = 10,     // S of row tile 1 read, P written, O rescaled (4 warps)
+  eOFull = 11,     // [2] the unit's last O += done
+  eKFirst = 13,    // the first K landed
+  eVLand = 14,     // a V tile whose last rows are zeroed landed
+  eDrain = 15,
+  eGo = 16,        // [4] by stage: all that the products of row tile 0 in a step need: S read, P written, O
+                   //     rescaled (4 warps), V landed, K of the next step landed
+  eKEmpty = 20,    // [4] K read, by stage
+  eVEmpty = 24,    // [4]
+  eNumBars = 28
 };
 
 struct ESmall {
@@ -155,7 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < eNumBars; ++i) {
       uint32_t n = 1;
       if (i == eUnitEmpty || i == eUnitEmpty + 1) n = 9;
-      if (i == ePFull || i == ePFull + 1) n = 4;
+      if (i == ePFull) n = 4;
+      if (i >= eGo && i < eGo + 4) n = 6;
       mbar_init(bar(i), n);
     }
     // (the swizzled tiles need the alignment that the declaration asks for)
@@ -226,12 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {
       // ------------------------------------------------------------ units and copies
       int uc = 0;                    // units published
-      uint32_t it = 0, freed = 0;    // ring items filled, and known to be read
-      int used = 0, slot = 0;        // ring slots of items freed .. it - 1; next slot
+      uint32_t nk = 0, nv = 0;       // K and V tiles copied
       uint32_t nq[2] = {0, 0};       // Q tiles copied
       uint32_t nland = 0;
       bool landing = false, ok = !*abort;
-      auto slots_of = [](uint32_t item) { return (item & 1) ? C::kVSlices : C::kQSlices; };
       auto publish = [&](const EUnit& u) {
         const int s = uc & 1;
         if (uc >= 2 && !wait_bar(bar(eUnitEmpty + s), ((uc >> 1) - 1) & 1, abort, p.status)) return false;
@@ -250,60 +253,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(bar(eQFull + w), C::kQBytes);
 #pragma unroll
           for (int s = 0; s < C::kQSlices; ++s)
-            tma_load_3d(sbase + w * C::kQBytes + s * kSlotBytes, &maps.q, s * 64, u.head, u.row0 + w * kRows,
+            tma_load_3d(sbase + w * C::kQBytes + s * kQSlice, &maps.q, s * 64, u.head, u.row0 + w * kRows,
                         bar(eQFull + w));
         }
         __syncwarp();
         ++nq[w];
         return true;
       };
-      // room in the ring for the next item
-      auto room = [&]() {
-        while (used + slots_of(it) > C::kSlots || it - freed >= kItems) {
-          if (!wait_bar(bar(eEmpty + freed % kItems), (freed / kItems) & 1, abort, p.status)) return false;
-          used -= slots_of(freed);
-          ++freed;
-        }
-        return true;
-      };
-      auto take = [&](int n) {  // the item's slots
-        used += n;
-        const int s = slot;
-        slot = (slot + n) % C::kSlots;
-        return s;
-      };
       auto load_k = [&](const EUnit& u, int t) {
-        if (!room()) return false;
-        const int s0 = take(C::kQSlices);
-        const uint32_t full = bar(eFull + it % kItems);
+        const uint32_t b = nk % C::kStages;
+        if (nk >= C::kStages && !wait_bar(bar(eKEmpty + b), (nk / C::kStages - 1) & 1, abort, p.status)) return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(full, C::kQSlices * kSlotBytes);
-          const int key = u.key0 + t * kKeys;
+          const uint32_t full = nk == 0 ? bar(eKFirst) : bar(eGo + (nk - 1) % C::kStages);
+          mbar_arrive_expect_tx(full, C::kKBytes);
 #pragma unroll
           for (int s = 0; s < C::kQSlices; ++s) {
-            const uint32_t dst = sbase + C::kRingOff + (s0 + s) % C::kSlots * kSlotBytes;
-            if (s < C::kVSlices) tma_load_3d(dst, &maps.k, s * 64, u.head, key, full);
-            else tma_load_2d(dst, &maps.kr, 0, key, full);
+            const uint32_t dst = sbase + C::kKOff + b * C::kKBytes + s * kKSlice;
+            if (s < C::kVSlices) tma_load_3d(dst, &maps.k, s * 64, u.head, u.key0 + t * kKeys, full);
+            else tma_load_2d(dst, &maps.kr, 0, u.key0 + t * kKeys, full);
           }
         }
         __syncwarp();
-        ++it;
+        ++nk;
         return true;
       };
       auto load_v = [&](const EUnit& u, int t) {
-        if (!room()) return false;
-        const int s0 = take(C::kVSlices);
+        const uint32_t b = nv % C::kStages;
+        if (nv >= C::kStages && !wait_bar(bar(eVEmpty + b), (nv / C::kStages - 1) & 1, abort, p.status)) return false;
         // rows behind the request's last key hold another's values or nothing: zeros, so that
         // a weight of zero meets no NaN
         const int rows = u.seq - t * kKeys;
         const bool trim = rows < kKeys;
-        const uint32_t full = bar(eFull + it % kItems), land = trim ? bar(eVLand) : full;
+        const uint32_t go = bar(eGo + b), land = trim ? bar(eVLand) : go, dst = sbase + C::kVOff + b * C::kVBytes;
         if (lane == 0) {
-          mbar_arrive_expect_tx(land, C::kVSlices * kSlotBytes);
+          mbar_arrive_expect_tx(land, C::kVBytes);
 #pragma unroll
           for (int s = 0; s < C::kVSlices; ++s)
-            tma_load_3d(sbase + C::kRingOff + (s0 + s) % C::kSlots * kSlotBytes, &maps.v, s * 64, u.head,
-                        u.key0 + t * kKeys, land);
+            tma_load_3d(dst + s * kKSlice, &maps.v, s * 64, u.head, u.key0 + t * kKeys, land);
         }
         __syncwarp();
         if (trim) {
@@ -313,20 +299,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nland;
           for (int i = lane; i < (kKeys - rows) * C::kVSlices * 8; i += 32) {
             const int c = i % 8, s = i / 8 % C::kVSlices, row = rows + i / (8 * C::kVSlices);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(
-                             sbase + C::kRingOff + (s0 + s) % C::kSlots * kSlotBytes + row * 128 + c * 16),
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(dst + s * kKSlice + row * 128 + c * 16),
                          "r"(0u)
                          : "memory");
           }
           fence_proxy_async_smem();
-          warp_arrive(full);
+          warp_arrive(go);
         }
-        ++it;
+        ++nv;
         return true;
       };
       auto run = [&](const EUnit& u) {
         const int n = max(u.n[0], u.n[1]);
-        if (!publish(u) || !load_q(u, 0) || !load_k(u, 0) || !load_q(u, 1)) return false;
+        if (!publish(u) || !load_k(u, 0) || !load_q(u, 0) || !load_q(u, 1)) return false;
         for (int t = 0; t < n; ++t) {
           if (!load_v(u, t)) return false;
           if (t + 1 < n && !load_k(u, t + 1)) return false;
@@ -367,9 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       EUnit end{};
       end.r = -1;
-      if (ok) publish(end);
+      if (ok && publish(end) && nk > 0) warp_arrive(bar(eGo + (nk - 1) % C::kStages));  // no K behind the last step
       if (*abort) {  // let every copy issued land before the CTA ends
-        for (uint32_t i = freed; i < it; ++i) drain_wait(bar(eFull + i % kItems), (i / kItems) & 1);
+        // (a phase of eGo may never complete: the limit outlasts its copies)
+        if (nk > 0) drain_wait(bar(eKFirst), 0);
+        const uint32_t steps = max(nv, nk > 0 ? nk - 1 : 0);
+        for (uint32_t i = steps > C::kStages ? steps - C::kStages : 0; i < steps; ++i)
+          drain_wait(bar(eGo + i % C::kStages), (i / C::kStages) & 1, 1u << 20);
         if (landing) drain_wait(bar(eVLand), nland & 1);
         for (int w = 0; w < 2; ++w)
           if (nq[w] > 0) drain_wait(bar(eQFull + w), (nq[w] - 1) & 1);
@@ -378,118 +367,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ MMA issue
       constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, 0);
-      constexpr uint32_t kIdO = idesc_bf16(kRows, D, 1), kIdHalf = idesc_bf16(kRows, 64, 1);
+      constexpr uint32_t kIdO = idesc_bf16(kRows, D, 1);
       const uint64_t dq = smem_desc_sw128(sbase, 16, 1024);
-      const uint64_t dk = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
-      const uint64_t dv = smem_desc_sw128(sbase + C::kRingOff, kSlotBytes, 1024);
+      const uint64_t dk = smem_desc_sw128(sbase + C::kKOff, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sbase + C::kVOff, kKSlice, 1024);
       auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
-      int uc = 0;               // units read
-      int n[2] = {0, 0}, t = 0; // the current step: tile t of a unit
-      uint32_t step = 0;        // its number: K is item 2 step, V item 2 step + 1
-      int ks = 0;               // first ring slot of the next K
-      uint32_t np[2] = {0, 0};  // P tiles taken
-      uint32_t nq[2] = {0, 0};  // Q tiles taken
-      bool ok = !*abort;
-      auto fetch = [&](int (&m)[2]) {  // the next unit's tiles; 0, 0 at the end
-        const int s = uc & 1;
-        if (!wait_bar(bar(eUnitFull + s), (uc >> 1) & 1, abort, p.status)) return false;
-        const bool end = sm.units[s].r < 0;
-        m[0] = end ? 0 : sm.units[s].n[0];
-        m[1] = end ? 0 : sm.units[s].n[1];
-        warp_arrive(bar(eUnitEmpty + s));
-        ++uc;
-        return true;
-      };
-      auto wait_item = [&](uint32_t i) {
-        return wait_bar(bar(eFull + i % kItems), (i / kItems) & 1, abort, p.status);
-      };
-      // S of row tile w for tile tt of a unit with m tiles, K item `item` at slot s0
-      auto issue_s = [&](int w, int tt, int m, uint32_t item, int s0) {
-        if (tt == 0) {
-          if (!wait_bar(bar(eQFull + w), nq[w] & 1, abort, p.status)) return false;
-          ++nq[w];
-        }
-        if (!wait_item(item)) return false;
-        tc_fence_after();
-        if (elect_one()) {
+      // One thread does it all.  What a step needs is waited for before its first product, so
+      // that the products of a row tile, O += P V and the next S, are issued in a row: every wait
+      // between them lets the short queue of the tensor cores run dry.
+      if (elect_one() && !*abort) {
+        int uc = 0;               // units read
+        int n0 = 0, n1 = 0, t = 0;  // the current step: tile t of a unit
+        uint32_t step = 0;        // its number: its K and V are in stage step % kStages
+        uint32_t np1 = 0;         // P tiles of row tile 1 taken
+        uint32_t nq0 = 0, nq1 = 0;  // Q tiles taken
+        auto wait = [&](int i, uint32_t parity) { return wait_one(bar(i), parity, abort, p.status); };
+        auto fetch = [&](int& a, int& b) {  // the next unit's tiles; 0, 0 at the end
+          const int s = uc & 1;
+          if (!wait(eUnitFull + s, (uc >> 1) & 1)) return false;
+          const bool end = sm.units[s].r < 0;
+          a = end ? 0 : sm.units[s].n[0];
+          b = end ? 0 : sm.units[s].n[1];
+          mbar_arrive(bar(eUnitEmpty + s));
+          ++uc;
+          return true;
+        };
+        auto stage = [](uint32_t i) { return static_cast<int>(i % C::kStages); };
+        // S of row tile w, K from stage b; last: the unit's last of the row tile
+        auto issue_s = [&](int w, int b, bool last) {
           // (slices one by one: unrolled, the descriptors of all of them spill, and an MMA waits for its own)
-          uint64_t qb = adv(dq, w * C::kQBytes);
-          uint32_t k = s0;
+          uint64_t qb = adv(dq, w * C::kQBytes), kb = adv(dk, b * C::kKBytes);
 #pragma unroll 1
           for (int s = 0; s < C::kQSlices; ++s) {
-            const uint64_t kb = adv(dk, k * kSlotBytes);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              tc_mma_f16(tmem + w * kKeys, adv(qb, i * 32), adv(kb, i * 32), kIdS, s > 0 || i > 0);
-            qb = adv(qb, kSlotBytes);
-            k = k + 1 == C::kSlots ? 0 : k + 1;
+              tc_mma_f16(tmem + w * kRows, adv(qb, i * 32), adv(kb, i * 32), kIdS, s > 0 || i > 0);
+            qb = adv(qb, kQSlice);
+            kb = adv(kb, kKSlice);
           }
           tc_commit(bar(eSFull + w));
-          if (tt == m - 1) tc_commit(bar(eQEmpty + w));
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_o = [&](int w, int s0) {
-        if (!wait_bar(bar(ePFull + w), np[w] & 1, abort, p.status)) return false;
-        ++np[w];
-        if (!wait_item(2 * step + 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t d = tmem + C::kTmemO + w * D, a = tmem + w * kKeys;
-          if (D == 64 || s0 + 1 < C::kSlots) {
-            const uint64_t vb = adv(dv, s0 * kSlotBytes);
+          if (last) tc_commit(bar(eQEmpty + w));
+        };
+        // O += P V of row tile w, V from stage b
+        auto issue_o = [&](int w, int b, bool first, bool last) {
+          const uint32_t d = tmem + C::kTmemO + w * D, a = tmem + w * kRows;
+          const uint64_t vb = adv(dv, b * C::kVBytes);
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              tc_mma_f16_ts(d, a + i * 8, adv(vb, i * 2048), kIdO, t > 0 || i > 0);
-          } else {  // V's two slots are the ring's last and first: each half of O by itself
-#pragma unroll 1
-            for (int s = 0; s < C::kVSlices; ++s)
-#pragma unroll
-              for (int i = 0; i < kKeys / 16; ++i)
-                tc_mma_f16_ts(d + s * 64, a + i * 8, adv(dv, (s0 + s) % C::kSlots * kSlotBytes + i * 2048), kIdHalf,
-                              t > 0 || i > 0);
+          for (int i = 0; i < kKeys / 16; ++i)
+            tc_mma_f16_ts(d, a + i * 8, adv(vb, i * 2048), kIdO, !first || i > 0);
+          if (last) tc_commit(bar(eOFull + w));
+        };
+        bool ok = fetch(n0, n1);
+        bool more = ok && n0 + n1 > 0;
+        if (more) {
+          ok = wait(eKFirst, 0) && wait(eQFull, nq0++ & 1);
+          if (ok) issue_s(0, 0, n0 == 1);
+          if (ok && n1 > 0) {
+            ok = wait(eQFull + 1, nq1++ & 1);
+            if (ok) issue_s(1, 0, n1 == 1);
           }
-          if (t == n[w] - 1) tc_commit(bar(eOFull + w));
+          if (ok) tc_commit(bar(eKEmpty));
         }
-        __syncwarp();
-        return true;
-      };
-      auto free_item = [&](uint32_t i) {
-        if (elect_one()) tc_commit(bar(eEmpty + i % kItems));
-        __syncwarp();
-      };
-      ok = ok && fetch(n);
-      if (ok && n[0] + n[1] > 0) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (ok && n[w] > 0) ok = issue_s(w, 0, n[w], 0, 0);
-        if (ok) free_item(0);
-        ks = C::kQSlices;  // (the V of the step comes next)
-        while (ok) {
-          const int vs = ks % C::kSlots;
-          const int k1 = (vs + C::kVSlices) % C::kSlots;
-          int m[2] = {n[0], n[1]}, t1 = t + 1;
-          if (t1 >= max(n[0], n[1])) {
+        while (ok && more) {
+          // the next step: its K stands behind this step's V
+          int m0 = n0, m1 = n1, t1 = t + 1;
+          if (t1 >= max(n0, n1)) {
             t1 = 0;
-            if (!fetch(m)) { ok = false; break; }
+            if (!fetch(m0, m1)) break;
+            more = m0 + m1 > 0;
           }
-          const bool more = m[0] + m[1] > 0;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (ok && t < n[w]) ok = issue_o(w, vs);
-            if (ok && w == 1) free_item(2 * step + 1);
-            if (ok && more && t1 < m[w]) ok = issue_s(w, t1, m[w], 2 * step + 2, k1);
+          const int b0 = stage(step), b1 = stage(step + 1);
+          const bool s0 = more && t1 < m0, s1 = more && t1 < m1;
+          if (s0 && t1 == 0 && !wait(eQFull, nq0++ & 1)) break;
+          if (!wait(eGo + b0, (step / C::kStages) & 1)) break;
+          tc_fence_after();
+          if (t < n0) issue_o(0, b0, t == 0, t == n0 - 1);
+          if (s0) issue_s(0, b1, t1 == m0 - 1);
+          if (s1 && t1 == 0 && !wait(eQFull + 1, nq1++ & 1)) break;
+          if (t < n1) {
+            if (!wait(ePFull, np1++ & 1)) break;
+            tc_fence_after();
+            issue_o(1, b0, t == 0, t == n1 - 1);
           }
-          if (!ok || !more) break;
-          free_item(2 * step + 2);
-          ks = k1 + C::kQSlices;
+          tc_commit(bar(eVEmpty + b0));
+          if (s1) issue_s(1, b1, t1 == m1 - 1);
+          if (more) tc_commit(bar(eKEmpty + b1));
           ++step;
-          n[0] = m[0];
-          n[1] = m[1];
+          n0 = m0;
+          n1 = m1;
           t = t1;
         }
       }
+      __syncwarp();
       if (*abort) {  // nothing may still run on tensor memory when it is freed
         if (elect_one()) tc_commit(bar(eDrain));
         __syncwarp();
@@ -502,11 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax and output
     const int w = warp >> 2, i = tid & 127;  // row tile, row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + w * kKeys + lanes, to = tmem + C::kTmemO + w * D + lanes;
+    const uint32_t ts = tmem + w * kRows + lanes, to = tmem + C::kTmemO + w * D + lanes;
     // maxima are taken of logits that grow with S: a negative scale turns S over
     const bool minus = p.scale_log2 < 0.f;
     const float scale = fabsf(p.scale_log2);
-    uint32_t ns = 0, no = 0;  // S tiles and units of this row tile so far
+    uint32_t ns = 0, no = 0, go = 0;  // S tiles, units and arrivals of this row tile so far
     bool ok = !*abort;
     for (int uc = 0; ok; ++uc) {
       if (!wait_bar(bar(eUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
@@ -514,36 +483,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(bar(eUnitEmpty + (uc & 1)));
       if (u.r < 0) break;
       const int n = w ? u.n[1] : u.n[0];
-      if (n == 0) continue;
+      if (n == 0) continue;  // (row tile 1)
       const int pos = u.pos0 + w * kRows + i;  // keys up to here are seen
       float m = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
       for (int t = 0; t < n; ++t, ++ns) {
         if (!wait_bar(bar(eSFull + w), ns & 1, abort, p.status)) { ok = false; break; }
         tc_fence_after();
-        float x[128];
+        float x[kKeys];
         {
-          uint32_t(&r)[128] = reinterpret_cast<uint32_t(&)[128]>(x);
+          uint32_t(&r)[kKeys] = reinterpret_cast<uint32_t(&)[kKeys]>(x);
           PA_TMEM_LD32(ts, (r + 0));
           PA_TMEM_LD32(ts + 32, (r + 32));
           PA_TMEM_LD32(ts + 64, (r + 64));
-          PA_TMEM_LD32(ts + 96, (r + 96));
           tmem_wait_ld();
         }
         if (minus) {
 #pragma unroll
-          for (int j = 0; j < 128; ++j) x[j] = -x[j];
+          for (int j = 0; j < kKeys; ++j) x[j] = -x[j];
         }
         if ((t + 1) * kKeys - 1 > u.pos0 + w * kRows) {
           const int last = pos - t * kKeys;
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
+          for (int j = 0; j < kKeys; ++j)
             if (j > last) x[j] = -CUDART_INF_F;
         }
         float mx[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) mx[j] = fmaxf(x[j], x[j + 4]);
 #pragma unroll
-        for (int j = 8; j < 128; j += 8)
+        for (int j = 8; j < kKeys; j += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
@@ -568,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ref = m == -CUDART_INF_F ? 0.f : -m;  // (no key seen yet: every weight 0)
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < kKeys; c += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
@@ -583,12 +551,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(bar(ePFull + w));
+        warp_arrive(w ? bar(ePFull) : bar(eGo + go++ % C::kStages));
       }
       if (!ok) break;
       if (!wait_bar(bar(eOFull + w), no & 1, abort, p.status)) break;
       ++no;
       tc_fence_after();
+      // steps of row tile 1 alone, two at most (this row tile's last is done, so their phases have begun)
+      for (int t = n; w == 0 && t < u.n[1]; ++t) warp_arrive(bar(eGo + go++ % C::kStages));
       const float inv = 1.f / (l0 + l1);
       const int row = w * kRows + i;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
@@ -638,19 +608,20 @@ cudaError_t launch_expanded(const ExpandedParams& args, int num_sms, cudaStream_
   // (a scale of zero would make NaN of the masked logits' -inf)
   if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;
   EMaps maps;
-  const cuuint32_t box3[3] = {64, 1, 128}, box2[2] = {64, 128};
-  auto rows3 = [&](CUtensorMap* m, const void* base, int size, long long head_stride, long long stride, int n) {
+  const cuuint32_t qbox[3] = {64, 1, kRows}, kbox[3] = {64, 1, kKeys}, rbox[2] = {64, kKeys};
+  auto rows3 = [&](CUtensorMap* m, const void* base, int size, long long head_stride, long long stride, int n,
+                   const cuuint32_t* box) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(size), static_cast<cuuint64_t>(p.num_heads),
                                 static_cast<cuuint64_t>(n)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(stride) * 2};
-    return encode_bf16(m, base, 3, dims, strides, box3);
+    return encode_bf16(m, base, 3, dims, strides, box);
   };
   const cuuint64_t dims2[2] = {kLatentRope, static_cast<cuuint64_t>(p.num_kv_tokens)};
   const cuuint64_t strides2[1] = {static_cast<cuuint64_t>(p.kr_stride) * 2};
-  if (!rows3(&maps.q, p.q, D + kLatentRope, p.q_head_stride, p.q_stride, p.num_tokens) ||
-      !rows3(&maps.k, p.k, D, p.k_head_stride, p.k_stride, p.num_kv_tokens) ||
-      !rows3(&maps.v, p.v, D, p.v_head_stride, p.v_stride, p.num_kv_tokens) ||
-      !encode_bf16(&maps.kr, p.kr, 2, dims2, strides2, box2))
+  if (!rows3(&maps.q, p.q, D + kLatentRope, p.q_head_stride, p.q_stride, p.num_tokens, qbox) ||
+      !rows3(&maps.k, p.k, D, p.k_head_stride, p.k_stride, p.num_kv_tokens, kbox) ||
+      !rows3(&maps.v, p.v, D, p.v_head_stride, p.v_stride, p.num_kv_tokens, kbox) ||
+      !encode_bf16(&maps.kr, p.kr, 2, dims2, strides2, rbox))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_sms));

@@ -33,9 +33,19 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   __syncwarp();
   return false;
 }
+// The same for one thread.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort != 0) return false;
+  }
+  *abort = 1;
+  flag_error(status, PA_DEV_TIMEOUT);
+  return false;
+}
 // Teardown wait (warp-uniform, bounded, ignores the abort flag).
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i)
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t limit = kWaitLimit) {
+  for (uint32_t i = 0; i < limit; ++i)
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
 }
 // One lane of a converged warp, the same one each time.  MMAs are issued under this and not under
