@@ -14,7 +14,9 @@
 //
 // Roles: warps 0-3 and 4-7 softmax and output of one tile each, a thread a row: no
 // trade between threads; O is rescaled only when a row's maximum grows by more than 2^8.  Warp 8
-// units and copies, warp 9 MMA issue.  A thread holds a row's 96 logits, so the softmax warps take
+// units and copies, warps 9 and 10 MMA issue of one tile each, in turn: a wait costs some 200 cycles even
+// for what is there, so each does its waiting while the other's products run, and hands
+// on the turn before its last four MMAs.  A thread holds a row's 96 logits, so the softmax warps take
 // 208 registers of the 168 that the launch gives every thread, the others 88.
 //
 // Work: units lie on a line in request, head, row order, each as long as its key tiles plus a
@@ -31,7 +33,7 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128, kUnitRows = 256, kKeys = 96;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;  // (and kMmaWarp + 1)
 constexpr int kThreads = 384;
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
 constexpr int kQSlice = kRows * 128, kKSlice = kKeys * 128;  // bytes of 64 numbers of a tile
@@ -64,20 +66,20 @@ struct EUnit {
 
 enum EBar : int {
   eUnitFull = 0,   // [2]
-  eUnitEmpty = 2,  // [2] (8 softmax warps, MMA)
+  eUnitEmpty = 2,  // [2] (8 softmax warps, 2 MMA)
   eQFull = 4,      // [2] TMA, by row tile
   eQEmpty = 6,     // [2] the unit's last S of the row tile done
-  eSFull = 8,      // [2] S done, by row tile (and everything issued before it)
-  ePFull = 10,     // S of row tile 1 read, P written, O rescaled (4 warps)
-  eOFull = 11,     // [2] the unit's last O += done
-  eKFirst = 13,    // the first K landed
+  eSFull = 8,      // [2] S done, by row tile (and O += before it)
+  ePFull = 10,     // [2] S read, P written, O rescaled (4 warps)
+  eOFull = 12,     // [2] the unit's last O += done
   eVLand = 14,     // a V tile whose last rows are zeroed landed
-  eDrain = 15,
-  eGo = 16,        // [4] by stage: all that the products of row tile 0 in a step need: S read, P written, O
-                   //     rescaled (4 warps), V landed, K of the next step landed
-  eKEmpty = 20,    // [4] K read, by stage
-  eVEmpty = 24,    // [4]
-  eNumBars = 28
+  eDrain = 15,     // [2]
+  eKFull = 17,     // [4] K landed, by stage
+  eKEmpty = 21,    // [4] ... and read (both row tiles)
+  eVFull = 25,     // [4]
+  eVEmpty = 29,    // [4]
+  eTurn = 33,      // [2] the row tile's turn to issue (the other's MMA warp)
+  eNumBars = 35
 };
 
 struct ESmall {
@@ -158,9 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < eNumBars; ++i) {
       uint32_t n = 1;
-      if (i == eUnitEmpty || i == eUnitEmpty + 1) n = 9;
-      if (i == ePFull) n = 4;
-      if (i >= eGo && i < eGo + 4) n = 6;
+      if (i == eUnitEmpty || i == eUnitEmpty + 1) n = 10;
+      if (i == ePFull || i == ePFull + 1) n = 4;
+      if ((i >= eKEmpty && i < eKEmpty + 4) || (i >= eVEmpty && i < eVEmpty + 4)) n = 2;
       mbar_init(bar(i), n);
     }
     // (the swizzled tiles need the alignment that the declaration asks for)
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b = nk % C::kStages;
         if (nk >= C::kStages && !wait_bar(bar(eKEmpty + b), (nk / C::kStages - 1) & 1, abort, p.status)) return false;
         if (lane == 0) {
-          const uint32_t full = nk == 0 ? bar(eKFirst) : bar(eGo + (nk - 1) % C::kStages);
+          const uint32_t full = bar(eKFull + b);
           mbar_arrive_expect_tx(full, C::kKBytes);
 #pragma unroll
           for (int s = 0; s < C::kQSlices; ++s) {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a weight of zero meets no NaN
         const int rows = u.seq - t * kKeys;
         const bool trim = rows < kKeys;
-        const uint32_t go = bar(eGo + b), land = trim ? bar(eVLand) : go, dst = sbase + C::kVOff + b * C::kVBytes;
+        const uint32_t full = bar(eVFull + b), land = trim ? bar(eVLand) : full, dst = sbase + C::kVOff + b * C::kVBytes;
         if (lane == 0) {
           mbar_arrive_expect_tx(land, C::kVBytes);
 #pragma unroll
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : "memory");
           }
           fence_proxy_async_smem();
-          warp_arrive(go);
+          warp_arrive(full);
         }
         ++nv;
         return true;
@@ -352,117 +354,102 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       EUnit end{};
       end.r = -1;
-      if (ok && publish(end) && nk > 0) warp_arrive(bar(eGo + (nk - 1) % C::kStages));  // no K behind the last step
+      if (ok) publish(end);
       if (*abort) {  // let every copy issued land before the CTA ends
-        // (a phase of eGo may never complete: the limit outlasts its copies)
-        if (nk > 0) drain_wait(bar(eKFirst), 0);
-        const uint32_t steps = max(nv, nk > 0 ? nk - 1 : 0);
-        for (uint32_t i = steps > C::kStages ? steps - C::kStages : 0; i < steps; ++i)
-          drain_wait(bar(eGo + i % C::kStages), (i / C::kStages) & 1, 1u << 20);
+        for (uint32_t i = nk > C::kStages ? nk - C::kStages : 0; i < nk; ++i)
+          drain_wait(bar(eKFull + i % C::kStages), (i / C::kStages) & 1);
+        for (uint32_t i = nv > C::kStages ? nv - C::kStages : 0; i < nv; ++i)
+          drain_wait(bar(eVFull + i % C::kStages), (i / C::kStages) & 1);
         if (landing) drain_wait(bar(eVLand), nland & 1);
         for (int w = 0; w < 2; ++w)
           if (nq[w] > 0) drain_wait(bar(eQFull + w), (nq[w] - 1) & 1);
       }
       __syncwarp();
-    } else if (warp == kMmaWarp) {
-      // ------------------------------------------------------------ MMA issue
+    } else if (warp <= kMmaWarp + 1) {
+      // ------------------------------------------------------------ MMA issue of one row tile
+      const int w = warp - kMmaWarp;
       constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, 0);
       constexpr uint32_t kIdO = idesc_bf16(kRows, D, 1);
-      const uint64_t dq = smem_desc_sw128(sbase, 16, 1024);
+      const uint64_t dq = smem_desc_sw128(sbase + w * C::kQBytes, 16, 1024);
       const uint64_t dk = smem_desc_sw128(sbase + C::kKOff, 16, 1024);
       const uint64_t dv = smem_desc_sw128(sbase + C::kVOff, kKSlice, 1024);
       auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
-      // One thread does it all.  What a step needs is waited for before its first product, so
-      // that the products of a row tile, O += P V and the next S, are issued in a row: every wait
-      // between them lets the short queue of the tensor cores run dry.
       if (elect_one() && !*abort) {
-        int uc = 0;               // units read
-        int n0 = 0, n1 = 0, t = 0;  // the current step: tile t of a unit
-        uint32_t step = 0;        // its number: its K and V are in stage step % kStages
-        uint32_t np1 = 0;         // P tiles of row tile 1 taken
-        uint32_t nq0 = 0, nq1 = 0;  // Q tiles taken
+        const uint32_t ts = tmem + w * kRows, to = tmem + C::kTmemO + w * D;
+        uint32_t np = 0, nq = 0;  // P tiles and Q tiles so far
         auto wait = [&](int i, uint32_t parity) { return wait_one(bar(i), parity, abort, p.status); };
-        auto fetch = [&](int& a, int& b) {  // the next unit's tiles; 0, 0 at the end
-          const int s = uc & 1;
-          if (!wait(eUnitFull + s, (uc >> 1) & 1)) return false;
-          const bool end = sm.units[s].r < 0;
-          a = end ? 0 : sm.units[s].n[0];
-          b = end ? 0 : sm.units[s].n[1];
-          mbar_arrive(bar(eUnitEmpty + s));
+        int uc = 0;
+        // the next unit's tiles of this row tile, and of the longer one (0: no more units)
+        auto fetch = [&](int& n, int& steps) {
+          const int slot = uc & 1;
+          if (!wait(eUnitFull + slot, (uc >> 1) & 1)) return false;
+          const EUnit& u = sm.units[slot];
+          const bool end = u.r < 0;
+          n = end ? 0 : w ? u.n[1] : u.n[0];
+          steps = end ? 0 : max(u.n[0], u.n[1]);
+          mbar_arrive(bar(eUnitEmpty + slot));
           ++uc;
           return true;
         };
-        auto stage = [](uint32_t i) { return static_cast<int>(i % C::kStages); };
-        // S of row tile w, K from stage b; last: the unit's last of the row tile
-        auto issue_s = [&](int w, int b, bool last) {
+        // S from the stage b of K; the turn goes on before the last slice, unless it is no one's
+        auto issue_s = [&](uint32_t b, bool pass, bool last) {
           // (slices one by one: unrolled, the descriptors of all of them spill, and an MMA waits for its own)
-          uint64_t qb = adv(dq, w * C::kQBytes), kb = adv(dk, b * C::kKBytes);
+          uint64_t qb = dq, kb = adv(dk, b * C::kKBytes);
 #pragma unroll 1
-          for (int s = 0; s < C::kQSlices; ++s) {
+          for (int i = 0; i < C::kQSlices; ++i) {
+            if (i == C::kQSlices - 1 && pass) mbar_arrive(bar(eTurn + (w ^ 1)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              tc_mma_f16(tmem + w * kRows, adv(qb, i * 32), adv(kb, i * 32), kIdS, s > 0 || i > 0);
+            for (int j = 0; j < 4; ++j) tc_mma_f16(ts, adv(qb, j * 32), adv(kb, j * 32), kIdS, i > 0 || j > 0);
             qb = adv(qb, kQSlice);
             kb = adv(kb, kKSlice);
           }
           tc_commit(bar(eSFull + w));
           if (last) tc_commit(bar(eQEmpty + w));
         };
-        // O += P V of row tile w, V from stage b
-        auto issue_o = [&](int w, int b, bool first, bool last) {
-          const uint32_t d = tmem + C::kTmemO + w * D, a = tmem + w * kRows;
-          const uint64_t vb = adv(dv, b * C::kVBytes);
-#pragma unroll
-          for (int i = 0; i < kKeys / 16; ++i)
-            tc_mma_f16_ts(d, a + i * 8, adv(vb, i * 2048), kIdO, !first || i > 0);
-          if (last) tc_commit(bar(eOFull + w));
-        };
-        bool ok = fetch(n0, n1);
-        bool more = ok && n0 + n1 > 0;
-        if (more) {
-          ok = wait(eKFirst, 0) && wait(eQFull, nq0++ & 1);
-          if (ok) issue_s(0, 0, n0 == 1);
-          if (ok && n1 > 0) {
-            ok = wait(eQFull + 1, nq1++ & 1);
-            if (ok) issue_s(1, 0, n1 == 1);
-          }
+        int n = 0, steps = 0, t = 0;
+        bool ok = fetch(n, steps);
+        if (ok && steps > 0) {
+          ok = wait(eKFull, 0) && (n == 0 || wait(eQFull + w, nq++ & 1));
+          if (ok && n > 0) issue_s(0, false, n == 1);
           if (ok) tc_commit(bar(eKEmpty));
         }
-        while (ok && more) {
-          // the next step: its K stands behind this step's V
-          int m0 = n0, m1 = n1, t1 = t + 1;
-          if (t1 >= max(n0, n1)) {
+        // step s: O += P V of its tile, then S of the next step's (a row tile that does not see a
+        // tile waits for it all the same, so that its barriers' phases stay in step)
+        for (uint32_t s = 0; ok && steps > 0; ++s) {
+          const uint32_t b0 = s % C::kStages, b1 = (s + 1) % C::kStages;
+          int n1 = n, steps1 = steps, t1 = t + 1;
+          if (t1 == steps) {
             t1 = 0;
-            if (!fetch(m0, m1)) break;
-            more = m0 + m1 > 0;
+            if (!fetch(n1, steps1)) break;
           }
-          const int b0 = stage(step), b1 = stage(step + 1);
-          const bool s0 = more && t1 < m0, s1 = more && t1 < m1;
-          if (s0 && t1 == 0 && !wait(eQFull, nq0++ & 1)) break;
-          if (!wait(eGo + b0, (step / C::kStages) & 1)) break;
+          const bool with_o = t < n, with_s = t1 < n1;
+          if (steps1 > 0 && !wait(eKFull + b1, ((s + 1) / C::kStages) & 1)) break;
+          if (with_s && t1 == 0 && !wait(eQFull + w, nq++ & 1)) break;
+          if (!wait(eVFull + b0, (s / C::kStages) & 1)) break;
+          if (with_o && !wait(ePFull + w, np++ & 1)) break;
+          if ((w || s) && !wait(eTurn + w, (w ? s : s - 1) & 1)) break;
           tc_fence_after();
-          if (t < n0) issue_o(0, b0, t == 0, t == n0 - 1);
-          if (s0) issue_s(0, b1, t1 == m0 - 1);
-          if (s1 && t1 == 0 && !wait(eQFull + 1, nq1++ & 1)) break;
-          if (t < n1) {
-            if (!wait(ePFull, np1++ & 1)) break;
-            tc_fence_after();
-            issue_o(1, b0, t == 0, t == n1 - 1);
+          if (!with_s) mbar_arrive(bar(eTurn + (w ^ 1)));
+          if (with_o) {
+            const uint64_t vb = adv(dv, b0 * C::kVBytes);
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+              tc_mma_f16_ts(to, ts + i * 8, adv(vb, i * 2048), kIdO, t > 0 || i > 0);
+            if (t == n - 1) tc_commit(bar(eOFull + w));
           }
           tc_commit(bar(eVEmpty + b0));
-          if (s1) issue_s(1, b1, t1 == m1 - 1);
-          if (more) tc_commit(bar(eKEmpty + b1));
-          ++step;
-          n0 = m0;
-          n1 = m1;
+          if (with_s) issue_s(b1, true, t1 == n1 - 1);
+          if (steps1 > 0) tc_commit(bar(eKEmpty + b1));
+          n = n1;
+          steps = steps1;
           t = t1;
         }
       }
       __syncwarp();
       if (*abort) {  // nothing may still run on tensor memory when it is freed
-        if (elect_one()) tc_commit(bar(eDrain));
+        if (elect_one()) tc_commit(bar(eDrain + w));
         __syncwarp();
-        drain_wait(bar(eDrain), 0);
+        drain_wait(bar(eDrain + w), 0);
       }
       __syncwarp();
     }
@@ -475,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // maxima are taken of logits that grow with S: a negative scale turns S over
     const bool minus = p.scale_log2 < 0.f;
     const float scale = fabsf(p.scale_log2);
-    uint32_t ns = 0, no = 0, go = 0;  // S tiles, units and arrivals of this row tile so far
+    uint32_t ns = 0, no = 0;  // S tiles and units of this row tile so far
     bool ok = !*abort;
     for (int uc = 0; ok; ++uc) {
       if (!wait_bar(bar(eUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
@@ -551,14 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(w ? bar(ePFull) : bar(eGo + go++ % C::kStages));
+        warp_arrive(bar(ePFull + w));
       }
       if (!ok) break;
       if (!wait_bar(bar(eOFull + w), no & 1, abort, p.status)) break;
       ++no;
       tc_fence_after();
-      // steps of row tile 1 alone, two at most (this row tile's last is done, so their phases have begun)
-      for (int t = n; w == 0 && t < u.n[1]; ++t) warp_arrive(bar(eGo + go++ % C::kStages));
       const float inv = 1.f / (l0 + l1);
       const int row = w * kRows + i;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
