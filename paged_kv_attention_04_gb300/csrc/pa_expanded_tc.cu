@@ -4,20 +4,20 @@
 //
 // A (query, key) pair costs 2 (2 D + 64) flops and no bytes worth counting, so the tensor cores
 // bound it.  A unit is 256 rows of one head of a request, two tiles of 128 that read every
-// staged K and V tile; while one tile's softmax runs, the tensor cores work on the other's
-// products: S = Q K' (Q and K in shared memory) and O += P V (P in tensor memory, over the S
-// it came from).  The two S and the two O fill tensor memory at D = 128.
-// Shared memory holds the two Q tiles and K and V of two key tiles (four at D = 64), in slices of 64
-// numbers (128-byte swizzle).  Key tiles are of 96 keys so that two fit at D = 128: S costs 56 cycles an
-// MMA instead of 48 for it, but with 128 keys, whose K and V fit one and a half times, the products
-// waited for their loads (4400 cycles a step of 128 keys, ideal 2560).
+// staged K and V tile.  S = Q K' takes Q and K from shared memory, O += P V takes P from tensor memory.
+// A step of 80 keys leaves room in tensor memory for P beside its S (2 x (80 + 40) columns, and the two
+// O in the other half), so the next S is formed while the softmax works on this one, and neither
+// the tensor cores nor the softmax wait for a hand-over.  (With P over S, 96 keys: 2870 cycles a step of
+// which the products are 2112; 128 keys, one and a half stages of K and V: 4400 of 2560.)
+// Shared memory holds the two Q tiles, K of three key tiles and V of two (D = 64: four), in slices of 64
+// numbers (128-byte swizzle).
 //
 // Roles: warps 0-3 and 4-7 softmax and output of one tile each, a thread a row: no
 // trade between threads; O is rescaled only when a row's maximum grows by more than 2^8.  Warp 8
-// units and copies, warps 9 and 10 MMA issue of one tile each, in turn: a wait costs some 200 cycles even
-// for what is there, so each does its waiting while the other's products run, and hands
-// on the turn before its last four MMAs.  A thread holds a row's 96 logits, so the softmax warps take
-// 208 registers of the 168 that the launch gives every thread, the others 88.
+// units and copies of Q and K, warp 11 copies of V, warp 9 issues the S products, warp 10 the O products (while S is formed, shared memory
+// is busy and a wait costs some 200 cycles even for what is there: each hides the other's).
+// A thread holds a row's 80 logits, so the softmax warps take 208 registers of the 168 that the launch
+// gives every thread, the others 88.
 //
 // Work: units lie on a line in request, head, row order, each as long as its key tiles plus a
 // constant; a CTA takes the units whose middle lies in its equal stretch.
@@ -32,8 +32,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kRows = 128, kUnitRows = 256, kKeys = 96;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;  // (and kMmaWarp + 1)
+constexpr int kRows = 128, kUnitRows = 256, kKeys = 80;
+constexpr int kCopyWarp = 8, kSWarp = 9, kOWarp = 10, kVWarp = 11;
 constexpr int kThreads = 384;
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
 constexpr int kQSlice = kRows * 128, kKSlice = kKeys * 128;  // bytes of 64 numbers of a tile
@@ -45,11 +45,14 @@ struct ECfg {
   static constexpr int kQSlices = D / 64 + 1, kVSlices = D / 64;
   static constexpr int kQBytes = kQSlices * kQSlice;
   static constexpr int kKBytes = kQSlices * kKSlice, kVBytes = kVSlices * kKSlice;
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kKOff = 2 * kQBytes, kVOff = kKOff + kStages * kKBytes;
-  static constexpr int kSmallOff = kVOff + kStages * kVBytes;
+  // (S runs a step ahead, so K needs a stage more than V: with two of each 254 us a 2048-token chunk)
+  static constexpr int kKStages = D == 128 ? 3 : 4, kVStages = D == 128 ? 2 : 4;
+  static constexpr int kKOff = 2 * kQBytes, kVOff = kKOff + kKStages * kKBytes;
+  static constexpr int kSmallOff = kVOff + kVStages * kVBytes;
   static constexpr int kSmemBytes = kSmallOff + 1024;
-  static constexpr int kTmemO = 256;
+  // row tile w: S at 128 w, its P behind it, O at 256 + D w
+  static constexpr int kTmemP = kKeys, kTmemO = 256;
+  static_assert(kKeys + kKeys / 2 <= kRows, "P fits behind S");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
 };
 
@@ -66,19 +69,19 @@ struct EUnit {
 
 enum EBar : int {
   eUnitFull = 0,   // [2]
-  eUnitEmpty = 2,  // [2] (8 softmax warps, 2 MMA)
+  eUnitEmpty = 2,  // [2] (8 softmax warps, 2 MMA, V)
   eQFull = 4,      // [2] TMA, by row tile
   eQEmpty = 6,     // [2] the unit's last S of the row tile done
-  eSFull = 8,      // [2] S done, by row tile (and O += before it)
-  ePFull = 10,     // [2] S read, P written, O rescaled (4 warps)
-  eOFull = 12,     // [2] the unit's last O += done
-  eVLand = 14,     // a V tile whose last rows are zeroed landed
-  eDrain = 15,     // [2]
-  eKFull = 17,     // [4] K landed, by stage
-  eKEmpty = 21,    // [4] ... and read (both row tiles)
-  eVFull = 25,     // [4]
-  eVEmpty = 29,    // [4]
-  eTurn = 33,      // [2] the row tile's turn to issue (the other's MMA warp)
+  eSFull = 8,      // [2] S done, by row tile
+  eSRead = 10,     // [2] ... and read (4 warps)
+  ePFull = 12,     // [2] P written, O rescaled (4 warps)
+  eODone = 14,     // [2] O += P V done
+  eVLand = 16,     // a V tile whose last rows are zeroed landed
+  eDrain = 17,     // [2]
+  eKFull = 19,     // [4] K landed, by stage
+  eKEmpty = 23,    // [4] ... and read
+  eVFull = 27,     // [4]
+  eVEmpty = 31,    // [4]
   eNumBars = 35
 };
 
@@ -160,9 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < eNumBars; ++i) {
       uint32_t n = 1;
-      if (i == eUnitEmpty || i == eUnitEmpty + 1) n = 10;
-      if (i == ePFull || i == ePFull + 1) n = 4;
-      if ((i >= eKEmpty && i < eKEmpty + 4) || (i >= eVEmpty && i < eVEmpty + 4)) n = 2;
+      if (i == eUnitEmpty || i == eUnitEmpty + 1) n = 11;
+      if (i >= eSRead && i < eSRead + 4) n = 4;  // (eSRead, ePFull)
       mbar_init(bar(i), n);
     }
     // (the swizzled tiles need the alignment that the declaration asks for)
@@ -233,10 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {
       // ------------------------------------------------------------ units and copies
       int uc = 0;                    // units published
-      uint32_t nk = 0, nv = 0;       // K and V tiles copied
+      uint32_t nk = 0;               // K tiles copied
       uint32_t nq[2] = {0, 0};       // Q tiles copied
-      uint32_t nland = 0;
-      bool landing = false, ok = !*abort;
+      bool ok = !*abort;
       auto publish = [&](const EUnit& u) {
         const int s = uc & 1;
         if (uc >= 2 && !wait_bar(bar(eUnitEmpty + s), ((uc >> 1) - 1) & 1, abort, p.status)) return false;
@@ -263,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       auto load_k = [&](const EUnit& u, int t) {
-        const uint32_t b = nk % C::kStages;
-        if (nk >= C::kStages && !wait_bar(bar(eKEmpty + b), (nk / C::kStages - 1) & 1, abort, p.status)) return false;
+        const uint32_t b = nk % C::kKStages;
+        if (nk >= C::kKStages && !wait_bar(bar(eKEmpty + b), (nk / C::kKStages - 1) & 1, abort, p.status)) return false;
         if (lane == 0) {
           const uint32_t full = bar(eKFull + b);
           mbar_arrive_expect_tx(full, C::kKBytes);
@@ -279,45 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nk;
         return true;
       };
-      auto load_v = [&](const EUnit& u, int t) {
-        const uint32_t b = nv % C::kStages;
-        if (nv >= C::kStages && !wait_bar(bar(eVEmpty + b), (nv / C::kStages - 1) & 1, abort, p.status)) return false;
-        // rows behind the request's last key hold another's values or nothing: zeros, so that
-        // a weight of zero meets no NaN
-        const int rows = u.seq - t * kKeys;
-        const bool trim = rows < kKeys;
-        const uint32_t full = bar(eVFull + b), land = trim ? bar(eVLand) : full, dst = sbase + C::kVOff + b * C::kVBytes;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(land, C::kVBytes);
-#pragma unroll
-          for (int s = 0; s < C::kVSlices; ++s)
-            tma_load_3d(dst + s * kKSlice, &maps.v, s * 64, u.head, u.key0 + t * kKeys, land);
-        }
-        __syncwarp();
-        if (trim) {
-          landing = true;
-          if (!wait_bar(land, nland & 1, abort, p.status)) return false;
-          landing = false;
-          ++nland;
-          for (int i = lane; i < (kKeys - rows) * C::kVSlices * 8; i += 32) {
-            const int c = i % 8, s = i / 8 % C::kVSlices, row = rows + i / (8 * C::kVSlices);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(dst + s * kKSlice + row * 128 + c * 16),
-                         "r"(0u)
-                         : "memory");
-          }
-          fence_proxy_async_smem();
-          warp_arrive(full);
-        }
-        ++nv;
-        return true;
-      };
       auto run = [&](const EUnit& u) {
         const int n = max(u.n[0], u.n[1]);
         if (!publish(u) || !load_k(u, 0) || !load_q(u, 0) || !load_q(u, 1)) return false;
-        for (int t = 0; t < n; ++t) {
-          if (!load_v(u, t)) return false;
-          if (t + 1 < n && !load_k(u, t + 1)) return false;
-        }
+        for (int t = 1; t < n; ++t)
+          if (!load_k(u, t)) return false;
         return true;
       };
       if (ok && sm.start_r >= 0) {
@@ -356,100 +323,135 @@ __global__ void __launch_bounds__(kThreads, 1)
       end.r = -1;
       if (ok) publish(end);
       if (*abort) {  // let every copy issued land before the CTA ends
-        for (uint32_t i = nk > C::kStages ? nk - C::kStages : 0; i < nk; ++i)
-          drain_wait(bar(eKFull + i % C::kStages), (i / C::kStages) & 1);
-        for (uint32_t i = nv > C::kStages ? nv - C::kStages : 0; i < nv; ++i)
-          drain_wait(bar(eVFull + i % C::kStages), (i / C::kStages) & 1);
-        if (landing) drain_wait(bar(eVLand), nland & 1);
+        for (uint32_t i = nk > C::kKStages ? nk - C::kKStages : 0; i < nk; ++i)
+          drain_wait(bar(eKFull + i % C::kKStages), (i / C::kKStages) & 1);
         for (int w = 0; w < 2; ++w)
           if (nq[w] > 0) drain_wait(bar(eQFull + w), (nq[w] - 1) & 1);
       }
       __syncwarp();
-    } else if (warp <= kMmaWarp + 1) {
-      // ------------------------------------------------------------ MMA issue of one row tile
-      const int w = warp - kMmaWarp;
-      constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, 0);
-      constexpr uint32_t kIdO = idesc_bf16(kRows, D, 1);
-      const uint64_t dq = smem_desc_sw128(sbase + w * C::kQBytes, 16, 1024);
-      const uint64_t dk = smem_desc_sw128(sbase + C::kKOff, 16, 1024);
-      const uint64_t dv = smem_desc_sw128(sbase + C::kVOff, kKSlice, 1024);
-      auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
-      if (elect_one() && !*abort) {
-        const uint32_t ts = tmem + w * kRows, to = tmem + C::kTmemO + w * D;
-        uint32_t np = 0, nq = 0;  // P tiles and Q tiles so far
-        auto wait = [&](int i, uint32_t parity) { return wait_one(bar(i), parity, abort, p.status); };
-        int uc = 0;
-        // the next unit's tiles of this row tile, and of the longer one (0: no more units)
-        auto fetch = [&](int& n, int& steps) {
-          const int slot = uc & 1;
-          if (!wait(eUnitFull + slot, (uc >> 1) & 1)) return false;
-          const EUnit& u = sm.units[slot];
-          const bool end = u.r < 0;
-          n = end ? 0 : w ? u.n[1] : u.n[0];
-          steps = end ? 0 : max(u.n[0], u.n[1]);
-          mbar_arrive(bar(eUnitEmpty + slot));
-          ++uc;
-          return true;
-        };
-        // S from the stage b of K; the turn goes on before the last slice, unless it is no one's
-        auto issue_s = [&](uint32_t b, bool pass, bool last) {
-          // (slices one by one: unrolled, the descriptors of all of them spill, and an MMA waits for its own)
-          uint64_t qb = dq, kb = adv(dk, b * C::kKBytes);
-#pragma unroll 1
-          for (int i = 0; i < C::kQSlices; ++i) {
-            if (i == C::kQSlices - 1 && pass) mbar_arrive(bar(eTurn + (w ^ 1)));
+    } else if (warp == kVWarp) {
+      // ------------------------------------------------------------ copies of V
+      uint32_t nv = 0, nland = 0;    // V tiles copied, those of them whose last rows are zeroed
+      bool landing = false, ok = !*abort;
+      auto load_v = [&](const EUnit& u, int t) {
+        const uint32_t b = nv % C::kVStages;
+        if (nv >= C::kVStages && !wait_bar(bar(eVEmpty + b), (nv / C::kVStages - 1) & 1, abort, p.status)) return false;
+        // rows behind the request's last key hold another's values or nothing: zeros, so that
+        // a weight of zero meets no NaN
+        const int rows = u.seq - t * kKeys;
+        const bool trim = rows < kKeys;
+        const uint32_t full = bar(eVFull + b), land = trim ? bar(eVLand) : full, dst = sbase + C::kVOff + b * C::kVBytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(land, C::kVBytes);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) tc_mma_f16(ts, adv(qb, j * 32), adv(kb, j * 32), kIdS, i > 0 || j > 0);
-            qb = adv(qb, kQSlice);
-            kb = adv(kb, kKSlice);
-          }
-          tc_commit(bar(eSFull + w));
-          if (last) tc_commit(bar(eQEmpty + w));
-        };
-        int n = 0, steps = 0, t = 0;
-        bool ok = fetch(n, steps);
-        if (ok && steps > 0) {
-          ok = wait(eKFull, 0) && (n == 0 || wait(eQFull + w, nq++ & 1));
-          if (ok && n > 0) issue_s(0, false, n == 1);
-          if (ok) tc_commit(bar(eKEmpty));
+          for (int s = 0; s < C::kVSlices; ++s)
+            tma_load_3d(dst + s * kKSlice, &maps.v, s * 64, u.head, u.key0 + t * kKeys, land);
         }
-        // step s: O += P V of its tile, then S of the next step's (a row tile that does not see a
-        // tile waits for it all the same, so that its barriers' phases stay in step)
-        for (uint32_t s = 0; ok && steps > 0; ++s) {
-          const uint32_t b0 = s % C::kStages, b1 = (s + 1) % C::kStages;
-          int n1 = n, steps1 = steps, t1 = t + 1;
-          if (t1 == steps) {
-            t1 = 0;
-            if (!fetch(n1, steps1)) break;
+        __syncwarp();
+        if (trim) {
+          landing = true;
+          if (!wait_bar(land, nland & 1, abort, p.status)) return false;
+          landing = false;
+          ++nland;
+          for (int i = lane; i < (kKeys - rows) * C::kVSlices * 8; i += 32) {
+            const int c = i % 8, s = i / 8 % C::kVSlices, row = rows + i / (8 * C::kVSlices);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};\n" ::"r"(dst + s * kKSlice + row * 128 + c * 16),
+                         "r"(0u)
+                         : "memory");
           }
-          const bool with_o = t < n, with_s = t1 < n1;
-          if (steps1 > 0 && !wait(eKFull + b1, ((s + 1) / C::kStages) & 1)) break;
-          if (with_s && t1 == 0 && !wait(eQFull + w, nq++ & 1)) break;
-          if (!wait(eVFull + b0, (s / C::kStages) & 1)) break;
-          if (with_o && !wait(ePFull + w, np++ & 1)) break;
-          if ((w || s) && !wait(eTurn + w, (w ? s : s - 1) & 1)) break;
-          tc_fence_after();
-          if (!with_s) mbar_arrive(bar(eTurn + (w ^ 1)));
-          if (with_o) {
-            const uint64_t vb = adv(dv, b0 * C::kVBytes);
+          fence_proxy_async_smem();
+          warp_arrive(full);
+        }
+        ++nv;
+        return true;
+      };
+      for (int uc = 0; ok; ++uc) {
+        if (!wait_bar(bar(eUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
+        const EUnit u = sm.units[uc & 1];
+        warp_arrive(bar(eUnitEmpty + (uc & 1)));
+        if (u.r < 0) break;
+        for (int t = 0; ok && t < max(u.n[0], u.n[1]); ++t) ok = load_v(u, t);
+      }
+      if (*abort) {
+        for (uint32_t i = nv > C::kVStages ? nv - C::kVStages : 0; i < nv; ++i)
+          drain_wait(bar(eVFull + i % C::kVStages), (i / C::kVStages) & 1);
+        if (landing) drain_wait(bar(eVLand), nland & 1);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ MMA issue, one thread each
+      if (elect_one() && !*abort) {
+        auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
+        auto wait = [&](int i, uint32_t parity) { return wait_one(bar(i), parity, abort, p.status); };
+        uint32_t b = 0, phase = 0;   // stage of the step's K (V), and its round
+        uint32_t num[2] = {0, 0};    // tiles of each row tile so far
+        uint32_t nq[2] = {0, 0};     // Q tiles so far
+        bool ok = true;
+        for (int uc = 0; ok; ++uc) {
+          const int slot = uc & 1;
+          if (!wait(eUnitFull + slot, (uc >> 1) & 1)) break;
+          const bool end = sm.units[slot].r < 0;
+          const int n[2] = {sm.units[slot].n[0], sm.units[slot].n[1]};
+          mbar_arrive(bar(eUnitEmpty + slot));
+          if (end) break;
+          const int steps = max(n[0], n[1]);
+          if (warp == kSWarp) {
+            constexpr uint32_t kId = idesc_bf16(kRows, kKeys, 0);
+            for (int t = 0; ok && t < steps; ++t) {
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              tc_mma_f16_ts(to, ts + i * 8, adv(vb, i * 2048), kIdO, t > 0 || i > 0);
-            if (t == n - 1) tc_commit(bar(eOFull + w));
+              for (int w = 0; w < 2; ++w) {
+                if (!ok || t >= n[w]) continue;
+                if (t == 0) ok = wait(eQFull + w, nq[w]++ & 1);
+                // (phase -1 of a barrier counts as complete)
+                if (ok) ok = wait_both(bar(eKFull + b), phase, bar(eSRead + w), (num[w] - 1) & 1, abort, p.status);
+                if (!ok) continue;
+                ++num[w];
+                tc_fence_after();
+                // (slices one by one: unrolled, the descriptors of all of them spill, and an MMA waits
+                // for its own)
+                uint64_t qb = smem_desc_sw128(sbase + w * C::kQBytes, 16, 1024);
+                uint64_t kb = smem_desc_sw128(sbase + C::kKOff + b * C::kKBytes, 16, 1024);
+#pragma unroll 1
+                for (int i = 0; i < C::kQSlices; ++i) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    tc_mma_f16(tmem + w * kRows, adv(qb, j * 32), adv(kb, j * 32), kId, i > 0 || j > 0);
+                  qb = adv(qb, kQSlice);
+                  kb = adv(kb, kKSlice);
+                }
+                tc_commit(bar(eSFull + w));
+                if (t == n[w] - 1) tc_commit(bar(eQEmpty + w));
+              }
+              if (++b == C::kKStages) b = 0, phase ^= 1;
+            }
+          } else {
+            constexpr uint32_t kId = idesc_bf16(kRows, D, 1);
+            for (int t = 0; ok && t < steps; ++t) {
+              const uint64_t vb = smem_desc_sw128(sbase + C::kVOff + b * C::kVBytes, kKSlice, 1024);
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                if (!ok || t >= n[w]) continue;
+                ok = wait_both(bar(eVFull + b), phase, bar(ePFull + w), num[w]++ & 1, abort, p.status);
+                if (!ok) continue;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i)
+                  tc_mma_f16_ts(tmem + C::kTmemO + w * D, tmem + w * kRows + C::kTmemP + i * 8, adv(vb, i * 2048),
+                                kId, t > 0 || i > 0);
+                tc_commit(bar(eODone + w));
+              }
+              if (ok) tc_commit(bar(eVEmpty + b));
+              if (++b == C::kVStages) b = 0, phase ^= 1;
+            }
           }
-          tc_commit(bar(eVEmpty + b0));
-          if (with_s) issue_s(b1, true, t1 == n1 - 1);
-          if (steps1 > 0) tc_commit(bar(eKEmpty + b1));
-          n = n1;
-          steps = steps1;
-          t = t1;
         }
       }
       __syncwarp();
       if (*abort) {  // nothing may still run on tensor memory when it is freed
-        if (elect_one()) tc_commit(bar(eDrain + w));
+        const int d = eDrain + (warp == kOWarp);
+        if (elect_one()) tc_commit(bar(d));
         __syncwarp();
-        drain_wait(bar(eDrain + w), 0);
+        drain_wait(bar(d), 0);
       }
       __syncwarp();
     }
@@ -462,7 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // maxima are taken of logits that grow with S: a negative scale turns S over
     const bool minus = p.scale_log2 < 0.f;
     const float scale = fabsf(p.scale_log2);
-    uint32_t ns = 0, no = 0;  // S tiles and units of this row tile so far
+    uint32_t ns = 0;    // tiles of this row tile so far
+    uint32_t step = 0;  // steps of both
     bool ok = !*abort;
     for (int uc = 0; ok; ++uc) {
       if (!wait_bar(bar(eUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
@@ -470,20 +473,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(bar(eUnitEmpty + (uc & 1)));
       if (u.r < 0) break;
       const int n = w ? u.n[1] : u.n[0];
-      if (n == 0) continue;  // (row tile 1)
+      const uint32_t first = step;  // the unit's first step
+      if (n == 0) {                 // (row tile 1)
+        step += u.n[0];
+        continue;
+      }
       const int pos = u.pos0 + w * kRows + i;  // keys up to here are seen
-      float m = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+      float m = -CUDART_INF_F, l = 0.f;
       for (int t = 0; t < n; ++t, ++ns) {
         if (!wait_bar(bar(eSFull + w), ns & 1, abort, p.status)) { ok = false; break; }
+        // K is read, unless row tile 1 is still to take it (here, not by a commit more of the issuing thread)
+        if (i == 0 && (w || t >= u.n[1])) mbar_arrive(bar(eKEmpty + step % C::kKStages));
+        ++step;
         tc_fence_after();
         float x[kKeys];
         {
           uint32_t(&r)[kKeys] = reinterpret_cast<uint32_t(&)[kKeys]>(x);
           PA_TMEM_LD32(ts, (r + 0));
           PA_TMEM_LD32(ts + 32, (r + 32));
-          PA_TMEM_LD32(ts + 64, (r + 64));
+          tmem_ld16(ts + 64, reinterpret_cast<uint32_t(&)[16]>(r[64]));
           tmem_wait_ld();
         }
+        tc_fence_before();
+        warp_arrive(bar(eSRead + w));
         if (minus) {
 #pragma unroll
           for (int j = 0; j < kKeys; ++j) x[j] = -x[j];
@@ -506,10 +518,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (top > m + kGrowth) {  // (also the first finite maximum: m = -inf)
           f = ex2(m - top);
           m = top;
-          l0 *= f;
-          l1 *= f;
+          l *= f;
         }
-        // O of earlier tiles takes the new reference (S done: so is every product before it)
+        const float ref = m == -CUDART_INF_F ? 0.f : -m;  // (no key seen yet: every weight 0)
+        uint32_t pk[kKeys / 2];
+#pragma unroll
+        for (int j = 0; j < kKeys; j += 2) {
+          float &a = x[j], &b = x[j + 1];
+          fma2(a, b, scale, ref);
+          a = ex2(a);
+          b = ex2(b);
+          pk[j / 2] = pack_bf16(a, b);
+        }
+        if (ns > 0 && !wait_bar(bar(eODone + w), (ns - 1) & 1, abort, p.status)) { ok = false; break; }
+        tc_fence_after();
         if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -521,30 +543,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(to + c, o);
           }
         }
-        const float ref = m == -CUDART_INF_F ? 0.f : -m;  // (no key seen yet: every weight 0)
-#pragma unroll
-        for (int c = 0; c < kKeys; c += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float &a = x[c + j], &b = x[c + j + 1];
-            fma2(a, b, scale, ref);
-            a = ex2(a);
-            b = ex2(b);
-            add2(l0, l1, a, b);
-            pk[j / 2] = pack_bf16(a, b);
-          }
-          tmem_st16(ts + c / 2, pk);
-        }
+        PA_TMEM_ST32(ts + C::kTmemP, pk);
+        tmem_st8(ts + C::kTmemP + 32, pk + 32);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(bar(ePFull + w));
+        // the sums while the products run
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kKeys; j += 4) {
+          add2(sum[0], sum[1], x[j], x[j + 1]);
+          add2(sum[2], sum[3], x[j + 2], x[j + 3]);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
       if (!ok) break;
-      if (!wait_bar(bar(eOFull + w), no & 1, abort, p.status)) break;
-      ++no;
+      step = first + max(u.n[0], u.n[1]);
+      if (!wait_bar(bar(eODone + w), (ns - 1) & 1, abort, p.status)) break;
       tc_fence_after();
-      const float inv = 1.f / (l0 + l1);
+      const float inv = 1.f / l;
       const int row = w * kRows + i;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
                            (static_cast<long long>(u.row0 + row) * p.num_heads + u.head) * D;

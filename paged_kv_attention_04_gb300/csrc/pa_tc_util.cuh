@@ -17,10 +17,23 @@ namespace tc {
 
 constexpr uint32_t kWaitLimit = 1u << 24;
 
+// Whether phase `parity` of `bar` is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Warp-uniform bounded wait for phase `parity` of `bar`; false after a timeout (which it
 // records) or once another role has given up.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort,
                                          int32_t* status) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     const bool ok = mbar_try_wait(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
@@ -35,6 +48,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 }
 // The same for one thread.
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort != 0) return false;
@@ -43,8 +57,23 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile
   flag_error(status, PA_DEV_TIMEOUT);
   return false;
 }
+// ... and for two barriers at once: a wait costs some 150 cycles even for what is there, two of them
+// polled together no more than one.
+__device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                          volatile int* abort, int32_t* status) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    const bool a = mbar_test(bar0, parity0), b = mbar_test(bar1, parity1);
+    if (a && b) return true;
+    if (*abort != 0) return false;
+  }
+  *abort = 1;
+  flag_error(status, PA_DEV_TIMEOUT);
+  return false;
+}
 // Teardown wait (warp-uniform, bounded, ignores the abort flag).
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t limit = kWaitLimit) {
+#pragma unroll 1
   for (uint32_t i = 0; i < limit; ++i)
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
 }
@@ -80,18 +109,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t w;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
-}
-
-// Whether phase `parity` of `bar` is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // TMEM loads, 16 lanes x 8 columns a step in the matrix fragment layout: register 4 i + j of
@@ -131,6 +148,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 
 // ---- host: tensor maps
