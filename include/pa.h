@@ -433,14 +433,21 @@ typedef struct {
  *   max_query_len, max_kv_len  host upper bounds of L and S
  * Pointers are 16-byte aligned, strides multiples of 16 bytes.  Requests with L < 1,
  * L > S or above a bound set PA_DEV_LENGTHS and their rows are left unwritten; bad start arrays
- * set PA_DEV_QSL and nothing is written.  No workspace.  Rounding, NaN and early reads (of
- * both start arrays) as for pa_latent_forward.
+ * set PA_DEV_QSL and nothing is written.  Rounding, NaN and early reads (of both start arrays)
+ * as for pa_latent_forward.
+ *   workspace  device scratch of pa_expanded_workspace_size bytes, 256-byte aligned, with which a
+ *              few long rows tiles are cut over the GPU's SMs; NULL: they are not (the results
+ *              differ in rounding alone, the time by up to a fifth and more)
  */
 int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, const void* v,
                         const int32_t* query_start_loc, const int32_t* kv_start_loc, int num_seqs,
                         int num_tokens, int num_kv_tokens, int max_query_len, int max_kv_len,
-                        float scale, void* out, const pa_expanded_layout* layout, int32_t* status,
-                        void* stream);
+                        float scale, void* out, void* workspace, size_t workspace_bytes,
+                        const pa_expanded_layout* layout, int32_t* status, void* stream);
+
+/* Bytes of workspace that are of use to pa_expanded_forward with these bounds (the layout's strides
+ * do not matter): 0 where none is, or on bad arguments (see pa_last_error). */
+size_t pa_expanded_workspace_size(const pa_expanded_layout* layout, int num_tokens, int max_kv_len);
 
 /* Message of the last failing call on this thread ("" if none). */
 const char* pa_last_error(void);

@@ -9,7 +9,8 @@ from .binding import (PA_BF16, PA_DEV_BLOCK_RANGE, PA_DEV_CAPACITY, PA_DEV_LENGT
                       PA_ROPE_HALVES, PA_ROPE_PAIRS, PaError,
                       alloc_latent_workspace, alloc_workspace, cache_shape, last_error, latent_cache_shape,
                       latent_layout_of, layout_of, lib, make_latent_layout, make_layout,
-                      pa_cache_read, pa_cache_write, pa_expanded_forward, pa_expanded_layout, pa_forward,
+                      pa_cache_read, pa_cache_write, pa_expanded_forward, pa_expanded_layout,
+                      pa_expanded_workspace_size, pa_forward,
                       pa_forward_noalloc, pa_forward_workspace_size, pa_latent_forward, pa_latent_layout,
                       pa_latent_read, pa_latent_workspace_size, pa_latent_write, pa_layout, pa_rope,
                       pa_rope_cache_write,
@@ -22,7 +23,8 @@ __all__ = ["PA_BF16", "PA_DEV_BLOCK_RANGE", "PA_DEV_CAPACITY", "PA_DEV_LENGTHS",
            "PA_ROPE_HALVES", "PA_ROPE_PAIRS", "PaError",
            "alloc_latent_workspace", "alloc_workspace", "cache_shape", "last_error", "latent_cache_shape",
            "latent_layout_of", "layout_of", "lib", "make_latent_layout", "make_layout",
-           "pa_cache_read", "pa_cache_write", "pa_expanded_forward", "pa_expanded_layout", "pa_forward",
+           "pa_cache_read", "pa_cache_write", "pa_expanded_forward", "pa_expanded_layout",
+           "pa_expanded_workspace_size", "pa_forward",
            "pa_forward_noalloc", "pa_forward_workspace_size", "pa_latent_forward", "pa_latent_layout",
            "pa_latent_read", "pa_latent_workspace_size", "pa_latent_write", "pa_layout", "pa_rope",
            "pa_rope_cache_write",

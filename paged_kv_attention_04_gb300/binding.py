@@ -88,8 +88,10 @@ def lib() -> ctypes.CDLL:
         L.pa_latent_forward.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, f32, vp, vp, sz, llp,
                                         vp, vp]
         L.pa_latent_forward.restype = i32
-        L.pa_expanded_forward.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, elp,
-                                          vp, vp]
+        L.pa_expanded_forward.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, vp, sz,
+                                          elp, vp, vp]
+        L.pa_expanded_workspace_size.argtypes = [elp, i32, i32]
+        L.pa_expanded_workspace_size.restype = sz
         L.pa_expanded_forward.restype = i32
         L.pa_forward_workspace_size.argtypes = [lp, i32, i32, i32]
         L.pa_forward_workspace_size.restype = sz
@@ -553,14 +555,16 @@ def pa_latent_forward(q, cache, block_tables, seq_lens, query_start_loc, max_que
 
 
 def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max_query_len: int,
-                        max_kv_len: int, scale: float, out, status: torch.Tensor | None = None,
-                        stream=None) -> None:
+                        max_kv_len: int, scale: float, out, workspace: torch.Tensor | None = None,
+                        status: torch.Tensor | None = None, stream=None) -> None:
     """Attention in the expanded form: q [T, H, D + 64] against the keys [k_nope [Tk, H, D], k_rope
     [Tk, 64] (shared by the heads)] and values v [Tk, H, D] of ragged requests, causal
     from the bottom right; out [T, H, D].  q, k_nope, k_rope and v may be slices (last
-    dimension contiguous)."""
+    dimension contiguous).  A workspace of pa_expanded_workspace_size bytes is taken from torch's
+    allocator for the call where none is given and it is of use."""
     dev = _on_one_device(strided=("q", "k_nope", "k_rope", "v"), q=q, k_nope=k_nope, k_rope=k_rope, v=v,
-                         query_start_loc=query_start_loc, kv_start_loc=kv_start_loc, out=out, status=status)
+                         query_start_loc=query_start_loc, kv_start_loc=kv_start_loc, out=out,
+                         workspace=workspace, status=status)
     _int32(query_start_loc=query_start_loc, kv_start_loc=kv_start_loc)
     if q.dim() != 3 or k_nope.dim() != 3 or q.dtype not in _DTYPES:
         raise PaError(PA_ERR_INVALID, f"q is {q.dtype} {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}: expected "
@@ -577,6 +581,25 @@ def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max
     layout = pa_expanded_layout(h, d, rs, _DTYPES[q.dtype], _stride(q, 0, h * (d + rs)), _stride(q, 1, d + rs),
                                 _stride(k_nope, 0, h * d), _stride(k_nope, 1, d), _stride(k_rope, 0, rs),
                                 _stride(v, 0, h * d), _stride(v, 1, d))
+    if workspace is None:
+        size = lib().pa_expanded_workspace_size(ctypes.byref(layout), n, int(max_kv_len))
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            if stream is not None:  # its memory may be given out again when that stream is done
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                        else torch.cuda.ExternalStream(int(stream), device=q.device))
     _launch(lib().pa_expanded_forward, dev, stream, _ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v),
             _ptr(query_start_loc), _ptr(kv_start_loc), b, n, tk, int(max_query_len), int(max_kv_len),
-            float(scale), _ptr(out), ctypes.byref(layout), _ptr(status))
+            float(scale), _ptr(out), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            ctypes.byref(layout), _ptr(status))
+
+
+def pa_expanded_workspace_size(num_heads: int, head_size: int, num_tokens: int, max_kv_len: int,
+                               dtype=torch.bfloat16, rope_size: int = 64) -> int:
+    """Bytes of workspace that are of use to pa_expanded_forward (0: none)."""
+    layout = pa_expanded_layout(num_heads, head_size, rope_size, _DTYPES[dtype])
+    n = lib().pa_expanded_workspace_size(ctypes.byref(layout), int(num_tokens), int(max_kv_len))
+    if n == 0 and last_error():
+        raise PaError(PA_ERR_INVALID, last_error())
+    return int(n)

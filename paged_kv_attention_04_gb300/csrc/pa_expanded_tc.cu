@@ -20,7 +20,9 @@
 // gives every thread, the others 88.
 //
 // Work: units lie on a line in request, head, row order, each as long as its key tiles plus a
-// constant; a CTA takes the units whose middle lies in its equal stretch.
+// constant, and a CTA takes an equal stretch. Where a CTA gets many units the stretches end at
+// the nearest unit; where it gets a few long ones they are cut, their pieces leave partial
+// states (two a CTA at most) and a second kernel joins them in order.
 #include <math_constants.h>
 
 #include "pa_latent.h"
@@ -39,6 +41,9 @@ constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x
 constexpr int kQSlice = kRows * 128, kKSlice = kKeys * 128;  // bytes of 64 numbers of a tile
 constexpr float kGrowth = 8.f;
 constexpr int kUnitCost = 2;       // what a unit costs beside its key tiles
+constexpr int kMinPiece = 6;       // fewest key tiles of a piece
+constexpr int kCutKeys = 1024;     // units are cut where a request may be this long ...
+constexpr int kCutUnits = 5;       // ... and a CTA gets fewer units than this
 
 template <int D>
 struct ECfg {
@@ -64,7 +69,9 @@ struct EUnit {
   int pos0;    // key position of the first row
   int key0;    // first key of the request in the step
   int seq;     // keys of the request
-  int n[2];    // key tiles of each row tile
+  int t0;      // first key tile
+  int n[2];    // key tiles of each row tile, from t0 on
+  int slot;    // partial state, -1: the whole unit
 };
 
 enum EBar : int {
@@ -89,9 +96,9 @@ struct ESmall {
   uint64_t bars[eNumBars];
   EUnit units[2];
   long long sums[kThreads / 32];
-  long long start_pos;
+  long long start_pos, total;
   uint32_t tmem;
-  int abort, bad, start_r;
+  int abort, bad, start_r, ctas;
 };
 static_assert(sizeof(ESmall) <= 1024, "small shared memory");
 
@@ -210,8 +217,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     before -= mine;
     if (sm.bad) total = 0;
-    lo = total * blockIdx.x / gridDim.x;
-    hi = total * (blockIdx.x + 1) / gridDim.x;
+    // (cut units: every stretch is long enough for a piece)
+    const long long ctas = p.part_acc ? max(1LL, min(static_cast<long long>(gridDim.x), total / (kUnitCost + kMinPiece)))
+                                      : gridDim.x;
+    if (blockIdx.x < ctas) {
+      lo = total * blockIdx.x / ctas;
+      hi = total * (blockIdx.x + 1) / ctas;
+    }
+    if (tid == 0) {
+      sm.total = total;
+      sm.ctas = static_cast<int>(ctas);
+    }
     if (lo < hi && before <= lo && lo < before + mine) {
       long long pos = before;
       for (int r = ra; r < rb; ++r) {
@@ -238,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t nk = 0;               // K tiles copied
       uint32_t nq[2] = {0, 0};       // Q tiles copied
       bool ok = !*abort;
+      if (lane == 0 && p.recs) p.recs[blockIdx.x * kLatentRecWords + 3] = 0;
       auto publish = [&](const EUnit& u) {
         const int s = uc & 1;
         if (uc >= 2 && !wait_bar(bar(eUnitEmpty + s), ((uc >> 1) - 1) & 1, abort, p.status)) return false;
@@ -282,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto run = [&](const EUnit& u) {
         const int n = max(u.n[0], u.n[1]);
-        if (!publish(u) || !load_k(u, 0) || !load_q(u, 0) || !load_q(u, 1)) return false;
+        if (!publish(u) || !load_k(u, u.t0) || !load_q(u, 0) || !load_q(u, 1)) return false;
         for (int t = 1; t < n; ++t)
-          if (!load_k(u, t)) return false;
+          if (!load_k(u, u.t0 + t)) return false;
         return true;
       };
       if (ok && sm.start_r >= 0) {
@@ -299,10 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (at >= hi) break;
             for (int m = 0; ok && m < s.tiles; ++m) {
               const int len = unit_len(s, m);
-              const long long middle = at + len / 2;
+              const long long at0 = at;
               at += len;
-              if (middle < lo) continue;
-              if (middle >= hi) break;
+              if (at <= lo) continue;
+              if (at0 >= hi) break;
+              // where a border of the line cuts the unit: 0 (in front of it) .. len (behind it)
+              auto cut = [&](long long x) {
+                if (x <= at0) return 0;
+                if (x >= at) return len;
+                const int rel = static_cast<int>(x - at0);
+                if (!p.part_acc) return 2 * rel > len ? len : 0;
+                return rel < kUnitCost + kMinPiece ? 0 : len - rel < kMinPiece ? len : rel;
+              };
+              const int c0 = cut(lo), c1 = cut(hi);
+              if (c0 >= c1) continue;
               EUnit u;
               u.r = r;
               u.head = h;
@@ -311,8 +338,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               u.pos0 = s.S - s.L + m * kUnitRows;
               u.key0 = s.ka;
               u.seq = s.S;
-              u.n[0] = tiles_to(u.pos0 + min(kRows, u.rows) - 1);
-              u.n[1] = u.rows > kRows ? tiles_to(u.pos0 + u.rows - 1) : 0;
+              const int t1 = c1 == len ? len - kUnitCost : c1 - kUnitCost;
+              u.t0 = c0 == 0 ? 0 : c0 - kUnitCost;
+              u.n[0] = max(0, min(t1, tiles_to(u.pos0 + min(kRows, u.rows) - 1)) - u.t0);
+              u.n[1] = u.rows > kRows ? t1 - u.t0 : 0;
+              const bool whole = c0 == 0 && c1 == len;
+              u.slot = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (c0 == 0);
+              if (!whole && c0 == 0 && lane == 0) {
+                int pieces = 2;  // and one for every later border inside
+                for (int c = blockIdx.x + 2; c < sm.ctas; ++c, ++pieces)
+                  if (cut(sm.total * c / sm.ctas) == len) break;
+                int* rec = p.recs + blockIdx.x * kLatentRecWords;
+                rec[0] = u.row0;
+                rec[1] = u.rows;
+                rec[2] = h;
+                rec[3] = pieces;
+              }
               ok = run(u);
             }
           }
@@ -370,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const EUnit u = sm.units[uc & 1];
         warp_arrive(bar(eUnitEmpty + (uc & 1)));
         if (u.r < 0) break;
-        for (int t = 0; ok && t < max(u.n[0], u.n[1]); ++t) ok = load_v(u, t);
+        for (int t = 0; ok && t < max(u.n[0], u.n[1]); ++t) ok = load_v(u, u.t0 + t);
       }
       if (*abort) {
         for (uint32_t i = nv > C::kVStages ? nv - C::kVStages : 0; i < nv; ++i)
@@ -474,8 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u.r < 0) break;
       const int n = w ? u.n[1] : u.n[0];
       const uint32_t first = step;  // the unit's first step
-      if (n == 0) {                 // (row tile 1)
-        step += u.n[0];
+      if (n == 0) {                 // (no rows, or no key of the piece)
+        step += max(u.n[0], u.n[1]);
+        if (u.slot >= 0) p.part_ml[static_cast<long long>(u.slot) * kUnitRows + w * kRows + i] = make_float2(-CUDART_INF_F, 0.f);
         continue;
       }
       const int pos = u.pos0 + w * kRows + i;  // keys up to here are seen
@@ -500,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kKeys; ++j) x[j] = -x[j];
         }
-        if ((t + 1) * kKeys - 1 > u.pos0 + w * kRows) {
-          const int last = pos - t * kKeys;
+        if ((u.t0 + t + 1) * kKeys - 1 > u.pos0 + w * kRows) {
+          const int last = pos - (u.t0 + t) * kKeys;
 #pragma unroll
           for (int j = 0; j < kKeys; ++j)
             if (j > last) x[j] = -CUDART_INF_F;
@@ -561,8 +603,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       step = first + max(u.n[0], u.n[1]);
       if (!wait_bar(bar(eODone + w), (ns - 1) & 1, abort, p.status)) break;
       tc_fence_after();
-      const float inv = 1.f / l;
       const int row = w * kRows + i;
+      if (u.slot >= 0) {
+        // (chunks of 4 numbers by row: a warp's lanes write side by side)
+        const long long base = static_cast<long long>(u.slot) * kUnitRows;
+        float4* part = p.part_acc + base * (D / 4) + row;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          PA_TMEM_LD32(to + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            part[(c + j) / 4 * kUnitRows] = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                        __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+        }
+        p.part_ml[base + row] = make_float2(m, l);
+        tc_fence_before();
+        continue;
+      }
+      const float inv = 1.f / l;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
                            (static_cast<long long>(u.row0 + row) * p.num_heads + u.head) * D;
 #pragma unroll 1
@@ -589,6 +649,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of cut units, in the order of their keys: 8 CTAs a record of 32 rows each, a lane
+// a row, a warp D / 8 of its numbers.
+template <int D>
+__global__ void __launch_bounds__(256) expanded_join_kernel(const ExpandedParams p) {
+  constexpr int kVec = D / 32;  // float4 of a thread
+  wait_prior_grid();
+  const int* rec = p.recs + blockIdx.x * kLatentRecWords;
+  const int pieces = rec[3], row = blockIdx.y * 32 + (threadIdx.x & 31), chunk = (threadIdx.x >> 5) * kVec;
+  if (pieces == 0 || row >= rec[1]) return;
+  float m = -CUDART_INF_F, l = 0.f;
+  float4 acc[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < pieces; ++k) {
+    // the first CTA's slot 1, then slot 0 of the following ones
+    const long long base = (static_cast<long long>(blockIdx.x + k) * 2 + (k == 0)) * kUnitRows;
+    const float2 ml = p.part_ml[base + row];
+    if (ml.y == 0.f) continue;  // no key of the piece is seen
+    const float nm = fmaxf(m, ml.x);
+    const float fa = m == nm ? 1.f : ex2(m - nm), fb = ml.x == nm ? 1.f : ex2(ml.x - nm);
+    m = nm;
+    l = l * fa + ml.y * fb;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float4 x = p.part_acc[base * (D / 4) + (chunk + i) * kUnitRows + row];
+      acc[i].x = acc[i].x * fa + x.x * fb;
+      acc[i].y = acc[i].y * fa + x.y * fb;
+      acc[i].z = acc[i].z * fa + x.z * fb;
+      acc[i].w = acc[i].w * fa + x.w * fb;
+    }
+  }
+  const float inv = 1.f / l;
+  uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
+                                        (static_cast<long long>(rec[0] + row) * p.num_heads + rec[2]) * D) + chunk;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+    out[i] = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
 }
 
 namespace {
@@ -626,7 +726,8 @@ cudaError_t launch_expanded(const ExpandedParams& args, int num_sms, cudaStream_
       !encode_bf16(&maps.kr, p.kr, 2, dims2, strides2, rbox))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
+  const unsigned ctas = num_sms < kLatentMaxCtas ? num_sms : kLatentMaxCtas;
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
@@ -635,10 +736,20 @@ cudaError_t launch_expanded(const ExpandedParams& args, int num_sms, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, expanded_tc_kernel<D>, p, maps);
+  e = cudaLaunchKernelEx(&cfg, expanded_tc_kernel<D>, p, maps);
+  if (e != cudaSuccess || !p.part_acc) return e;
+  cfg.gridDim = dim3(ctas, kUnitRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, expanded_join_kernel<D>, p);
 }
 
 }  // namespace
+
+size_t expanded_tc_partial_rows(int num_heads, int num_tokens, int max_kv_len) {
+  const long long units = static_cast<long long>(num_heads) * ((num_tokens + kUnitRows - 1) / kUnitRows);
+  return max_kv_len < kCutKeys || units >= kCutUnits * kLatentMaxCtas ? 0 : 2 * kLatentMaxCtas * kUnitRows;
+}
 
 cudaError_t launch_expanded_tc(const ExpandedParams& p, int head_size, int num_sms, cudaStream_t stream) {
   return head_size == 128 ? launch_expanded<128>(p, num_sms, stream) : launch_expanded<64>(p, num_sms, stream);

@@ -57,6 +57,10 @@ struct ExpandedParams {
   long long q_stride, q_head_stride, k_stride, k_head_stride, kr_stride, v_stride, v_head_stride;
   float scale_log2;
   int32_t* status;
+  // bf16: partial states of units cut in pieces, and per CTA a record; null: units are not cut
+  float4* part_acc;   // [slot][D / 4][rows of a unit]
+  float2* part_ml;    // [slot][rows]: maximum, sum
+  int* recs;
 };
 
 // fp32: CUDA cores.
@@ -66,6 +70,8 @@ cudaError_t launch_expanded_cc(const ExpandedParams& p, int head_size, cudaStrea
 size_t latent_tc_partial_rows(int num_heads, int max_query_len);
 // bf16: tensor cores (tcgen05).
 cudaError_t launch_latent_tc(const LatentParams& p, int latent_size, int num_sms, cudaStream_t stream);
+// Rows of partial states that its units may leave; 0 where cutting them is of no use.
+size_t expanded_tc_partial_rows(int num_heads, int num_tokens, int max_kv_len);
 cudaError_t launch_expanded_tc(const ExpandedParams& p, int head_size, int num_sms, cudaStream_t stream);
 
 }  // namespace pa

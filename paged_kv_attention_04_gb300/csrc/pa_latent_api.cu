@@ -214,16 +214,42 @@ int pa_latent_forward(const void* q, const void* cache, const int32_t* block_tab
   return done(launch_latent_tc(p, layout->latent_size, num_sms, st), "latent attention launch");
 }
 
-int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, const void* v,
-                        const int32_t* query_start_loc, const int32_t* kv_start_loc, int num_seqs,
-                        int num_tokens, int num_kv_tokens, int max_query_len, int max_kv_len,
-                        float scale, void* out, const pa_expanded_layout* L, int32_t* status,
-                        void* stream) {
-  set_last_error(PA_OK, "");
+// Regions of pa_expanded_forward's workspace.
+static LatentWs expanded_ws(const pa_expanded_layout* L, int num_tokens, int max_kv_len) {
+  LatentWs w{};
+  const size_t rows = L->dtype == PA_BF16 ? expanded_tc_partial_rows(L->num_heads, num_tokens, max_kv_len) : 0;
+  if (rows == 0) return w;
+  w.ml = align256(rows * L->head_size * sizeof(float));
+  w.recs = align256(w.ml + rows * 2 * sizeof(float));
+  w.total = align256(w.recs + kLatentMaxCtas * kLatentRecWords * sizeof(int));
+  return w;
+}
+
+static int check_expanded(const pa_expanded_layout* L) {
   if (!L) return fail(PA_ERR_INVALID, "layout is NULL");
   if (int rc = check_common(L->dtype, L->num_heads, L->rope_size)) return rc;
   if (L->head_size != 64 && L->head_size != 128)
     return fail(PA_ERR_UNSUPPORTED, "head_size %d (built for 64 and 128)", L->head_size);
+  return PA_OK;
+}
+
+size_t pa_expanded_workspace_size(const pa_expanded_layout* layout, int num_tokens, int max_kv_len) {
+  set_last_error(PA_OK, "");
+  if (check_expanded(layout)) return 0;
+  if (num_tokens < 0 || max_kv_len < 0) {
+    fail(PA_ERR_INVALID, "negative size");
+    return 0;
+  }
+  return expanded_ws(layout, num_tokens, max_kv_len).total;
+}
+
+int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, const void* v,
+                        const int32_t* query_start_loc, const int32_t* kv_start_loc, int num_seqs,
+                        int num_tokens, int num_kv_tokens, int max_query_len, int max_kv_len,
+                        float scale, void* out, void* workspace, size_t workspace_bytes,
+                        const pa_expanded_layout* L, int32_t* status, void* stream) {
+  set_last_error(PA_OK, "");
+  if (int rc = check_expanded(L)) return rc;
   if (num_seqs < 0 || num_tokens < 0 || num_kv_tokens < 0 || max_query_len < 0 || max_kv_len < 0)
     return fail(PA_ERR_INVALID, "negative size argument");
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
@@ -250,10 +276,20 @@ int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, c
     return fail(PA_ERR_INVALID, "step too large for one call");
   int num_sms = 0;
   if (int rc = sms_of_current_device(&num_sms)) return rc;
-  const ExpandedParams p{q, k_nope, k_rope, v, query_start_loc, kv_start_loc, out, num_seqs, num_tokens,
+  if (workspace && !aligned(workspace, 256)) return fail(PA_ERR_INVALID, "workspace must be 256-byte aligned");
+  const LatentWs w = expanded_ws(L, num_tokens, max_kv_len);
+  if (workspace && workspace_bytes < w.total)
+    return fail(PA_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
+  ExpandedParams p{q, k_nope, k_rope, v, query_start_loc, kv_start_loc, out, num_seqs, num_tokens,
                          num_kv_tokens, max_query_len, max_kv_len, L->num_heads, L->q_stride, L->q_head_stride,
                          L->k_stride, L->k_head_stride, L->kr_stride, L->v_stride, L->v_head_stride,
-                         scale * 1.4426950408889634f, status};
+                         scale * 1.4426950408889634f, status, nullptr, nullptr, nullptr};
+  if (workspace && w.total) {
+    char* ws = static_cast<char*>(workspace);
+    p.part_acc = reinterpret_cast<float4*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    p.recs = reinterpret_cast<int*>(ws + w.recs);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return done(L->dtype == PA_F32 ? launch_expanded_cc(p, L->head_size, st)
                                  : launch_expanded_tc(p, L->head_size, num_sms, st),

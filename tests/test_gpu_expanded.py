@@ -91,6 +91,25 @@ def test_long_prompts():
     attend(Prompts(40, 64, [900, 300], [900, 1300], seed=3))
 
 
+@pytest.mark.parametrize("heads,size,q_lens,seq_lens", [
+    (1, 128, [300], [5000]), (3, 64, [700, 1], [2100, 3000]), (2, 128, [130, 257, 40], [1500, 257, 4100]),
+    (24, 128, [1000], [1000]), (16, 64, [900], [3700])])
+def test_cut_units(heads, size, q_lens, seq_lens):
+    """Few units of many tiles, in pieces over the SMs; with a caller's workspace, filled with anything, too."""
+    step = Prompts(heads, size, q_lens, seq_lens, seed=20)
+    need = P.pa_expanded_workspace_size(heads, size, step.tokens, max(seq_lens)) if max(seq_lens) >= 1024 else 0
+    assert (need > 0) == (max(seq_lens) >= 1024)
+    d = attend(step)
+    first = d["out"].clone()
+    ws = torch.randint(0, 256, (max(need, 256),), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        d["out"].zero_()
+        P.pa_expanded_forward(d["q"], d["k"], d["kr"], d["v"], d["qsl"], d["kvsl"], max(q_lens), max(seq_lens), step.scale,
+                              d["out"], workspace=ws, status=d["status"])
+        torch.cuda.synchronize()
+        assert torch.equal(d["out"], first) and int(d["status"].item()) == 0
+
+
 def test_many_requests():
     n = [1 + i % 40 for i in range(500)]
     attend(Prompts(2, 64, n, [x + 3 * (i % 7) for i, x in enumerate(n)], seed=4))
