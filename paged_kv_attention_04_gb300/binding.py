@@ -128,17 +128,17 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _on_one_device(strided=(), **tensors) -> int:
-    """Every tensor argument must be a CUDA tensor, contiguous unless its name is
-    in `strided`, all on one device (a host pointer would reach the kernels
-    unchecked).  Returns the device's index."""
+def _on_one_device(**tensors) -> int:
+    """Every tensor argument must be a contiguous CUDA tensor, all on one
+    device (a host pointer would reach the kernels unchecked).  Returns the
+    device's index."""
     dev = None
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise PaError(PA_ERR_INVALID, f"{name} is not a CUDA tensor")
-        if name not in strided and not t.is_contiguous():
+        if not t.is_contiguous():
             raise PaError(PA_ERR_INVALID, f"{name} is not contiguous")
         d = t.get_device()
         if dev is None:
@@ -358,54 +358,95 @@ def alloc_workspace(layout: pa_layout, num_seqs: int, num_tokens: int, max_seq_l
 
 # ---------------------------------------------------------------- rotation and latent attention
 
-def _want(name: str, t, dtype, shape, strided: int | None = None) -> None:
-    """t must have this type and shape; with `strided`, its last `strided` dimensions
-    must lie side by side (the ones before may have any stride)."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+# Small calls are bound by their host time, so what passes is checked by few comparisons a
+# tensor, and only what does not is looked into (_explain).
+
+def _explain(name: str, t, dev: int, dtype, shape, inner: int | None) -> None:
+    d = t.get_device()
+    if d < 0:
+        raise PaError(PA_ERR_INVALID, f"{name} is not a CUDA tensor")
+    if d != dev:
+        raise PaError(PA_ERR_INVALID, f"{name} is on cuda:{d}, expected cuda:{dev}")
+    if t.dtype is not dtype or t.shape != shape:
         raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
-    if strided is not None:
-        step = 1
-        for n, s in zip(reversed(t.shape[-strided:]), reversed(t.stride()[-strided:])):
-            if n != 1 and s != step:
-                raise PaError(PA_ERR_INVALID, f"{name}: its last {strided} dimensions must be contiguous, "
-                                              f"strides {t.stride()}")
-            step *= n
+    if inner is None:
+        raise PaError(PA_ERR_INVALID, f"{name} is not contiguous")
+    raise PaError(PA_ERR_INVALID, f"{name}: its last {inner} dimensions must be contiguous, strides {t.stride()}")
+
+
+def _device(name: str, t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _explain(name, t, dev, t.dtype, t.shape, None)
+    return dev
+
+
+def _whole(name: str, t, dev: int, dtype, shape) -> int:
+    """Pointer of a contiguous tensor of this device, type and shape."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _explain(name, t, dev, dtype, shape, None)
+    return t.data_ptr()
+
+
+def _rows(name: str, t, dev: int, dtype, shape, inner: int, step: int) -> int:
+    """Token stride of a tensor [tokens, ...] whose last `inner` dimensions lie side by side, `step`
+    elements in all (a single token's is never stepped over)."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _explain(name, t, dev, dtype, shape, inner)
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1 or inner == 2 and shape[-2] > 1 and st[-2] != shape[-1]:
+        _explain(name, t, dev, dtype, shape, inner)
+    return st[0] if shape[0] > 1 else step
+
+
+def _heads(name: str, t, dev: int, dtype, shape) -> tuple:
+    """Token and head strides of a tensor [tokens, heads, size] whose last dimension is contiguous."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _explain(name, t, dev, dtype, shape, 1)
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and shape[2] > 1:
+        _explain(name, t, dev, dtype, shape, 1)
+    if shape[1] <= 1:
+        s1 = shape[2]
+    return (s0 if shape[0] > 1 else s1 * shape[1]), s1
+
+
+def _list_of(name: str, t, dev: int, dtype, least: int, what: str) -> int:
+    """Pointer of a contiguous array of at least `least` numbers."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _explain(name, t, dev, dtype, t.shape, None)
+    if t.numel() < least:
+        raise PaError(PA_ERR_INVALID, f"{t.numel()} {what} for {least} tokens")
+    return t.data_ptr()
+
+
+def _status(status, dev: int) -> int | None:
+    if status is None:
+        return None
+    if status.get_device() != dev or status.dtype is not torch.int32 or status.numel() < 1:
+        _explain("status", status, dev, torch.int32, (1,), None)
+    return status.data_ptr()
+
+
+_TORCH = {PA_F32: torch.float32, PA_BF16: torch.bfloat16}
 
 
 def _torch_dtype(code: int):
-    return torch.float32 if code == PA_F32 else torch.bfloat16
+    return _TORCH[code] if code in _TORCH else torch.bfloat16  # (a bad code is refused by the library)
 
 
-def _stride(t, dim: int, least: int) -> int:
-    """Stride of a dimension; of one that is never stepped over, one that passes."""
-    return t.stride(dim) if t.shape[dim] > 1 else least
-
-
-def _rope(positions, cos_sin, tokens: int, pairs: bool) -> pa_rope:
-    if positions.dtype != torch.int64:
-        raise PaError(PA_ERR_INVALID, f"positions is {positions.dtype}, expected torch.int64")
-    if positions.numel() < tokens:
-        raise PaError(PA_ERR_INVALID, f"{positions.numel()} positions for {tokens} tokens")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-        raise PaError(PA_ERR_INVALID, f"cos_sin is {cos_sin.dtype} {tuple(cos_sin.shape)}, expected float32 "
-                                      "[max_position, rope_size]")
-    return pa_rope(positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+def _rope(positions, cos_sin, dev: int, tokens: int, pairs: bool) -> pa_rope:
+    at = _list_of("positions", positions, dev, torch.int64, tokens, "positions")
+    if cos_sin.dim() != 2:
+        raise PaError(PA_ERR_INVALID, f"cos_sin is {tuple(cos_sin.shape)}, expected [max_position, rope_size]")
+    rows, size = cos_sin.shape
+    return pa_rope(at, _whole("cos_sin", cos_sin, dev, torch.float32, (rows, size)), rows, size,
                    PA_ROPE_PAIRS if pairs else PA_ROPE_HALVES)
 
 
-def _slots_for(slot_mapping, n: int) -> None:
-    _int64_slots(slot_mapping)
-    if slot_mapping.numel() < n:
-        raise PaError(PA_ERR_INVALID, f"{slot_mapping.numel()} slots for {n} tokens")
-
-
-def _cache_rows(layout: pa_layout, *caches) -> None:
-    """The caches of an unquantised or FP8 layout."""
-    want = torch.uint8 if layout.cache_dtype == PA_FP8_E4M3 else _torch_dtype(layout.dtype)
-    for c in caches:
-        if c.dtype != want or tuple(c.shape) != cache_shape(layout):
-            raise PaError(PA_ERR_INVALID, f"a cache is {c.dtype} {tuple(c.shape)}, expected {want} "
-                                          f"{cache_shape(layout)}")
+def _both(q, q_out) -> None:
+    if (q is None) != (q_out is None):
+        raise PaError(PA_ERR_INVALID, "q and q_out must both be given, or neither")
 
 
 def pa_rope_cache_write(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
@@ -417,29 +458,22 @@ def pa_rope_cache_write(q, k, v, positions, cos_sin, slot_mapping, q_out, k_cach
     (float32: n / 2 cosines, then n / 2 sines), in pairs (x_i, x_(i + n/2)), or with
     `pairs` (x_2i, x_(2i+1)).  q, k and v may be slices of one projection (any token
     stride, heads contiguous); q_out may be q.  q and q_out None: only k and v."""
-    dev = _on_one_device(strided=("q", "k", "v"), q=q, k=k, v=v, positions=positions, cos_sin=cos_sin,
-                         slot_mapping=slot_mapping, q_out=q_out, k_cache=k_cache, v_cache=v_cache,
-                         status=status)
-    if layout.cache_dtype == PA_INT4:
-        _int4_pages(layout, k_cache, v_cache)
-    else:
-        _cache_rows(layout, k_cache, v_cache)
-    n, d, dt = k.shape[0], layout.head_size, _torch_dtype(layout.dtype)
-    kv = (n, layout.num_kv_heads, d)
-    _want("k", k, dt, kv, 2)
-    _want("v", v, dt, kv, 2)
-    if (q is None) != (q_out is None):
-        raise PaError(PA_ERR_INVALID, "q and q_out must both be given, or neither")
+    dev, hq, hkv, d = _device("k_cache", k_cache), layout.num_q_heads, layout.num_kv_heads, layout.head_size
+    dt, n = _torch_dtype(layout.dtype), k.shape[0]
+    held, shape = dt if layout.cache_dtype == layout.dtype else torch.uint8, cache_shape(layout)
+    kc = _whole("k_cache", k_cache, dev, held, shape)
+    vc = _whole("v_cache", v_cache, dev, held, shape)
+    ks = _rows("k", k, dev, dt, (n, hkv, d), 2, hkv * d)
+    vs = _rows("v", v, dev, dt, (n, hkv, d), 2, hkv * d)
+    _both(q, q_out)
+    qp, qs, qo = None, 0, None
     if q is not None:
-        _want("q", q, dt, (n, layout.num_q_heads, d), 2)
-        _want("q_out", q_out, dt, (n, layout.num_q_heads, d))
-    _slots_for(slot_mapping, n)
-    rope = _rope(positions, cos_sin, n, pairs)
-    q_row, kv_row = layout.num_q_heads * d, layout.num_kv_heads * d
-    _launch(lib().pa_rope_cache_write, dev, stream, _ptr(q), 0 if q is None else _stride(q, 0, q_row),
-            _ptr(k), _stride(k, 0, kv_row), _ptr(v), _stride(v, 0, kv_row), ctypes.byref(rope),
-            _ptr(slot_mapping), n, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), ctypes.byref(layout),
-            _ptr(status))
+        qs = _rows("q", q, dev, dt, (n, hq, d), 2, hq * d)
+        qp, qo = q.data_ptr(), _whole("q_out", q_out, dev, dt, (n, hq, d))
+    slots = _list_of("slot_mapping", slot_mapping, dev, torch.int64, n, "slots")
+    rope = _rope(positions, cos_sin, dev, n, pairs)
+    _launch(lib().pa_rope_cache_write, dev, stream, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, rope, slots, n,
+            qo, kc, vc, layout, _status(status, dev))
 
 
 def make_latent_layout(num_heads: int, latent_size: int, num_blocks: int, dtype=torch.bfloat16,
@@ -460,10 +494,6 @@ def latent_layout_of(cache: torch.Tensor, num_heads: int, rope_size: int = 64) -
     return make_latent_layout(num_heads, row - rope_size, nb, cache.dtype, rope_size, bs)
 
 
-def _latent_cache(layout: pa_latent_layout, cache) -> None:
-    _want("cache", cache, _torch_dtype(layout.dtype), latent_cache_shape(layout))
-
-
 def pa_latent_write(c, k_rope, q, positions, cos_sin, slot_mapping, q_out, cache,
                     layout: pa_latent_layout, norm_weight=None, eps: float = 1e-6,
                     pairs: bool = False, status: torch.Tensor | None = None, stream=None) -> None:
@@ -473,42 +503,32 @@ def pa_latent_write(c, k_rope, q, positions, cos_sin, slot_mapping, q_out, cache
     weighted first.  positions, cos_sin and pairs as for pa_rope_cache_write.  c [T, latent_size],
     k_rope [T, rope_size], q and q_out may be slices (last dimension contiguous); q_out may be
     q.  q and q_out None: only the cache is written."""
-    dev = _on_one_device(strided=("c", "k_rope", "q", "q_out"), c=c, k_rope=k_rope, q=q, positions=positions,
-                         cos_sin=cos_sin, slot_mapping=slot_mapping, q_out=q_out, cache=cache,
-                         norm_weight=norm_weight, status=status)
-    _latent_cache(layout, cache)
-    n, dt, rs = c.shape[0], _torch_dtype(layout.dtype), layout.rope_size
-    _want("c", c, dt, (n, layout.latent_size), 1)
-    _want("k_rope", k_rope, dt, (n, rs), 1)
-    if norm_weight is not None:
-        _want("norm_weight", norm_weight, dt, (layout.latent_size,))
-    if (q is None) != (q_out is None):
-        raise PaError(PA_ERR_INVALID, "q and q_out must both be given, or neither")
-    strides = [0] * 4
+    dev, h, size, rs = _device("cache", cache), layout.num_heads, layout.latent_size, layout.rope_size
+    dt, n = _torch_dtype(layout.dtype), c.shape[0]
+    held = _whole("cache", cache, dev, dt, latent_cache_shape(layout))
+    cs = _rows("c", c, dev, dt, (n, size), 1, size)
+    ks = _rows("k_rope", k_rope, dev, dt, (n, rs), 1, rs)
+    weight = None if norm_weight is None else _whole("norm_weight", norm_weight, dev, dt, (size,))
+    _both(q, q_out)
+    qp, qs, qh, qo, os, oh = None, 0, 0, None, 0, 0
     if q is not None:
-        for i, (name, t) in enumerate((("q", q), ("q_out", q_out))):
-            _want(name, t, dt, (n, layout.num_heads, rs), 1)
-            strides[2 * i + 1] = _stride(t, 1, rs)
-            strides[2 * i] = _stride(t, 0, strides[2 * i + 1] * layout.num_heads)
-    _slots_for(slot_mapping, n)
-    rope = _rope(positions, cos_sin, n, pairs)
-    _launch(lib().pa_latent_write, dev, stream, _ptr(c), _stride(c, 0, layout.latent_size), _ptr(k_rope),
-            _stride(k_rope, 0, rs), _ptr(norm_weight), float(eps), _ptr(q), strides[0], strides[1],
-            ctypes.byref(rope), _ptr(slot_mapping), n, _ptr(q_out), strides[2], strides[3], _ptr(cache),
-            ctypes.byref(layout), _ptr(status))
+        qs, qh = _heads("q", q, dev, dt, (n, h, rs))
+        os, oh = _heads("q_out", q_out, dev, dt, (n, h, rs))
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    slots = _list_of("slot_mapping", slot_mapping, dev, torch.int64, n, "slots")
+    rope = _rope(positions, cos_sin, dev, n, pairs)
+    _launch(lib().pa_latent_write, dev, stream, c.data_ptr(), cs, k_rope.data_ptr(), ks, weight, eps, qp, qs, qh,
+            rope, slots, n, qo, os, oh, held, layout, _status(status, dev))
 
 
 def pa_latent_read(cache, slot_mapping, c, k_rope, layout: pa_latent_layout,
                    status: torch.Tensor | None = None, stream=None) -> None:
     """Read slot slot_mapping[t] of the latent cache into c[t], k_rope[t] (in place)."""
-    dev = _on_one_device(cache=cache, slot_mapping=slot_mapping, c=c, k_rope=k_rope, status=status)
-    _latent_cache(layout, cache)
-    _int64_slots(slot_mapping)
-    n, dt = slot_mapping.shape[0], _torch_dtype(layout.dtype)
-    _want("c", c, dt, (n, layout.latent_size))
-    _want("k_rope", k_rope, dt, (n, layout.rope_size))
-    _launch(lib().pa_latent_read, dev, stream, _ptr(cache), _ptr(slot_mapping), n, _ptr(c), _ptr(k_rope),
-            ctypes.byref(layout), _ptr(status))
+    dev, dt, n = _device("cache", cache), _torch_dtype(layout.dtype), slot_mapping.numel()
+    _launch(lib().pa_latent_read, dev, stream, _whole("cache", cache, dev, dt, latent_cache_shape(layout)),
+            _list_of("slot_mapping", slot_mapping, dev, torch.int64, n, "slots"), n,
+            _whole("c", c, dev, dt, (n, layout.latent_size)),
+            _whole("k_rope", k_rope, dev, dt, (n, layout.rope_size)), layout, _status(status, dev))
 
 
 def pa_latent_workspace_size(layout: pa_latent_layout, num_seqs: int, num_tokens: int,
@@ -527,10 +547,10 @@ def alloc_latent_workspace(layout: pa_latent_layout, num_seqs: int, num_tokens: 
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _int32(**arrays) -> None:
-    for name, t in arrays.items():
-        if t.dtype != torch.int32:
-            raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype}, expected torch.int32")
+def _workspace(workspace, dev: int) -> tuple:
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _explain("workspace", workspace, dev, workspace.dtype, workspace.shape, None)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def pa_latent_forward(q, cache, block_tables, seq_lens, query_start_loc, max_query_len: int,
@@ -538,20 +558,19 @@ def pa_latent_forward(q, cache, block_tables, seq_lens, query_start_loc, max_que
                       status: torch.Tensor | None = None, stream=None) -> None:
     """Attention over a latent cache (absorbed form): q [T, H, latent_size + rope_size], out
     [T, H, latent_size], the rest as for pa_forward."""
-    dev = _on_one_device(q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens,
-                         query_start_loc=query_start_loc, out=out, workspace=workspace, status=status)
-    _latent_cache(layout, cache)
-    _int32(block_tables=block_tables, seq_lens=seq_lens, query_start_loc=query_start_loc)
-    n, b, dt = q.shape[0], seq_lens.shape[0], _torch_dtype(layout.dtype)
-    _want("q", q, dt, (n, layout.num_heads, layout.latent_size + layout.rope_size))
-    _want("out", out, dt, (n, layout.num_heads, layout.latent_size))
-    if query_start_loc.numel() != b + 1 or block_tables.dim() != 2 or block_tables.shape[0] != b:
-        raise PaError(PA_ERR_INVALID, f"{b} requests, but query_start_loc {tuple(query_start_loc.shape)} and "
-                                      f"block_tables {tuple(block_tables.shape)}")
-    _launch(lib().pa_latent_forward, dev, stream, _ptr(q), _ptr(cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(seq_lens), _ptr(query_start_loc), b, n, int(max_query_len),
-            int(max_seq_len), float(scale), _ptr(out), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), ctypes.byref(layout), _ptr(status))
+    dev, dt, n, b = _device("cache", cache), _torch_dtype(layout.dtype), q.shape[0], seq_lens.shape[0]
+    h, size = layout.num_heads, layout.latent_size
+    if block_tables.dim() != 2:
+        raise PaError(PA_ERR_INVALID, f"block_tables is {tuple(block_tables.shape)}, expected [requests, blocks]")
+    width = block_tables.shape[1]
+    ws, nbytes = _workspace(workspace, dev)
+    _launch(lib().pa_latent_forward, dev, stream, _whole("q", q, dev, dt, (n, h, size + layout.rope_size)),
+            _whole("cache", cache, dev, dt, latent_cache_shape(layout)),
+            _whole("block_tables", block_tables, dev, torch.int32, (b, width)), width,
+            _whole("seq_lens", seq_lens, dev, torch.int32, (b,)),
+            _whole("query_start_loc", query_start_loc, dev, torch.int32, (b + 1,)), b, n, max_query_len,
+            max_seq_len, scale, _whole("out", out, dev, dt, (n, h, size)), ws, nbytes, layout,
+            _status(status, dev))
 
 
 def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max_query_len: int,
@@ -562,44 +581,40 @@ def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max
     from the bottom right; out [T, H, D].  q, k_nope, k_rope and v may be slices (last
     dimension contiguous).  A workspace of pa_expanded_workspace_size bytes is taken from torch's
     allocator for the call where none is given and it is of use."""
-    dev = _on_one_device(strided=("q", "k_nope", "k_rope", "v"), q=q, k_nope=k_nope, k_rope=k_rope, v=v,
-                         query_start_loc=query_start_loc, kv_start_loc=kv_start_loc, out=out,
-                         workspace=workspace, status=status)
-    _int32(query_start_loc=query_start_loc, kv_start_loc=kv_start_loc)
-    if q.dim() != 3 or k_nope.dim() != 3 or q.dtype not in _DTYPES:
-        raise PaError(PA_ERR_INVALID, f"q is {q.dtype} {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}: expected "
-                                      "[tokens, heads, size] of float32 or bfloat16")
-    (n, h, _), (tk, _, d), b = q.shape, k_nope.shape, query_start_loc.numel() - 1
-    rs = k_rope.shape[-1]
-    _want("q", q, q.dtype, (n, h, d + rs), 1)
-    _want("k_nope", k_nope, q.dtype, (tk, h, d), 1)
-    _want("k_rope", k_rope, q.dtype, (tk, rs), 1)
-    _want("v", v, q.dtype, (tk, h, d), 1)
-    _want("out", out, q.dtype, (n, h, d))
-    if b < 0 or kv_start_loc.numel() != b + 1:
-        raise PaError(PA_ERR_INVALID, f"query_start_loc has {b + 1} entries, kv_start_loc {kv_start_loc.numel()}")
-    layout = pa_expanded_layout(h, d, rs, _DTYPES[q.dtype], _stride(q, 0, h * (d + rs)), _stride(q, 1, d + rs),
-                                _stride(k_nope, 0, h * d), _stride(k_nope, 1, d), _stride(k_rope, 0, rs),
-                                _stride(v, 0, h * d), _stride(v, 1, d))
-    if workspace is None:
-        size = lib().pa_expanded_workspace_size(ctypes.byref(layout), n, int(max_kv_len))
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    dev, dt = _device("q", q), q.dtype
+    if q.dim() != 3 or k_nope.dim() != 3 or k_rope.dim() != 2 or dt not in _DTYPES:
+        raise PaError(PA_ERR_INVALID, f"q is {dt} {tuple(q.shape)}, k_nope {tuple(k_nope.shape)}, k_rope "
+                                      f"{tuple(k_rope.shape)}: expected [tokens, heads, size] of float32 or "
+                                      "bfloat16 and [tokens, size]")
+    (n, h, _), (tk, _, d), rs, b = q.shape, k_nope.shape, k_rope.shape[1], query_start_loc.numel() - 1
+    if b < 0:
+        raise PaError(PA_ERR_INVALID, "query_start_loc is empty")
+    layout = pa_expanded_layout(h, d, rs, _DTYPES[dt], *_heads("q", q, dev, dt, (n, h, d + rs)),
+                                *_heads("k_nope", k_nope, dev, dt, (tk, h, d)),
+                                _rows("k_rope", k_rope, dev, dt, (tk, rs), 1, rs),
+                                *_heads("v", v, dev, dt, (tk, h, d)))
+    ws, nbytes = None, 0
+    if workspace is not None:
+        ws, nbytes = _workspace(workspace, dev)
+    else:
+        nbytes = lib().pa_expanded_workspace_size(layout, n, max_kv_len)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
             if stream is not None:  # its memory may be given out again when that stream is done
                 workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                                         else torch.cuda.ExternalStream(int(stream), device=q.device))
-    _launch(lib().pa_expanded_forward, dev, stream, _ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v),
-            _ptr(query_start_loc), _ptr(kv_start_loc), b, n, tk, int(max_query_len), int(max_kv_len),
-            float(scale), _ptr(out), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            ctypes.byref(layout), _ptr(status))
+    _launch(lib().pa_expanded_forward, dev, stream, q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(),
+            v.data_ptr(), _whole("query_start_loc", query_start_loc, dev, torch.int32, (b + 1,)),
+            _whole("kv_start_loc", kv_start_loc, dev, torch.int32, (b + 1,)), b, n, tk, max_query_len, max_kv_len,
+            scale, _whole("out", out, dev, dt, (n, h, d)), ws, nbytes, layout, _status(status, dev))
 
 
 def pa_expanded_workspace_size(num_heads: int, head_size: int, num_tokens: int, max_kv_len: int,
                                dtype=torch.bfloat16, rope_size: int = 64) -> int:
     """Bytes of workspace that are of use to pa_expanded_forward (0: none)."""
     layout = pa_expanded_layout(num_heads, head_size, rope_size, _DTYPES[dtype])
-    n = lib().pa_expanded_workspace_size(ctypes.byref(layout), int(num_tokens), int(max_kv_len))
+    n = lib().pa_expanded_workspace_size(layout, num_tokens, max_kv_len)
     if n == 0 and last_error():
         raise PaError(PA_ERR_INVALID, last_error())
     return int(n)
