@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t(&r)[kKeys] = reinterpret_cast<uint32_t(&)[kKeys]>(x);
           PA_TMEM_LD32(ts, (r + 0));
           PA_TMEM_LD32(ts + 32, (r + 32));
-          tmem_ld16(ts + 64, reinterpret_cast<uint32_t(&)[16]>(r[64]));
+          tmem_ld(ts + 64, reinterpret_cast<uint32_t(&)[16]>(r[64]));
           tmem_wait_ld();
         }
         tc_fence_before();
@@ -578,15 +578,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             uint32_t o[16];
-            tmem_ld16(to + c, o);
+            tmem_ld(to + c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st16(to + c, o);
+            tmem_st(to + c, o);
           }
         }
         PA_TMEM_ST32(ts + C::kTmemP, pk);
-        tmem_st8(ts + C::kTmemP + 32, pk + 32);
+        tmem_st(ts + C::kTmemP + 32, reinterpret_cast<uint32_t(&)[8]>(pk[32]));
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(bar(ePFull + w));

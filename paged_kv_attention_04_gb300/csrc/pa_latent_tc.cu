@@ -15,7 +15,10 @@
 // Read with the keys as rows (K-major) it is A of the first product, with the numbers
 // as rows (MN-major) A of the second, so there is one copy of it.
 //
-// Roles: warps 0-3 softmax and output, warp 4 units and copies, warp 5 MMA issue.
+// Roles: warps 0-3 and 4-7 softmax and output of half of the query rows each, warp 8 units and copies,
+// warp 9 MMA issue.  Two 64-key tiles of R = 512 fill shared memory, and a tile stays for its copy
+// (2 us from HBM), S, softmax and O: to keep HBM busy the copies of the tiles after them are begun as
+// prefetches to L2.
 // S' has a key per TMEM lane (16 of every 32) and is read as matrix fragments: column maxima by
 // shuffles over lanes and a trade between the four warps in shared memory.  The reference
 // of a column moves only when its maximum grows by more than 2^8; P is written transposed
@@ -37,9 +40,10 @@ using namespace tc;
 
 constexpr int kKeys = 64;           // keys of a tile
 constexpr int kPages = kKeys / kBlockSize;
-constexpr int kCopyWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 192;
-constexpr int kSoftThreads = 128;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kSoftThreads = 256;
+constexpr int kAhead = 2;           // tiles that are prefetched to L2 behind the one to be copied
 constexpr float kGrowth = 8.f;      // base-2 growth of a maximum that moves the reference
 constexpr int kUnitCost = 2;        // what a unit costs beside its tiles, in tiles
 constexpr uint32_t kPollLimit = 1u << 26;
@@ -80,16 +84,16 @@ struct Unit {
 
 enum Bar : int {
   kUnitFull = 0,   // [2]
-  kUnitEmpty = 2,  // [2] (4 softmax warps, MMA)
+  kUnitEmpty = 2,  // [2] (8 softmax warps, MMA)
   kQFull = 4,      // [2] TMA
   kQEmpty = 6,     // [2] the unit's last S done
   kKFull = 8,      // [4] TMA
   kKEmpty = 12,    // [4] O += of the tile done: frees the tile and its P
   kSFull = 16,     // [2] S done
-  kPFull = 18,     // [2] S read, P written, O rescaled (4 warps)
-  kTrade = 20,     // the softmax warps meet (4 warps)
-  kDrain = 21,
-  kNumBars = 22
+  kPFull = 18,     // [2] S read, P written, O rescaled (8 warps)
+  kTrade = 20,     // [2] the softmax warps of a half meet (4 warps)
+  kDrain = 22,
+  kNumBars = 23
 };
 
 struct Small {
@@ -154,8 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 5;
-      if (i == kPFull || i == kPFull + 1 || i == kTrade) n = 4;
+      if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 9;
+      if (i == kPFull || i == kPFull + 1) n = 8;
+      if (i == kTrade || i == kTrade + 1) n = 4;
       mbar_init(bar(i), n);
     }
     // (the swizzled tiles need the alignment that the declaration asks for)
@@ -258,22 +263,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bar(kQFull + qs));
       ++uc;
       const int32_t* table = p.block_tables + static_cast<long long>(u.r) * p.max_blocks_per_seq;
-      auto entry = [&](int t) {  // block of page `lane` of tile t, -1 past the request's keys
-        const int b = t * kPages + lane;
-        return lane < kPages && b * kBlockSize < u.seq ? __ldg(table + b) : -1;
+      // table entries of the pages of 8 tiles, one a lane: of group g, -1 past the request's keys
+      auto entries = [&](int g) {
+        const int b = g * 32 + lane;
+        return b * kBlockSize < u.seq ? __ldg(table + b) : -1;
       };
-      int ph = entry(u.t0);
-      for (int t = 0; t < u.n; ++t, ++g) {
+      int now = entries(u.t0 / 8), then = entries(u.t0 / 8 + 1);
+      // block of page `lane` (< 4) of tile t: `now`'s group or the next
+      auto block_of = [&](int t, int group) {
+        const int src = (t & 7) * kPages + (lane & (kPages - 1));
+        const int a = __shfl_sync(0xffffffffu, now, src), b = __shfl_sync(0xffffffffu, then, src);
+        return (t >> 3) == group ? a : b;
+      };
+      const int end = u.t0 + u.n;
+      int fetched = u.t0 + 1;  // tiles before it are copied or on their way to L2
+      for (int t = u.t0; t < end; ++t, ++g) {
         const int b = g % C::kBufs;
-        int cur = ph;
-        if (t + 1 < u.n) ph = entry(u.t0 + t + 1);
+        if ((t & 7) == 0 && t > u.t0) {
+          now = then;
+          then = entries(t / 8 + 1);
+        }
+        for (; fetched <= t + kAhead && fetched < end; ++fetched) {
+          const int ph = block_of(fetched, t >> 3);
+          if (lane < kPages && ph >= 0 && ph < p.num_blocks) tma_prefetch_5d(&kmap, 0, 0, 0, 0, ph);
+        }
+        int cur = block_of(t, t >> 3);
         if (g >= C::kBufs && !wait_bar(bar(kKEmpty + b), (g / C::kBufs - 1) & 1, abort, p.status)) return false;
         if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + b), C::kTileBytes);
         __syncwarp();
         if (lane < kPages) {
           // a page past the keys or with a bad table entry is read out of bounds: zeros
           if (cur < 0 || cur >= p.num_blocks) {
-            if (((u.t0 + t) * kPages + lane) * kBlockSize < u.seq) flag_error(p.status, PA_DEV_BLOCK_RANGE);
+            if ((t * kPages + lane) * kBlockSize < u.seq) flag_error(p.status, PA_DEV_BLOCK_RANGE);
             cur = p.num_blocks;
           }
           tma_load_5d(sbase + b * C::kTileBytes + lane * C::kPageBytes, &kmap, 0, 0, 0, 0, cur, bar(kKFull + b));
@@ -429,10 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and output
-    constexpr int F = N / 8;  // column groups of a fragment
-    const int c0 = 2 * (lane & 3);
-    const int key0 = warp * 16 + (lane >> 2);
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    constexpr int H = N / 2, F = H / 8;  // columns of this half, column groups of a fragment
+    constexpr int kStep = H < 16 ? H : 16;
+    const int half = warp >> 2, quarter = warp & 3;
+    const int c0 = half * H + 2 * (lane & 3);  // this lane's first column
+    const int key0 = quarter * 16 + (lane >> 2);
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t g = 0;
     bool ok = !*abort;
     // phase of tile i's "O += done"
@@ -441,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t trades = 0;
     auto meet = [&]() {
-      warp_arrive(bar(kTrade));
-      return wait_bar(bar(kTrade), trades++ & 1, abort, p.status);
+      warp_arrive(bar(kTrade + half));
+      return wait_bar(bar(kTrade + half), trades++ & 1, abort, p.status);
     };
     for (int uc = 0; ok; ++uc) {
       if (!wait_bar(bar(kUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
@@ -459,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_bar(bar(kSFull + (g & 1)), (g >> 1) & 1, abort, p.status)) { ok = false; break; }
         tc_fence_after();
         uint32_t raw[F * 4];
-        tmem_ld_frag(tmem + C::kTmemS + (g & 1) * N + lanes, raw);
+        tmem_ld_frag(tmem + C::kTmemS + (g & 1) * N + half * H + lanes, raw);
         tmem_wait_ld();
         float x[F][4];
 #pragma unroll
@@ -503,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < 4) {
 #pragma unroll
           for (int i = 0; i < F; ++i)
-            *reinterpret_cast<float2*>(&sm.mx[g & 1][warp][8 * i + c0]) = make_float2(mx[i][0], mx[i][1]);
+            *reinterpret_cast<float2*>(&sm.mx[g & 1][quarter][8 * i + c0]) = make_float2(mx[i][0], mx[i][1]);
         }
         if (!meet()) { ok = false; break; }
         bool moved = false;
@@ -539,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         // O' of earlier tiles takes the new references, once it is there
         if (moved && t > 0) {
-          if (warp == 0 && lane < 4) {
+          if (quarter == 0 && lane < 4) {
 #pragma unroll
             for (int i = 0; i < F; ++i)
               *reinterpret_cast<float2*>(&sm.f[8 * i + c0]) = make_float2(f[i][0], f[i][1]);
@@ -547,28 +570,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!meet() || !wait_o(g - 1)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < C::kBlocks * N; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tmem + lanes + c, o);
+          for (int c = 0; c < C::kBlocks * H; c += kStep) {
+            const uint32_t at = tmem + lanes + c / H * N + half * H + c % H;
+            uint32_t o[kStep];
+            tmem_ld(at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.f[(c & (N - 1)) + i]);
-            tmem_st16(tmem + lanes + c, o);
+            for (int i = 0; i < kStep; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.f[half * H + c % H + i]);
+            tmem_st(at, o);
           }
           tmem_wait_st();
         } else if (g >= C::kPs) {
           if (!wait_o(g - C::kPs)) { ok = false; break; }  // P's buffer is free
         }
         const uint32_t pbuf = sbase + C::kPOff + (g % C::kPs) * C::kPBytes;
-#pragma unroll
-        for (int i = 0; i < F; i += 2) {
-          const int row = 8 * (i + (lane >> 4)) + (lane & 7), chunk = 2 * warp + ((lane >> 3) & 1);
-          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(
+        // (a matrix of 8 keys x 8 rows a register; lanes 8 k .. 8 k + 7 address matrix k's rows)
+        if constexpr (F == 1) {
+          const int row = half * H + (lane & 7), chunk = 2 * quarter + ((lane >> 3) & 1);
+          asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};\n" ::"r"(
                            pbuf + row * 128 + ((chunk ^ (row & 7)) << 4)),
-                       "r"(pack_bf16(x[i][0], x[i][1])), "r"(pack_bf16(x[i][2], x[i][3])),
-                       "r"(pack_bf16(x[i + 1][0], x[i + 1][1])), "r"(pack_bf16(x[i + 1][2], x[i + 1][3]))
+                       "r"(pack_bf16(x[0][0], x[0][1])), "r"(pack_bf16(x[0][2], x[0][3]))
                        : "memory");
+        } else {
+#pragma unroll
+          for (int i = 0; i < F; i += 2) {
+            const int row = half * H + 8 * (i + (lane >> 4)) + (lane & 7), chunk = 2 * quarter + ((lane >> 3) & 1);
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(
+                             pbuf + row * 128 + ((chunk ^ (row & 7)) << 4)),
+                         "r"(pack_bf16(x[i][0], x[i][1])), "r"(pack_bf16(x[i][2], x[i][3])),
+                         "r"(pack_bf16(x[i + 1][0], x[i + 1][1])), "r"(pack_bf16(x[i + 1][2], x[i + 1][3]))
+                         : "memory");
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -587,41 +619,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < 4) {
 #pragma unroll
         for (int i = 0; i < F; ++i)
-          *reinterpret_cast<float2*>(&sm.mx[0][warp][8 * i + c0]) = make_float2(l[i][0], l[i][1]);
-        if (warp == 0 && u.slot >= 0) {
+          *reinterpret_cast<float2*>(&sm.mx[0][quarter][8 * i + c0]) = make_float2(l[i][0], l[i][1]);
+        if (quarter == 0 && u.slot >= 0) {
 #pragma unroll
           for (int i = 0; i < F; ++i)
             *reinterpret_cast<float2*>(&sm.mx[1][0][8 * i + c0]) = make_float2(m[i][0], m[i][1]);
         }
       }
       if (!meet()) break;
-      if (tid < N) {
-        const float sum = sm.mx[0][0][tid] + sm.mx[0][1][tid] + sm.mx[0][2][tid] + sm.mx[0][3][tid];
-        sm.f[tid] = u.slot >= 0 ? 1.f : 1.f / sum;
+      if ((tid & 127) < H) {
+        const int n = half * H + (tid & 127);
+        const float sum = sm.mx[0][0][n] + sm.mx[0][1][n] + sm.mx[0][2][n] + sm.mx[0][3][n];
+        sm.f[n] = u.slot >= 0 ? 1.f : 1.f / sum;
         if (u.slot >= 0)
-          reinterpret_cast<float2*>(p.part_ml)[static_cast<long long>(u.slot) * N + tid] =
-              make_float2(sm.mx[1][0][tid], sum);
+          reinterpret_cast<float2*>(p.part_ml)[static_cast<long long>(u.slot) * N + n] = make_float2(sm.mx[1][0][n], sum);
       }
       if (!meet() || !wait_o(g - 1)) break;
       tc_fence_after();
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(u.row0) * R;
       float* part = p.part_acc + static_cast<long long>(u.slot) * N * R;
+      // (the next columns are on their way while these are written)
+      uint32_t next[kStep];
+      tmem_ld(tmem + lanes + half * H, next);
 #pragma unroll 1
-      for (int c = 0; c < C::kBlocks * N; c += 16) {
-        const int n0 = c & (N - 1);                        // rows n0 .. n0 + 15
-        const int d = (c / N) * 128 + warp * 32 + lane;    // this lane's number
-        if (n0 >= u.rows) continue;
-        uint32_t o[16];
-        tmem_ld16(tmem + lanes + c, o);
+      for (int c = 0; c < C::kBlocks * H; c += kStep) {
+        uint32_t o[kStep];
         tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) o[i] = next[i];
+        const int c1 = c + kStep;
+        if (c1 < C::kBlocks * H) tmem_ld(tmem + lanes + c1 / H * N + half * H + c1 % H, next);
+        const int n0 = half * H + c % H;                    // rows n0 .. n0 + kStep - 1
+        const int d = c / H * 128 + quarter * 32 + lane;    // this lane's number
         if (u.slot >= 0) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
+          for (int i = 0; i < kStep; ++i)
             if (n0 + i < u.rows) part[(n0 + i) * R + d] = __uint_as_float(o[i]);
         } else {
           // lanes of a pair trade: the even one writes both numbers of row i, the odd one of row i + 1
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < kStep; i += 2) {
             const float a = __uint_as_float(o[i]) * sm.f[n0 + i], b = __uint_as_float(o[i + 1]) * sm.f[n0 + i + 1];
             const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
             const int row = n0 + i + (lane & 1);
