@@ -47,7 +47,7 @@ constexpr int kAhead = 2;           // tiles that are prefetched to L2 behind th
 constexpr float kGrowth = 8.f;      // base-2 growth of a maximum that moves the reference
 constexpr int kUnitCost = 2;        // what a unit costs beside its tiles, in tiles
 constexpr uint32_t kPollLimit = 1u << 26;
-constexpr int kMinStretch = 4;      // shortest stretch of the line for a CTA
+constexpr int kMinStretch = kUnitCost + 1;  // shortest stretch of the line for a CTA: a unit of one tile
 
 template <int R, int N>
 struct Cfg {
@@ -96,6 +96,11 @@ enum Bar : int {
   kNumBars = 23
 };
 
+// The line: what request r (rows a .. a + L - 1 of the step, S keys) takes of it.
+struct Span {
+  int a, L, S, units, len;  // units of this way, each len long
+};
+
 struct Small {
   uint64_t bars[kNumBars];
   Unit units[2];
@@ -105,14 +110,10 @@ struct Small {
   int abort;
   int start_r;
   int bad;
-  long long start_pos, total;
+  long long start_pos;
+  Span start;
 };
 static_assert(sizeof(Small) <= 3072, "small shared memory");
-
-// The line: what request r (rows a .. a + L - 1 of the step, S keys) takes of it.
-struct Span {
-  int a, L, S, units, len;  // units of this way, each len long
-};
 
 struct Shape {
   int ways, way;     // a request's row tiles are dealt to `ways` CTAs that read the same keys
@@ -155,6 +156,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sm.abort;
   auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
 
+  // ---- this CTA's place, and this thread's requests of the step (the first one's loads are on
+  // their way while the barriers are set up)
+  Shape sh;
+  sh.ways = ways;
+  sh.way = blockIdx.x % ways;
+  sh.group = blockIdx.x / ways;
+  sh.groups = gridDim.x / ways;
+  const int per = (p.num_seqs + kThreads - 1) / kThreads;
+  const int ra = min(tid * per, p.num_seqs), rb = min(ra + per, p.num_seqs);
+  Span s0{};
+  int err = ra < rb ? span_of<N>(p, sh, ra, s0) : 0;
+
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
@@ -177,18 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem;
 
   // ---- this CTA's stretch of the line: [lo, hi), beginning in request start_r
-  Shape sh;
-  sh.ways = ways;
-  sh.way = blockIdx.x % ways;
-  sh.group = blockIdx.x / ways;
-  sh.groups = gridDim.x / ways;
   long long lo = 0, hi = 0, total = 0;
   {
-    const int per = (p.num_seqs + kThreads - 1) / kThreads;
-    const int ra = min(tid * per, p.num_seqs), rb = min(ra + per, p.num_seqs);
-    long long mine = 0;
-    int err = 0;
-    for (int r = ra; r < rb; ++r) {
+    long long mine = static_cast<long long>(s0.units) * s0.len;
+#pragma unroll 1
+    for (int r = ra + 1; r < rb; ++r) {
       Span s;
       err |= span_of<N>(p, sh, r, s);
       mine += static_cast<long long>(s.units) * s.len;
@@ -220,13 +226,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lo < hi && before <= lo && lo < before + mine) {
       long long pos = before;
+      Span s = s0;
+#pragma unroll 1
       for (int r = ra; r < rb; ++r) {
-        Span s;
-        span_of<N>(p, sh, r, s);
+        if (r > ra) span_of<N>(p, sh, r, s);
         const long long len = static_cast<long long>(s.units) * s.len;
         if (lo < pos + len) {
           sm.start_r = r;
           sm.start_pos = pos;
+          sm.start = s;
           break;
         }
         pos += len;
@@ -253,6 +261,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     auto run = [&](const Unit& u) {
+      const int32_t* table = p.block_tables + static_cast<long long>(u.r) * p.max_blocks_per_seq;
+      // table entries of the pages of 8 tiles, one a lane: of group g, -1 past the request's keys
+      auto entries = [&](int g) {
+        const int b = g * 32 + lane;
+        return b * kBlockSize < u.seq ? __ldg(table + b) : -1;
+      };
+      int now = entries(u.t0 / 8), then = entries(u.t0 / 8 + 1);
       if (!publish(u)) return false;
       const int qs = uc % C::kQs;
       if (uc >= C::kQs && !wait_bar(bar(kQEmpty + qs), (uc / C::kQs - 1) & 1, abort, p.status)) return false;
@@ -262,13 +277,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_2d(sbase + C::kQOff + qs * C::kQBytes + lane * N * 128, &qmap, lane * 64, u.row0,
                     bar(kQFull + qs));
       ++uc;
-      const int32_t* table = p.block_tables + static_cast<long long>(u.r) * p.max_blocks_per_seq;
-      // table entries of the pages of 8 tiles, one a lane: of group g, -1 past the request's keys
-      auto entries = [&](int g) {
-        const int b = g * 32 + lane;
-        return b * kBlockSize < u.seq ? __ldg(table + b) : -1;
-      };
-      int now = entries(u.t0 / 8), then = entries(u.t0 / 8 + 1);
       // block of page `lane` (< 4) of tile t: `now`'s group or the next
       auto block_of = [&](int t, int group) {
         const int src = (t & 7) * kPages + (lane & (kPages - 1));
@@ -304,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (ok && sm.start_r >= 0) {
       long long pos = sm.start_pos;
+      Span s = sm.start;
       for (int r = sm.start_r; ok && r < p.num_seqs && pos < hi; ++r) {
-        Span s;
-        span_of<N>(p, sh, r, s);
+        if (r > sm.start_r) span_of<N>(p, sh, r, s);
         const long long skip = s.len && lo > pos ? (lo - pos) / s.len : 0;
         for (int j = static_cast<int>(skip); ok && j < s.units; ++j) {
           const long long ua = pos + static_cast<long long>(j) * s.len;
@@ -717,15 +725,22 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) 
         acc[i].w = acc[i].w * fa + x[i].w * fb;
       }
     };
-#pragma unroll 2
-    for (int k = few ? 0 : warp; k < pieces; k += few ? 1 : 8) {
-      const long long row = slot(k) + n;
-      const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[row];
-      const float4* src = reinterpret_cast<const float4*>(p.part_acc + row * R);
-      float4 x[kVec];
+    const int k0 = few ? 0 : warp, dk = few ? 1 : 8;
+    for (int k = k0; k < pieces; k += 2 * dk) {  // two pieces' loads at once
+      float2 ml[2];
+      float4 x[2][kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = src[i * 32 + lane];
-      add(ml, x);
+      for (int j = 0; j < 2; ++j) {
+        const bool is = k + j * dk < pieces;
+        const long long row = slot(is ? k + j * dk : k) + n;
+        ml[j] = reinterpret_cast<const float2*>(p.part_ml)[row];
+        if (!is) ml[j].y = 0.f;
+        const float4* src = reinterpret_cast<const float4*>(p.part_acc + row * R);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[j][i] = src[i * 32 + lane];
+      }
+      add(ml[0], x[0]);
+      add(ml[1], x[1]);
     }
     if (!few) {
 #pragma unroll
