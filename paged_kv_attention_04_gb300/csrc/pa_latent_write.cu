@@ -36,37 +36,41 @@ __global__ void __launch_bounds__(kThreads) latent_write_kernel(const LatentWrit
   if (t >= static_cast<unsigned>(p.a.num_tokens)) return;  // whole warps
   const int job = static_cast<int>(w - t * p.jobs);
   const bool pairs = p.rope.pairs != 0;
-  const float* table = rope_row(p.rope, t, lane == 0, p.a.status);
-  if (!table) return;
   const int j = lane & 3;
   int oa, ob;
   rope_groups(j, kLatentRope, pairs, oa, ob);
+  // (the numbers are on their way while the token's position and slot are looked up)
+  Eight<T> a, b;
   if (job > 0) {
     const int h = (job - 1) * kHeadsPerWarp + (lane >> 2);
     if (h >= p.num_heads) return;
     const T* src = static_cast<const T*>(p.a.q) + t * p.a.q_stride + h * p.a.q_head_stride;
-    T* dst = static_cast<T*>(p.a.q_out) + t * p.a.qo_stride + h * p.a.qo_head_stride;
-    Eight<T> a, b;
     a.load(src + oa);
     b.load(src + ob);
+    const float* table = rope_row(p.rope, t, lane == 0, p.a.status);
+    if (!table) return;
     rope_turn(a, b, table, j, kLatentRope, pairs);
+    T* dst = static_cast<T*>(p.a.q_out) + t * p.a.qo_stride + h * p.a.qo_head_stride;
     a.store(dst + oa);
     b.store(dst + ob);
     return;
   }
-  const int64_t s = __ldg(p.a.slots + t);
-  if (s >= p.num_slots && lane == 0) flag_error(p.a.status, PA_DEV_SLOT_RANGE);
-  if (s < 0 || s >= p.num_slots) return;
   const T* c = static_cast<const T*>(p.a.c) + t * p.a.c_stride;
-  T* row = static_cast<T*>(p.a.cache) + s * kRow;
   Eight<T> e[kGroups];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) e[g].load(c + g * 256 + lane * 8);
   if (lane < 4) {
     const T* k = static_cast<const T*>(p.a.k) + t * p.a.k_stride;
-    Eight<T> a, b;
     a.load(k + oa);
     b.load(k + ob);
+  }
+  const int64_t s = __ldg(p.a.slots + t);
+  const float* table = rope_row(p.rope, t, lane == 0, p.a.status);
+  if (!table) return;
+  if (s >= p.num_slots && lane == 0) flag_error(p.a.status, PA_DEV_SLOT_RANGE);
+  if (s < 0 || s >= p.num_slots) return;
+  T* row = static_cast<T*>(p.a.cache) + s * kRow;
+  if (lane < 4) {
     rope_turn(a, b, table, j, kLatentRope, pairs);
     a.store(row + R + oa);
     b.store(row + R + ob);

@@ -42,13 +42,22 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 
+// 16 bytes that are read once: not kept in L1, where the table's rows are.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 w;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "l"(p));
+  return w;
+}
+
 // 8 numbers as they lie in memory.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 w;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = load_once(p); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
   __device__ __forceinline__ void get(float (&x)[8]) const { Chunk<__nv_bfloat16>::unpack(w, x); }
   __device__ __forceinline__ void set(const float (&x)[8]) {
@@ -63,8 +72,9 @@ template <>
 struct Eight<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+    const uint4 u = load_once(p), v = load_once(p + 4);
+    a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+    b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
   }
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;

@@ -55,22 +55,20 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const RopeWrite p)
   const int head = is_q ? row : row - p.q_rows - (is_v ? p.kv_rows : 0);
   const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) +
                  t * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) + head * D;
-  const float* table = rope_row(p.rope, t, j == 0, p.status);
-  if (!table) return;
-  int64_t s = 0;
-  if (!is_q) {
-    s = __ldg(p.slots + t);
-    if (s >= p.num_slots && j == 0) flag_error(p.status, PA_DEV_SLOT_RANGE);
-    if (s < 0 || s >= p.num_slots) return;
-  }
   const bool pairs = p.rope.pairs != 0;
   const int n = p.rope.size;
   const bool turned = !is_v && j * 16 < n;
   int oa = 16 * j, ob = oa + 8;
   if (turned) rope_groups(j, n, pairs, oa, ob);
+  // (the numbers are on their way while the token's position and slot are looked up)
   Eight<T> a, b;
   a.load(src + oa);
   b.load(src + ob);
+  int64_t s = is_q ? 0 : __ldg(p.slots + t);
+  const float* table = rope_row(p.rope, t, j == 0, p.status);
+  if (!table) return;
+  if (s >= p.num_slots && j == 0) flag_error(p.status, PA_DEV_SLOT_RANGE);
+  if (s < 0 || s >= p.num_slots) return;
   if (turned) rope_turn(a, b, table, j, n, pairs);
   if (is_q) {
     T* dst = static_cast<T*>(p.q_out) + (static_cast<long long>(t) * p.q_rows + head) * D;
