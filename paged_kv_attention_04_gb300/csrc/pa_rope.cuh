@@ -108,27 +108,50 @@ __device__ __forceinline__ void rope_groups(int j, int n, bool pairs, int& oa, i
   }
 }
 
-// Rotate thread j's groups by the table row.
+// Two numbers (word i of a group).
+__device__ __forceinline__ float2 get2(const Eight<__nv_bfloat16>& e, int i) {
+  const uint32_t w = i == 0 ? e.w.x : i == 1 ? e.w.y : i == 2 ? e.w.z : e.w.w;
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ void set2(Eight<__nv_bfloat16>& e, int i, float x, float y) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w) : "f"(y), "f"(x));
+  (i == 0 ? e.w.x : i == 1 ? e.w.y : i == 2 ? e.w.z : e.w.w) = w;
+}
+__device__ __forceinline__ float2 get2(const Eight<float>& e, int i) {
+  return i == 0 ? make_float2(e.a.x, e.a.y) : i == 1 ? make_float2(e.a.z, e.a.w)
+       : i == 2 ? make_float2(e.b.x, e.b.y) : make_float2(e.b.z, e.b.w);
+}
+__device__ __forceinline__ void set2(Eight<float>& e, int i, float x, float y) {
+  float4& f = i < 2 ? e.a : e.b;
+  if (i & 1) f.z = x, f.w = y;
+  else f.x = x, f.y = y;
+}
+
+// Rotate thread j's groups by the table row, two pairs at a time (few registers).
 template <typename T>
 __device__ __forceinline__ void rope_turn(Eight<T>& ea, Eight<T>& eb, const float* row, int j, int n,
                                           bool pairs) {
-  float a[8], b[8], c[8], s[8];
-  load8(row + 8 * j, c);
-  load8(row + n / 2 + 8 * j, s);
-  ea.get(a);
-  eb.get(b);
-  if (pairs) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      turn(a[2 * i], a[2 * i + 1], c[i], s[i]);
-      turn(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 c = __ldg(reinterpret_cast<const float2*>(row + 8 * j) + i);
+    const float2 s = __ldg(reinterpret_cast<const float2*>(row + n / 2 + 8 * j) + i);
+    if (pairs) {
+      // words 2 i, 2 i + 1 of the 16 numbers
+      Eight<T>& e = i < 2 ? ea : eb;
+      float2 x = get2(e, 2 * (i & 1)), y = get2(e, 2 * (i & 1) + 1);
+      turn(x.x, x.y, c.x, s.x);
+      turn(y.x, y.y, c.y, s.y);
+      set2(e, 2 * (i & 1), x.x, x.y);
+      set2(e, 2 * (i & 1) + 1, y.x, y.y);
+    } else {
+      float2 a = get2(ea, i), b = get2(eb, i);
+      turn(a.x, b.x, c.x, s.x);
+      turn(a.y, b.y, c.y, s.y);
+      set2(ea, i, a.x, a.y);
+      set2(eb, i, b.x, b.y);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn(a[i], b[i], c[i], s[i]);
   }
-  ea.set(a);
-  eb.set(b);
 }
 
 }  // namespace pa
