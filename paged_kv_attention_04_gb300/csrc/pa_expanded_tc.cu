@@ -19,10 +19,11 @@
 // A thread holds a row's 80 logits, so the softmax warps take 208 registers of the 168 that the launch
 // gives every thread, the others 88.
 //
-// Work: units lie on a line in request, head, row order, each as long as its key tiles plus a
-// constant, and a CTA takes an equal stretch. Where a CTA gets many units the stretches end at
-// the nearest unit; where it gets a few long ones they are cut, their pieces leave partial
-// states (two a CTA at most) and a second kernel joins them in order.
+// Work: where a CTA gets a few long units, they lie on a line in request, head, row order, each as long
+// as its key tiles; every CTA takes an equal stretch, cut units leave partial states (two a
+// CTA at most), and a second kernel joins them in order.  Where it gets many, whole units are
+// dealt out by length, the longest first and every other round backwards (of more than 32 requests:
+// the units whose middle lies in the CTA's stretch).
 #include <math_constants.h>
 
 #include "pa_latent.h"
@@ -40,7 +41,8 @@ constexpr int kThreads = 384;
 constexpr int kSoftRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
 constexpr int kQSlice = kRows * 128, kKSlice = kKeys * 128;  // bytes of 64 numbers of a tile
 constexpr float kGrowth = 8.f;
-constexpr int kUnitCost = 2;       // what a unit costs beside its key tiles
+constexpr int kUnitCost = 0;       // what a unit costs beside its key tiles (measured: nothing, its start
+                                   // and output run beside other units' products)
 constexpr int kMinPiece = 6;       // fewest key tiles of a piece
 constexpr int kCutKeys = 1024;     // units are cut where a request may be this long ...
 constexpr int kCutUnits = 5;       // ... and a CTA gets fewer units than this
@@ -304,7 +306,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!load_k(u, u.t0 + t)) return false;
         return true;
       };
-      if (ok && sm.start_r >= 0) {
+      auto unit_of = [&](const ESpan& s, int r, int h, int m) {
+        EUnit u;
+        u.r = r;
+        u.head = h;
+        u.row0 = s.a + m * kUnitRows;
+        u.rows = min(kUnitRows, s.L - m * kUnitRows);
+        u.pos0 = s.S - s.L + m * kUnitRows;
+        u.key0 = s.ka;
+        u.seq = s.S;
+        u.t0 = 0;
+        u.n[0] = tiles_to(u.pos0 + min(kRows, u.rows) - 1);
+        u.n[1] = u.rows > kRows ? tiles_to(u.pos0 + u.rows - 1) : 0;
+        u.slot = -1;
+        return u;
+      };
+      if (!p.part_acc && p.num_seqs <= 32) {
+        // a lane a request: its units have levels, 256 keys apart, and come in order of these
+        ESpan s{};
+        if (lane < p.num_seqs && !sm.bad) span_of(p, lane, s);
+        const int low = (s.S - s.L) / kUnitRows;
+        int level = __reduce_max_sync(0xffffffffu, s.tiles ? low + s.tiles - 1 : -1);
+        long long base = 0;  // units of higher levels
+        for (int round = 0; ok && level >= 0; ++round) {
+          const long long i = static_cast<long long>(round) * gridDim.x +
+                              ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+          uint32_t with = 0;
+          for (; level >= 0; --level) {
+            with = __ballot_sync(0xffffffffu, level >= low && level < low + s.tiles);
+            const long long n = static_cast<long long>(__popc(with)) * p.num_heads;
+            if (i < base + n) break;
+            base += n;
+          }
+          if (level < 0) break;
+          const int j = static_cast<int>(i - base), r = __fns(with, 0, j / p.num_heads + 1);
+          ESpan t;
+          t.a = __shfl_sync(0xffffffffu, s.a, r);
+          t.L = __shfl_sync(0xffffffffu, s.L, r);
+          t.ka = __shfl_sync(0xffffffffu, s.ka, r);
+          t.S = __shfl_sync(0xffffffffu, s.S, r);
+          ok = run(unit_of(t, r, j % p.num_heads, level - (t.S - t.L) / kUnitRows));
+        }
+      } else if (ok && sm.start_r >= 0) {
         long long pos = sm.start_pos;
         for (int r = sm.start_r; ok && r < p.num_seqs && pos < hi; ++r) {
           ESpan s;
@@ -330,18 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               };
               const int c0 = cut(lo), c1 = cut(hi);
               if (c0 >= c1) continue;
-              EUnit u;
-              u.r = r;
-              u.head = h;
-              u.row0 = s.a + m * kUnitRows;
-              u.rows = min(kUnitRows, s.L - m * kUnitRows);
-              u.pos0 = s.S - s.L + m * kUnitRows;
-              u.key0 = s.ka;
-              u.seq = s.S;
+              EUnit u = unit_of(s, r, h, m);
               const int t1 = c1 == len ? len - kUnitCost : c1 - kUnitCost;
               u.t0 = c0 == 0 ? 0 : c0 - kUnitCost;
-              u.n[0] = max(0, min(t1, tiles_to(u.pos0 + min(kRows, u.rows) - 1)) - u.t0);
-              u.n[1] = u.rows > kRows ? t1 - u.t0 : 0;
+              u.n[0] = max(0, min(t1, u.n[0]) - u.t0);
+              if (u.n[1]) u.n[1] = t1 - u.t0;
               const bool whole = c0 == 0 && c1 == len;
               u.slot = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (c0 == 0);
               if (!whole && c0 == 0 && lane == 0) {
