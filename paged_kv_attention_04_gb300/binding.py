@@ -363,10 +363,9 @@ def alloc_workspace(layout: pa_layout, num_seqs: int, num_tokens: int, max_seq_l
 
 def _explain(name: str, t, dev: int, dtype, shape, inner: int | None) -> None:
     d = t.get_device()
-    if d < 0:
-        raise PaError(PA_ERR_INVALID, f"{name} is not a CUDA tensor")
     if d != dev:
-        raise PaError(PA_ERR_INVALID, f"{name} is on cuda:{d}, expected cuda:{dev}")
+        raise PaError(PA_ERR_INVALID, f"{name} is on cuda:{d}, expected cuda:{dev}" if d >= 0 else
+                      f"{name} is not a CUDA tensor")
     if t.dtype is not dtype or t.shape != shape:
         raise PaError(PA_ERR_INVALID, f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
     if inner is None:
@@ -377,7 +376,7 @@ def _explain(name: str, t, dev: int, dtype, shape, inner: int | None) -> None:
 def _device(name: str, t) -> int:
     dev = t.get_device()
     if dev < 0:
-        _explain(name, t, dev, t.dtype, t.shape, None)
+        raise PaError(PA_ERR_INVALID, f"{name} is not a CUDA tensor")
     return dev
 
 

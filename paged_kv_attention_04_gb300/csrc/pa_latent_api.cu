@@ -274,12 +274,12 @@ int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, c
       return fail(PA_ERR_INVALID, "strides must be positive multiples of 16 bytes below 2^40");
   if (static_cast<long long>(num_tokens) * L->num_heads > 0x7fffffffLL)
     return fail(PA_ERR_INVALID, "step too large for one call");
-  int num_sms = 0;
-  if (int rc = sms_of_current_device(&num_sms)) return rc;
   if (workspace && !aligned(workspace, 256)) return fail(PA_ERR_INVALID, "workspace must be 256-byte aligned");
   const LatentWs w = expanded_ws(L, num_tokens, max_kv_len);
   if (workspace && workspace_bytes < w.total)
     return fail(PA_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
+  int num_sms = 0;
+  if (int rc = sms_of_current_device(&num_sms)) return rc;
   ExpandedParams p{q, k_nope, k_rope, v, query_start_loc, kv_start_loc, out, num_seqs, num_tokens,
                          num_kv_tokens, max_query_len, max_kv_len, L->num_heads, L->q_stride, L->q_head_stride,
                          L->k_stride, L->k_head_stride, L->kr_stride, L->v_stride, L->v_head_stride,
