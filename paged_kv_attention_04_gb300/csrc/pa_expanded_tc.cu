@@ -169,6 +169,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sm.abort;
   auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
 
+  if (tid == kCopyWarp * 32) {
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.kr);
+    prefetch_map(&maps.v);
+  }
+  // few requests and whole units: the copy warp alone looks at the lengths, a lane a request
+  const bool dealt = !p.part_acc && p.num_seqs <= 32;
+  ESpan mine{};
+  int err = 0;
+  if (dealt && warp == kCopyWarp && lane < p.num_seqs) err = span_of(p, lane, mine);
   if (tid == 0) {
     for (int i = 0; i < eNumBars; ++i) {
       uint32_t n = 1;
@@ -191,21 +202,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's stretch of the line, beginning in request start_r
   long long lo = 0, hi = 0;
-  {
+  if (!dealt) {
     const int per = (p.num_seqs + kThreads - 1) / kThreads;
     const int ra = min(tid * per, p.num_seqs), rb = min(ra + per, p.num_seqs);
-    long long mine = 0, total = 0;
-    int err = 0;
+    long long line = 0, total = 0;  // this thread's requests, all
+#pragma unroll 1
     for (int r = ra; r < rb; ++r) {
       ESpan s;
       err |= span_of(p, r, s);
-      mine += s.head_len * p.num_heads;
+      line += s.head_len * p.num_heads;
     }
     if (err) {
       if (blockIdx.x == 0) flag_error(p.status, err);
       if (err & PA_DEV_QSL) sm.bad = 1;
     }
-    long long before = mine;  // inclusive scan over the threads
+    long long before = line;  // inclusive scan over the threads
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, before, o);
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) before += sm.sums[w];
       total += sm.sums[w];
     }
-    before -= mine;
+    before -= line;
     if (sm.bad) total = 0;
     // (cut units: every stretch is long enough for a piece)
     const long long ctas = p.part_acc ? max(1LL, min(static_cast<long long>(gridDim.x), total / (kUnitCost + kMinPiece)))
@@ -230,8 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.total = total;
       sm.ctas = static_cast<int>(ctas);
     }
-    if (lo < hi && before <= lo && lo < before + mine) {
+    if (lo < hi && before <= lo && lo < before + line) {
       long long pos = before;
+#pragma unroll 1
       for (int r = ra; r < rb; ++r) {
         ESpan s;
         span_of(p, r, s);
@@ -247,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   wait_prior_grid();
+  launch_dependents();  // (the joining kernel's launch; it waits for this grid)
 
   if (warp >= kCopyWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
@@ -321,10 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         u.slot = -1;
         return u;
       };
-      if (!p.part_acc && p.num_seqs <= 32) {
+      if (dealt) {
         // a lane a request: its units have levels, 256 keys apart, and come in order of these
-        ESpan s{};
-        if (lane < p.num_seqs && !sm.bad) span_of(p, lane, s);
+        ESpan s = mine;
+        err = __reduce_or_sync(0xffffffffu, err);
+        if (err && blockIdx.x == 0 && lane == 0) flag_error(p.status, err);
+        if (err & PA_DEV_QSL) s.tiles = 0;
         const int low = (s.S - s.L) / kUnitRows;
         int level = __reduce_max_sync(0xffffffffu, s.tiles ? low + s.tiles - 1 : -1);
         long long base = 0;  // units of higher levels

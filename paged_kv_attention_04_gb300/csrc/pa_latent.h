@@ -8,7 +8,7 @@ namespace pa {
 constexpr int kLatentRope = 64;       // numbers of the shared key part
 constexpr int kLatentMaxHeads = 256;
 constexpr int kLatentMaxCtas = 152;  // of the bf16 kernel: workspaces are sized for them
-constexpr int kLatentRecWords = 4;   // of a CTA's record
+constexpr int kLatentRecWords = 8;   // of a CTA's record
 
 struct LatentWriteArgs {
   const void *c, *k;

@@ -48,6 +48,7 @@ constexpr float kGrowth = 8.f;      // base-2 growth of a maximum that moves the
 constexpr int kUnitCost = 2;        // what a unit costs beside its tiles, in tiles
 constexpr uint32_t kPollLimit = 1u << 26;
 constexpr int kMinStretch = kUnitCost + 1;  // shortest stretch of the line for a CTA: a unit of one tile
+constexpr int kWholeTiles = 6;      // units of up to so many tiles are not cut: joining costs 5 us
 
 template <int R, int N>
 struct Cfg {
@@ -147,7 +148,7 @@ __device__ __forceinline__ int group_of(long long x, long long total, int groups
 template <int R, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_tc_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap,
-                     const __grid_constant__ CUtensorMap kmap, const int ways) {
+                     const __grid_constant__ CUtensorMap kmap, const int ways, const bool whole) {
   using C = Cfg<R, N>;
   extern __shared__ __align__(1024) unsigned char smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + C::kSmallOff);
@@ -168,6 +169,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Span s0{};
   int err = ra < rb ? span_of<N>(p, sh, ra, s0) : 0;
 
+  if (tid == kCopyWarp * 32) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+  }
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
@@ -243,10 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   wait_prior_grid();
+  launch_dependents();  // (the joining kernel's launch; it waits for this grid)
 
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------ units and copies
-    if (lane == 0) p.recs[blockIdx.x * kLatentRecWords + 3] = 0;
+    if (lane == 0) {
+      p.recs[blockIdx.x * kLatentRecWords + 3] = 0;
+      p.recs[blockIdx.x * kLatentRecWords + 4] = 0;
+    }
     int uc = 0;        // units published
     uint32_t g = 0;    // tiles copied
     bool ok = !*abort;
@@ -335,7 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nk = (seen + kKeys - 1) / kKeys;
           const long long f = ua + kUnitCost;  // the first tile's place
           u.t0 = static_cast<int>(max(0LL, lo - f));
-          const int t1 = static_cast<int>(min(static_cast<long long>(nk), hi - f));
+          int t1 = static_cast<int>(min(static_cast<long long>(nk), hi - f));
+          if (whole) {  // the CTA in whose stretch its middle lies takes it
+            const long long middle = ua + s.len / 2;
+            u.t0 = 0;
+            t1 = middle >= lo && middle < hi ? nk : 0;
+          }
           if (u.t0 >= t1) continue;
           u.n = t1 - u.t0;
           u.slot = u.n == nk ? -1 : static_cast<int>(blockIdx.x) * 2 + (u.t0 == 0);
@@ -346,6 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             rec[2] = ways;
             rec[3] = group_of(f + nk - 1, total, sh.groups) - sh.group + 1;
           }
+          // (a CTA of a later piece helps joining: how many CTAs before it the first piece lies)
+          if (u.t0 > 0 && lane == 0)
+            p.recs[blockIdx.x * kLatentRecWords + 4] = (sh.group - group_of(f, total, sh.groups)) * ways;
           ok = run(u);
         }
         pos += static_cast<long long>(s.units) * s.len;
@@ -686,27 +703,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of units that a border cut, in the order of their keys.  The CTA that
-// holds a unit's first piece has left a record; 8 CTAs a record.  A warp joins a row's pieces
-// one after the other where they are few; else a CTA's warps take every eighth piece of a row.
+// Joins the pieces of units that a border cut, in the order of their keys.  The CTA that held a unit's
+// first piece has left a record; 8 CTAs a record.  Where there are few pieces, a warp of these
+// joins a row's one after the other; else the 8 CTAs of every piece take a row each, and
+// their warps every eighth piece of it.
 template <int R, int N>
 __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) {
   constexpr int kVec = R / 128;  // float4 of a lane
+  constexpr int kFew = 8;
   __shared__ float4 acc_s[8][R / 4];
   __shared__ float2 ml_s[8];
   wait_prior_grid();
-  const int* rec = p.recs + blockIdx.x * kLatentRecWords;
-  const int pieces = rec[3];
-  if (pieces == 0) return;
-  const int row0 = rec[0], rows = rec[1], ways = rec[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // piece k: the first CTA's slot 1, then slot 0 of the following ones
-  auto slot = [&](int k) {
-    return (static_cast<long long>(blockIdx.x + k * ways) * 2 + (k == 0)) * N;
-  };
-  const bool few = pieces <= 8;
-  const int step = few ? 64 : 8;
-  for (int n = few ? blockIdx.y * 8 + warp : blockIdx.y; n < rows; n += step) {
+  const int back = p.recs[blockIdx.x * kLatentRecWords + 4];
+  // the unit that begins in this CTA's stretch, then the one that goes on in it
+  for (int own = 1; own >= 0; --own) {
+    if (!own && back == 0) break;
+    const int first = blockIdx.x - (own ? 0 : back);  // CTA of the first piece
+    const int* rec = p.recs + first * kLatentRecWords;
+    const int row0 = rec[0], rows = rec[1], ways = rec[2], pieces = rec[3];
+    const bool few = pieces <= kFew;
+    if (pieces == 0 || (few && !own)) continue;
+    // piece k: the first CTA's slot 1, then slot 0 of the following ones
+    auto slot = [&](int k) { return (static_cast<long long>(first + k * ways) * 2 + (k == 0)) * N; };
+    const int n = few ? blockIdx.y * 8 + warp : (own ? 0 : back / ways) * 8 + blockIdx.y;
+    if (n >= rows) continue;  // (a whole CTA where its warps share a row)
     float m = -CUDART_INF_F, l = 0.f;
     float4 acc[kVec];
 #pragma unroll
@@ -743,20 +764,18 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) 
       add(ml[1], x[1]);
     }
     if (!few) {
+      __syncthreads();  // (the row before is read)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) acc_s[warp][i * 32 + lane] = acc[i];
       if (lane == 0) ml_s[warp] = make_float2(m, l);
       __syncthreads();
-      if (warp == 0) {
-        for (int w = 1; w < 8; ++w) {
-          float4 x[kVec];
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) x[i] = acc_s[w][i * 32 + lane];
-          add(ml_s[w], x);
-        }
-      }
-      __syncthreads();
       if (warp != 0) continue;
+      for (int w = 1; w < 8; ++w) {
+        float4 x[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[i] = acc_s[w][i * 32 + lane];
+        add(ml_s[w], x);
+      }
     }
     const float inv = 1.f / l;
     uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(row0 + n) * R);
@@ -798,7 +817,11 @@ cudaError_t launch_latent(const LatentParams& p, int num_sms, cudaStream_t strea
   // decodes of more heads than a unit's rows: CTAs side by side take the row tiles of
   // the same keys, so that all but the first read them from L2
   int ways = p.max_query_len == 1 ? (p.num_heads + N - 1) / N : 1;
-  const int ctas = (num_sms < kLatentMaxCtas ? num_sms : kLatentMaxCtas) / ways * ways;
+  // no more CTAs than the step can have stretches
+  const long long tiles = (static_cast<long long>(p.num_heads) * p.max_query_len + N - 1) / N;
+  const long long line = p.num_seqs * ((tiles + ways - 1) / ways) * ((p.max_seq_len + kKeys - 1) / kKeys + kUnitCost);
+  const int most = (num_sms < kLatentMaxCtas ? num_sms : kLatentMaxCtas) / ways;
+  const int ctas = static_cast<int>(line / kMinStretch < most ? line / kMinStretch : most) * ways;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
@@ -809,8 +832,9 @@ cudaError_t launch_latent(const LatentParams& p, int num_sms, cudaStream_t strea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, latent_tc_kernel<R, N>, p, qmap, kmap, ways);
-  if (e != cudaSuccess || p.max_seq_len <= kKeys) return e;  // (units of one tile are never cut)
+  const bool whole = p.max_seq_len <= kWholeTiles * kKeys;
+  e = cudaLaunchKernelEx(&cfg, latent_tc_kernel<R, N>, p, qmap, kmap, ways, whole);
+  if (e != cudaSuccess || whole) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
