@@ -174,6 +174,9 @@ def _rows_message(name: str, t, n: int, layout: pa_layout) -> str:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream, dev: int) -> int | None:
     if stream is None:
         return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
@@ -186,7 +189,7 @@ def _launch(fn, dev: int, stream, *args) -> None:
     """Call fn(*args, stream) with the tensors' device current: the library
     launches on the current device."""
     s = _stream(stream, dev)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -595,7 +598,7 @@ def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max
     ws, nbytes = None, 0
     if workspace is not None:
         ws, nbytes = _workspace(workspace, dev)
-    else:
+    elif max_kv_len >= 1024:  # (shorter requests are never cut)
         nbytes = lib().pa_expanded_workspace_size(layout, n, max_kv_len)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
