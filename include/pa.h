@@ -396,6 +396,8 @@ size_t pa_latent_workspace_size(const pa_latent_layout* layout, int num_seqs, in
  * the second product.  NaN or infinity in a slot within a request's length reaches
  * the rows that see it, and may reach (as NaN) rows of the same request that do not.
  * Results do not depend on timing: the work is cut by lengths alone and joined in order.
+ * Calls whose work overlaps on the GPU (other streams, graphs replayed side by side) need
+ * workspaces of their own.  Everything runs on `stream`.
  */
 int pa_latent_forward(const void* q, const void* cache, const int32_t* block_tables,
                       int max_blocks_per_seq, const int32_t* seq_lens,
@@ -435,9 +437,10 @@ typedef struct {
  * L > S or above a bound set PA_DEV_LENGTHS and their rows are left unwritten; bad start arrays
  * set PA_DEV_QSL and nothing is written.  Rounding, NaN and early reads (of both start arrays)
  * as for pa_latent_forward.
- *   workspace  device scratch of pa_expanded_workspace_size bytes, 256-byte aligned, with which a
- *              few long rows tiles are cut over the GPU's SMs; NULL: they are not (the results
- *              differ in rounding alone, the time by up to a fifth and more)
+ *   workspace  device scratch of pa_expanded_workspace_size bytes, 256-byte aligned, with which the work
+ *              of a few long requests is cut over the GPU's SMs (its contents need no initialisation);
+ *              NULL: it is not (results differ in rounding alone)
+ * Calls whose work overlaps on the GPU need workspaces of their own.
  */
 int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, const void* v,
                         const int32_t* query_start_loc, const int32_t* kv_start_loc, int num_seqs,

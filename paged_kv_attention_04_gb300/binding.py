@@ -601,11 +601,13 @@ def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max
     elif max_kv_len >= 1024:  # (shorter requests are never cut)
         nbytes = lib().pa_expanded_workspace_size(layout, n, max_kv_len)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            if stream is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            else:  # of that stream: behind what it still runs, and before what it gets next
+                with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                       else torch.cuda.ExternalStream(int(stream), device=q.device)):
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
-            if stream is not None:  # its memory may be given out again when that stream is done
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                        else torch.cuda.ExternalStream(int(stream), device=q.device))
     _launch(lib().pa_expanded_forward, dev, stream, q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(),
             v.data_ptr(), _whole("query_start_loc", query_start_loc, dev, torch.int32, (b + 1,)),
             _whole("kv_start_loc", kv_start_loc, dev, torch.int32, (b + 1,)), b, n, tk, max_query_len, max_kv_len,

@@ -119,6 +119,8 @@ int pa_latent_write(const void* c, int64_t c_stride, const void* k_rope, int64_t
     return fail(PA_ERR_INVALID, "q or q_out: a head or token stride is smaller than what it steps over");
   if (q && q == q_out && (q_stride != qo_stride || q_head_stride != qo_head_stride))
     return fail(PA_ERR_INVALID, "q_out may be q only with the same strides");
+  if (num_tokens * (1LL + (q ? layout->num_heads : 0)) > 0x7fffffffLL)
+    return fail(PA_ERR_INVALID, "too many rows for one call");
   const LatentWriteArgs a{c, k_rope, c_stride, k_stride, norm_weight, eps, q, q_stride, q_head_stride,
                           rope, slot_mapping, num_tokens, q_out, qo_stride, qo_head_stride, cache, status};
   return done(launch_latent_write(a, *layout, static_cast<cudaStream_t>(stream)), "latent write launch");

@@ -205,6 +205,28 @@ def test_repeats_streams_and_graph():
     assert torch.equal(ds[0]["out"], first[1])
 
 
+def test_cut_units_on_another_stream():
+    """The workspace that the call takes itself belongs to the stream it runs on: memory that work on the current
+    stream still reads is not given to it."""
+    step = Prompts(4, 128, [300], [3000], seed=12)
+    want, mag = step.want()
+    side = torch.cuda.Stream()
+    d = step.gpu()
+    torch.cuda.synchronize()
+    need = P.pa_expanded_workspace_size(4, 128, 300, 3000)
+    for handle in (side, side.cuda_stream):
+        busy = torch.full((need // 4,), 3.0, device="cuda")
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            big = (big @ big).clamp(-1, 1)
+        kept = busy + big[0, 0] * 0  # read late on the current stream
+        del busy
+        step.run(d, stream=handle)
+        torch.cuda.synchronize()
+        assert (kept == 3).all()
+        check(d["out"], want, mag, BF16, step.logit_size(), 192)
+
+
 def test_layer_step():
     """A layer as it runs: prompts' latents appended (norm, rotation), read back and expanded for the prompts'
     attention, then two decode steps over the cache in the absorbed form; each against the 64-bit layer."""

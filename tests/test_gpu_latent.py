@@ -318,3 +318,51 @@ def test_streams_and_graph():
     steps[0].q, steps[0].seq_lens = steps[1].q, np.maximum(1, steps[0].seq_lens - 37)
     want, mag = steps[0].want()
     check(d["out"], want, mag, BF16, steps[0].logit_size(), 576)
+
+
+def test_cache_past_4_gib():
+    """Slots whose bytes lie past 32 bits: written, read back and attended over."""
+    heads, r, n = 4, 512, 300
+    blocks = (5 << 30) // (16 * 576 * 2)
+    cache = torch.empty(blocks, 16, r + 64, dtype=BF16, device="cuda")
+    small = Step(heads, r, [1, 2], [n, 40], seed=30)
+    lay = P.latent_layout_of(cache, heads)
+    # the small cache's blocks, written far up by their rows
+    high = blocks - 1 - torch.arange(small.blocks)
+    rows = small.cache.flatten(0, 1).nan_to_num()
+    slots = (high[:, None] * 16 + torch.arange(16)).flatten().cuda()
+    tab = torch.from_numpy(O.table(1, 64)).float().cuda()  # position 0 turns nothing
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = rows.cuda()
+    P.pa_latent_write(g[:, :r], g[:, r:], None, torch.zeros(len(rows), dtype=torch.int64, device="cuda"), tab, slots, None, cache,
+                      lay, status=status)
+    c, k = torch.empty(len(rows), r, dtype=BF16, device="cuda"), torch.empty(len(rows), 64, dtype=BF16, device="cuda")
+    P.pa_latent_read(cache, slots, c, k, lay, status)
+    d = small.gpu()
+    d["cache"] = cache
+    d["tables"] = torch.where(d["tables"] >= 0, blocks - 1 - d["tables"], d["tables"])
+    d["status"] = status
+    small.run(d, layout=lay)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(torch.cat([c, k], -1).cpu(), rows)
+    want, mag = small.want()
+    check(d["out"], want, mag, BF16, small.logit_size(), 576)
+
+
+def test_same_cache_two_steps_at_once():
+    """Two steps on two streams read one cache, each with its workspace and its head count."""
+    a = Step(16, 512, [1] * 20, list(range(50, 1050, 50)), seed=31)
+    b = Step(64, 512, [1] * 20, list(range(50, 1050, 50)), seed=31)
+    b.cache, b.tables = a.cache, a.tables
+    da, db = a.gpu(), b.gpu()
+    db["cache"] = da["cache"]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        a.run(da, stream=s1)
+        b.run(db, stream=s2.cuda_stream)
+    torch.cuda.synchronize()
+    for st, d in ((a, da), (b, db)):
+        want, mag = st.want()
+        check(d["out"], want, mag, BF16, st.logit_size(), 576)
