@@ -16,9 +16,11 @@
 // as rows (MN-major) A of the second, so there is one copy of it.
 //
 // Roles: warps 0-3 and 4-7 softmax and output of half of the query rows each, warp 8 units and copies,
-// warp 9 MMA issue.  Two 64-key tiles of R = 512 fill shared memory, and a tile stays for its copy
-// (2 us from HBM), S, softmax and O: to keep HBM busy the copies of the tiles after them are begun as
-// prefetches to L2.
+// warps 9 and 10 the issue of S and of O.  Two 64-key tiles of R = 512 fill shared memory, and a tile stays for its
+// copy (2 us from HBM), S, softmax and O, so this chain is kept short: the copies of the tiles
+// after them are begun as prefetches to L2; a tile comes and goes in two parts (half of the latent
+// each, the second with the key part), S beginning on the first and O freeing it; P takes the
+// place of the key part, which only S reads; O does not wait for the issue of the next S.
 // S' has a key per TMEM lane (16 of every 32) and is read as matrix fragments: column maxima by
 // shuffles over lanes and a trade between the four warps in shared memory.  The reference
 // of a column moves only when its maximum grows by more than 2^8; P is written transposed
@@ -40,13 +42,12 @@ using namespace tc;
 
 constexpr int kKeys = 64;           // keys of a tile
 constexpr int kPages = kKeys / kBlockSize;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kCopyWarp = 8, kSWarp = 9, kOWarp = 10;
+constexpr int kThreads = 352;
 constexpr int kSoftThreads = 256;
 constexpr int kAhead = 2;           // tiles that are prefetched to L2 behind the one to be copied
 constexpr float kGrowth = 8.f;      // base-2 growth of a maximum that moves the reference
 constexpr int kUnitCost = 2;        // what a unit costs beside its tiles, in tiles
-constexpr uint32_t kPollLimit = 1u << 26;
 constexpr int kMinStretch = kUnitCost + 1;  // shortest stretch of the line for a CTA: a unit of one tile
 constexpr int kWholeTiles = 6;      // units of up to so many tiles are not cut: joining costs 5 us
 
@@ -57,18 +58,20 @@ struct Cfg {
   static constexpr int kPageBytes = 2 * kGroupBytes;
   static constexpr int kTileBytes = kPages * kPageBytes;
   static constexpr int kQBytes = N * (R + kLatentRope) * 2;  // [slice][N rows][128 bytes]
-  static constexpr int kPBytes = N * kKeys * 2;              // [N rows][128 bytes]
-  static constexpr bool kTight = R == 512 && N == 64;
   static constexpr int kBufs = R == 512 ? 2 : 4;   // tiles
   static constexpr int kQs = N == 64 ? 1 : 2;
-  static constexpr int kPs = kTight ? 1 : 2;
   static constexpr int kQOff = kBufs * kTileBytes;
-  static constexpr int kPOff = kQOff + kQs * kQBytes;
-  static constexpr int kSmallOff = kPOff + kPs * kPBytes;
+  static constexpr int kSmallOff = kQOff + kQs * kQBytes;
   static constexpr int kSmemBytes = kSmallOff + 3072;
+  // parts of a tile: slices 0 .. kHalf - 1, and the others with the key part; P in that one's place,
+  // [N rows][128 bytes] with the slice's 1 KB a group of 8
+  static constexpr int kHalf = R / 128;
+  __host__ __device__ static constexpr int part_bytes(int h) { return kKeys * (kHalf + h) * 128; }
+  static constexpr int kPOff = (kSlices - 1) * 1024;
   static constexpr int kBlocks = R / 128;          // of 128 latent numbers
   static constexpr int kTmemS = 256;               // S of even and odd tiles behind O
   static_assert(kBlocks * N <= 256, "O fits beside S");
+  static_assert(N <= kKeys, "P fits the key part");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
 };
 
@@ -85,16 +88,16 @@ struct Unit {
 
 enum Bar : int {
   kUnitFull = 0,   // [2]
-  kUnitEmpty = 2,  // [2] (8 softmax warps, MMA)
+  kUnitEmpty = 2,  // [2] (8 softmax warps, S, O)
   kQFull = 4,      // [2] TMA
   kQEmpty = 6,     // [2] the unit's last S done
-  kKFull = 8,      // [4] TMA
-  kKEmpty = 12,    // [4] O += of the tile done: frees the tile and its P
-  kSFull = 16,     // [2] S done
-  kPFull = 18,     // [2] S read, P written, O rescaled (8 warps)
-  kTrade = 20,     // [2] the softmax warps of a half meet (4 warps)
-  kDrain = 22,
-  kNumBars = 23
+  kKFull = 8,      // [4] TMA, the tile's first part; [4] its second
+  kKEmpty = 16,    // [4] O += of the first part done: frees it; [4] the second's, and P
+  kSFull = 24,     // [2] S done
+  kPFull = 26,     // [2] S read, P written, O rescaled (8 warps)
+  kTrade = 28,     // [2] the softmax warps of a half meet (4 warps)
+  kDrain = 30,     // [2]
+  kNumBars = 32
 };
 
 // The line: what request r (rows a .. a + L - 1 of the step, S keys) takes of it.
@@ -115,6 +118,12 @@ struct Small {
   Span start;
 };
 static_assert(sizeof(Small) <= 3072, "small shared memory");
+
+struct Maps {
+  CUtensorMap q;
+  CUtensorMap part[2];  // the parts of 8 keys of a page
+  CUtensorMap page;     // a page, for prefetches
+};
 
 struct Shape {
   int ways, way;     // a request's row tiles are dealt to `ways` CTAs that read the same keys
@@ -147,8 +156,7 @@ __device__ __forceinline__ int group_of(long long x, long long total, int groups
 
 template <int R, int N>
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_tc_kernel(const LatentParams p, const __grid_constant__ CUtensorMap qmap,
-                     const __grid_constant__ CUtensorMap kmap, const int ways, const bool whole) {
+    latent_tc_kernel(const LatentParams p, const __grid_constant__ Maps maps, const int ways, const bool whole) {
   using C = Cfg<R, N>;
   extern __shared__ __align__(1024) unsigned char smem[];
   Small& sm = *reinterpret_cast<Small*>(smem + C::kSmallOff);
@@ -170,13 +178,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   int err = ra < rb ? span_of<N>(p, sh, ra, s0) : 0;
 
   if (tid == kCopyWarp * 32) {
-    prefetch_map(&qmap);
-    prefetch_map(&kmap);
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.page);
+    prefetch_map(&maps.part[0]);
+    prefetch_map(&maps.part[1]);
   }
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 9;
+      if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 10;
       if (i == kPFull || i == kPFull + 1) n = 8;
       if (i == kTrade || i == kTrade + 1) n = 4;
       mbar_init(bar(i), n);
@@ -258,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int uc = 0;        // units published
     uint32_t g = 0;    // tiles copied
+    bool half = false; // ... and the first part of one more
     bool ok = !*abort;
     auto publish = [&](const Unit& u) {
       const int slot = uc & 1;
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_expect_tx(bar(kQFull + qs), C::kQBytes);
       __syncwarp();
       if (lane < C::kSlices)
-        tma_load_2d(sbase + C::kQOff + qs * C::kQBytes + lane * N * 128, &qmap, lane * 64, u.row0,
+        tma_load_2d(sbase + C::kQOff + qs * C::kQBytes + lane * N * 128, &maps.q, lane * 64, u.row0,
                     bar(kQFull + qs));
       ++uc;
       // block of page `lane` (< 4) of tile t: `now`'s group or the next
@@ -302,19 +313,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (; fetched <= t + kAhead && fetched < end; ++fetched) {
           const int ph = block_of(fetched, t >> 3);
-          if (lane < kPages && ph >= 0 && ph < p.num_blocks) tma_prefetch_5d(&kmap, 0, 0, 0, 0, ph);
+          if (lane < kPages && ph >= 0 && ph < p.num_blocks) tma_prefetch_5d(&maps.page, 0, 0, 0, 0, ph);
         }
-        int cur = block_of(t, t >> 3);
-        if (g >= C::kBufs && !wait_bar(bar(kKEmpty + b), (g / C::kBufs - 1) & 1, abort, p.status)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + b), C::kTileBytes);
-        __syncwarp();
-        if (lane < kPages) {
-          // a page past the keys or with a bad table entry is read out of bounds: zeros
-          if (cur < 0 || cur >= p.num_blocks) {
-            if ((t * kPages + lane) * kBlockSize < u.seq) flag_error(p.status, PA_DEV_BLOCK_RANGE);
-            cur = p.num_blocks;
-          }
-          tma_load_5d(sbase + b * C::kTileBytes + lane * C::kPageBytes, &kmap, 0, 0, 0, 0, cur, bar(kKFull + b));
+        // 8 lanes a part, one for every 8 keys; a page past the keys or with a bad table entry is
+        // read out of bounds: zeros
+        const int page = (lane & 7) >> 1, part = lane >> 3;
+        const int src = (t & 7) * kPages + page;
+        int cur = __shfl_sync(0xffffffffu, now, src);
+        if (cur < 0 || cur >= p.num_blocks) {
+          if (lane < 8 && (t * kPages + page) * kBlockSize < u.seq) flag_error(p.status, PA_DEV_BLOCK_RANGE);
+          cur = p.num_blocks;
+        }
+        const uint32_t dst = sbase + b * C::kTileBytes + (lane & 7) * C::kGroupBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (g >= C::kBufs && !wait_bar(bar(kKEmpty + 4 * h + b), (g / C::kBufs - 1) & 1, abort, p.status)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + 4 * h + b), C::part_bytes(h));
+          __syncwarp();
+          if (part == h)
+            tma_load_5d(dst + h * C::kHalf * 1024, &maps.part[h], 0, 0, h * C::kHalf, lane & 1, cur,
+                        bar(kKFull + 4 * h + b));
+          half = h == 0;
         }
       }
       return true;
@@ -373,104 +392,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) publish(end);
     if (*abort) {  // let every copy issued land before the CTA ends
       for (uint32_t i = g > C::kBufs ? g - C::kBufs : 0; i < g; ++i)
-        drain_wait(bar(kKFull + i % C::kBufs), (i / C::kBufs) & 1);
+        for (int h = 0; h < 2; ++h) drain_wait(bar(kKFull + 4 * h + i % C::kBufs), (i / C::kBufs) & 1);
+      // (the first part of a tile whose second was not waited for any more)
+      if (half) drain_wait(bar(kKFull + g % C::kBufs), (g / C::kBufs) & 1);
       for (int i = uc > C::kQs ? uc - C::kQs : 0; i < uc; ++i)
         drain_wait(bar(kQFull + i % C::kQs), (i / C::kQs) & 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issue
-    constexpr uint32_t kIdS = idesc_bf16(kKeys, N, 0);
-    constexpr uint32_t kIdO = idesc_bf16(128, N, 0) | (1u << 15);  // A MN-major
-    const uint64_t dk = smem_desc_sw128(sbase, 16, C::kGroupBytes);
-    const uint64_t dv = smem_desc_sw128(sbase, 1024, C::kGroupBytes);
-    const uint64_t dq = smem_desc_sw128(sbase + C::kQOff, 16, 1024);
-    const uint64_t dp = smem_desc_sw128(sbase + C::kPOff, 16, 1024);
-    auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
-    auto ready = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
-    };
-    // S of the next tile and O += of the oldest are issued as what they need arrives, S at
-    // most one tile ahead (two S buffers): waiting for either would hold up the other.
-    int uc = -1;            // unit of the next S
-    int left = 0;           // its tiles without an S
-    bool fresh = false;     // its Q has not been waited for
-    bool ends = false;
-    uint32_t gs = 0, gp = 0;
-    uint32_t firsts = 0;    // bit g & 1: tile g is its unit's first
-    uint32_t idle = 0;      // polls without progress
-    while (!(ends && gp == gs)) {
-      bool moved = false;
-      if (!ends && gs - gp < 2) {
-        if (left == 0) {
-          const int slot = (uc + 1) & 1;
-          if (ready(bar(kUnitFull + slot), ((uc + 1) >> 1) & 1)) {
-            ++uc;
-            const int r = sm.units[slot].r;
-            left = sm.units[slot].n;
-            warp_arrive(bar(kUnitEmpty + slot));
-            if (r < 0) {
-              ends = true;
-              left = 0;
-            }
-            fresh = true;
-            moved = true;
-          }
-        } else if (ready(bar(kKFull + gs % C::kBufs), (gs / C::kBufs) & 1) &&
-                   (!fresh || ready(bar(kQFull + uc % C::kQs), (uc / C::kQs) & 1))) {
-          const uint32_t b = gs % C::kBufs;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t kb = adv(dk, b * C::kTileBytes), qb = adv(dq, (uc % C::kQs) * C::kQBytes);
-            const uint32_t d = tmem + C::kTmemS + (gs & 1) * N;
+  } else if (warp >= kSWarp) {
+    // ------------------------------------------------------------ MMA issue, one thread each
+    if (elect_one() && !*abort) {
+      auto adv = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
+      auto wait = [&](int i, uint32_t parity) { return wait_one(bar(i), parity, abort, p.status); };
+      const uint64_t dk = smem_desc_sw128(sbase, 16, C::kGroupBytes);
+      const uint64_t dv = smem_desc_sw128(sbase, 1024, C::kGroupBytes);
+      const uint64_t dq = smem_desc_sw128(sbase + C::kQOff, 16, 1024);
+      uint32_t g = 0, b = 0, phase = 0;  // tiles, and the buffer and its round
+      bool ok = true;
+      for (int uc = 0; ok; ++uc) {
+        const int slot = uc & 1;
+        if (!wait(kUnitFull + slot, (uc >> 1) & 1)) break;
+        const int n = sm.units[slot].r < 0 ? 0 : sm.units[slot].n;
+        mbar_arrive(bar(kUnitEmpty + slot));
+        if (n == 0) break;
+        const int qs = uc % C::kQs;
+        if (warp == kSWarp && !wait(kQFull + qs, (uc / C::kQs) & 1)) break;
+        for (int t = 0; t < n; ++t, ++g) {
+          if (warp == kSWarp) {
+            // S of tile g - 2 is read (phase -1 of a barrier counts as complete)
+            ok = wait_both(bar(kKFull + b), phase, bar(kPFull + (g & 1)), ((g >> 1) - 1) & 1, abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            constexpr uint32_t kId = idesc_bf16(kKeys, N, 0);
+            const uint64_t kb = adv(dk, b * C::kTileBytes), qb = adv(dq, qs * C::kQBytes);
+            const uint32_t d = tmem + C::kTmemS + (g & 1) * N;
 #pragma unroll
-            for (int i = 0; i < C::kSlices * 4; ++i)
+            for (int i = 0; i < C::kHalf * 4; ++i)
               tc_mma_f16(d, adv(kb, (i >> 2) * 1024 + (i & 3) * 32), adv(qb, (i >> 2) * (N * 128) + (i & 3) * 32),
-                         kIdS, i > 0);
-            tc_commit(bar(kSFull + (gs & 1)));
-            if (left == 1) tc_commit(bar(kQEmpty + uc % C::kQs));
+                         kId, i > 0);
+            ok = wait(kKFull + 4 + b, phase);
+            if (!ok) break;
+#pragma unroll
+            for (int i = C::kHalf * 4; i < C::kSlices * 4; ++i)
+              tc_mma_f16(d, adv(kb, (i >> 2) * 1024 + (i & 3) * 32), adv(qb, (i >> 2) * (N * 128) + (i & 3) * 32),
+                         kId, 1);
+            tc_commit(bar(kSFull + (g & 1)));
+            if (t == n - 1) tc_commit(bar(kQEmpty + qs));
+          } else {
+            ok = wait(kPFull + (g & 1), (g >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            constexpr uint32_t kId = idesc_bf16(128, N, 0) | (1u << 15);  // A MN-major
+            const uint64_t vb = adv(dv, b * C::kTileBytes), pb = adv(dk, b * C::kTileBytes + C::kPOff);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int m = h * C::kBlocks / 2; m < (h + 1) * C::kBlocks / 2; ++m)
+#pragma unroll
+                for (int pg = 0; pg < kPages; ++pg)
+                  tc_mma_f16(tmem + m * N, adv(vb, pg * C::kPageBytes + m * 2048), adv(pb, pg * 32), kId,
+                             t > 0 || pg > 0);
+              tc_commit(bar(kKEmpty + 4 * h + b));
+            }
           }
-          __syncwarp();
-          firsts = fresh ? firsts | (1u << (gs & 1)) : firsts & ~(1u << (gs & 1));
-          fresh = false;
-          --left;
-          ++gs;
-          moved = true;
+          if (++b == C::kBufs) b = 0, phase ^= 1;
         }
-      }
-      if (gp < gs && ready(bar(kPFull + (gp & 1)), (gp >> 1) & 1)) {
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t b = gp % C::kBufs;
-          const uint64_t vb = adv(dv, b * C::kTileBytes), pb = adv(dp, (gp % C::kPs) * C::kPBytes);
-          const bool first = (firsts >> (gp & 1)) & 1;
-#pragma unroll
-          for (int pg = 0; pg < kPages; ++pg)
-#pragma unroll
-            for (int m = 0; m < C::kBlocks; ++m)
-              tc_mma_f16(tmem + m * N, adv(vb, pg * C::kPageBytes + m * 2048), adv(pb, pg * 32), kIdO,
-                         !first || pg > 0);
-          tc_commit(bar(kKEmpty + b));
-        }
-        __syncwarp();
-        ++gp;
-        moved = true;
-      }
-      idle = moved ? 0 : idle + 1;
-      if (__any_sync(0xffffffffu, *abort != 0)) break;
-      if (idle > kPollLimit) {
-        if (elect_one()) {
-          *abort = 1;
-          flag_error(p.status, PA_DEV_TIMEOUT);
-        }
-        __syncwarp();
-        break;
       }
     }
+    __syncwarp();
     if (*abort) {  // nothing may still run on tensor memory when it is freed
-      if (elect_one()) tc_commit(bar(kDrain));
+      const int d = kDrain + (warp == kOWarp);
+      if (elect_one()) tc_commit(bar(d));
       __syncwarp();
-      drain_wait(bar(kDrain), 0);
+      drain_wait(bar(d), 0);
     }
     __syncwarp();
   } else {
@@ -485,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = !*abort;
     // phase of tile i's "O += done"
     auto wait_o = [&](uint32_t i) {
-      return wait_bar(bar(kKEmpty + i % C::kBufs), (i / C::kBufs) & 1, abort, p.status);
+      return wait_bar(bar(kKEmpty + 4 + i % C::kBufs), (i / C::kBufs) & 1, abort, p.status);
     };
     uint32_t trades = 0;
     auto meet = [&]() {
@@ -605,15 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st(at, o);
           }
           tmem_wait_st();
-        } else if (g >= C::kPs) {
-          if (!wait_o(g - C::kPs)) { ok = false; break; }  // P's buffer is free
         }
-        const uint32_t pbuf = sbase + C::kPOff + (g % C::kPs) * C::kPBytes;
+        // P, where the key part was (S has read it)
+        const uint32_t pbuf = sbase + (g % C::kBufs) * C::kTileBytes + C::kPOff;
         // (a matrix of 8 keys x 8 rows a register; lanes 8 k .. 8 k + 7 address matrix k's rows)
         if constexpr (F == 1) {
           const int row = half * H + (lane & 7), chunk = 2 * quarter + ((lane >> 3) & 1);
           asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};\n" ::"r"(
-                           pbuf + row * 128 + ((chunk ^ (row & 7)) << 4)),
+                           pbuf + (row >> 3) * C::kGroupBytes + (row & 7) * 128 + ((chunk ^ (row & 7)) << 4)),
                        "r"(pack_bf16(x[0][0], x[0][1])), "r"(pack_bf16(x[0][2], x[0][3]))
                        : "memory");
         } else {
@@ -621,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < F; i += 2) {
             const int row = half * H + 8 * (i + (lane >> 4)) + (lane & 7), chunk = 2 * quarter + ((lane >> 3) & 1);
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(
-                             pbuf + row * 128 + ((chunk ^ (row & 7)) << 4)),
+                             pbuf + (row >> 3) * C::kGroupBytes + (row & 7) * 128 + ((chunk ^ (row & 7)) << 4)),
                          "r"(pack_bf16(x[i][0], x[i][1])), "r"(pack_bf16(x[i][2], x[i][3])),
                          "r"(pack_bf16(x[i + 1][0], x[i + 1][1])), "r"(pack_bf16(x[i + 1][2], x[i + 1][3]))
                          : "memory");
@@ -801,18 +794,22 @@ cudaError_t launch_latent(const LatentParams& p, int num_sms, cudaStream_t strea
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  CUtensorMap qmap, kmap;
+  Maps maps;
   {
     const cuuint64_t dims[2] = {W, static_cast<cuuint64_t>(p.num_tokens) * p.num_heads};
     const cuuint64_t strides[1] = {W * 2};
     const cuuint32_t box[2] = {64, N};
-    if (!encode_bf16(&qmap, p.q, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode_bf16(&maps.q, p.q, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
   {
     const cuuint64_t dims[5] = {64, 8, C::kSlices, 2, static_cast<cuuint64_t>(p.num_blocks)};
     const cuuint64_t strides[4] = {W * 2, 128, 8 * W * 2, kBlockSize * W * 2};
-    const cuuint32_t box[5] = {64, 8, C::kSlices, 2, 1};
-    if (!encode_bf16(&kmap, p.cache, 5, dims, strides, box)) return cudaErrorInvalidValue;
+    const cuuint32_t page[5] = {64, 8, C::kSlices, 2, 1};
+    const cuuint32_t part0[5] = {64, 8, C::kHalf, 1, 1}, part1[5] = {64, 8, C::kHalf + 1, 1, 1};
+    if (!encode_bf16(&maps.page, p.cache, 5, dims, strides, page) ||
+        !encode_bf16(&maps.part[0], p.cache, 5, dims, strides, part0) ||
+        !encode_bf16(&maps.part[1], p.cache, 5, dims, strides, part1))
+      return cudaErrorInvalidValue;
   }
   // decodes of more heads than a unit's rows: CTAs side by side take the row tiles of
   // the same keys, so that all but the first read them from L2
@@ -833,7 +830,7 @@ cudaError_t launch_latent(const LatentParams& p, int num_sms, cudaStream_t strea
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool whole = p.max_seq_len <= kWholeTiles * kKeys;
-  e = cudaLaunchKernelEx(&cfg, latent_tc_kernel<R, N>, p, qmap, kmap, ways, whole);
+  e = cudaLaunchKernelEx(&cfg, latent_tc_kernel<R, N>, p, maps, ways, whole);
   if (e != cudaSuccess || whole) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8);
   cfg.blockDim = dim3(256);
