@@ -15,8 +15,8 @@
 // Read with the keys as rows (K-major) it is A of the first product, with the numbers
 // as rows (MN-major) A of the second, so there is one copy of it.
 //
-// Roles: warps 0-3 and 4-7 softmax and output of half of the query rows each, warp 8 units and copies,
-// warps 9 and 10 the issue of S and of O.  Two 64-key tiles of R = 512 fill shared memory, and a tile stays for its
+// Roles: warps 0-3 and 4-7 softmax and output of half of the query rows each, warp 8 units and copies (of
+// Q and of the first part of every tile, warp 11 of the second), warps 9 and 10 the issue of S and of O.  Two 64-key tiles of R = 512 fill shared memory, and a tile stays for its
 // copy (2 us from HBM), S, softmax and O, so this chain is kept short: the copies of the tiles
 // after them are begun as prefetches to L2; a tile comes and goes in two parts (half of the latent
 // each, the second with the key part), S beginning on the first and O freeing it; P takes the
@@ -42,8 +42,8 @@ using namespace tc;
 
 constexpr int kKeys = 64;           // keys of a tile
 constexpr int kPages = kKeys / kBlockSize;
-constexpr int kCopyWarp = 8, kSWarp = 9, kOWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kCopyWarp = 8, kSWarp = 9, kOWarp = 10, kCopy2Warp = 11;
+constexpr int kThreads = 384;
 constexpr int kSoftThreads = 256;
 constexpr int kAhead = 2;           // tiles that are prefetched to L2 behind the one to be copied
 constexpr float kGrowth = 8.f;      // base-2 growth of a maximum that moves the reference
@@ -88,7 +88,7 @@ struct Unit {
 
 enum Bar : int {
   kUnitFull = 0,   // [2]
-  kUnitEmpty = 2,  // [2] (8 softmax warps, S, O)
+  kUnitEmpty = 2,  // [2] (8 softmax warps, S, O, second copy warp)
   kQFull = 4,      // [2] TMA
   kQEmpty = 6,     // [2] the unit's last S done
   kKFull = 8,      // [4] TMA, the tile's first part; [4] its second
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 10;
+      if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 11;
       if (i == kPFull || i == kPFull + 1) n = 8;
       if (i == kTrade || i == kTrade + 1) n = 4;
       mbar_init(bar(i), n);
@@ -260,6 +260,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_prior_grid();
   launch_dependents();  // (the joining kernel's launch; it waits for this grid)
 
+  // ---- what both copy warps do: part h of the tiles of a unit
+  // table entries of the pages of 8 tiles, one a lane: of group i of unit u, -1 past the request's keys
+  auto entries = [&](const Unit& u, int i) {
+    const int b = i * 32 + lane;
+    return b * kBlockSize < u.seq ? __ldg(p.block_tables + static_cast<long long>(u.r) * p.max_blocks_per_seq + b) : -1;
+  };
+  // tile t, the g-th of the CTA; now: the entries of its group
+  auto copy_part = [&](const Unit& u, int h, int t, uint32_t g, int now) {
+    const int b = g % C::kBufs, page = (lane & 7) >> 1;  // 8 lanes, one for every 8 keys
+    int cur = __shfl_sync(0xffffffffu, now, (t & 7) * kPages + page);
+    // a page past the keys or with a bad table entry is read out of bounds: zeros
+    if (cur < 0 || cur >= p.num_blocks) {
+      if (lane < 8 && (t * kPages + page) * kBlockSize < u.seq) flag_error(p.status, PA_DEV_BLOCK_RANGE);
+      cur = p.num_blocks;
+    }
+    if (g >= C::kBufs && !wait_bar(bar(kKEmpty + 4 * h + b), (g / C::kBufs - 1) & 1, abort, p.status)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + 4 * h + b), C::part_bytes(h));
+    __syncwarp();
+    if (lane < 8)
+      tma_load_5d(sbase + b * C::kTileBytes + lane * C::kGroupBytes + h * C::kHalf * 1024, &maps.part[h], 0, 0,
+                  h * C::kHalf, lane & 1, cur, bar(kKFull + 4 * h + b));
+    return true;
+  };
+  // (after a timeout: let every copy issued land before the CTA ends)
+  auto drain_part = [&](int h, uint32_t g) {
+    for (uint32_t i = g > C::kBufs ? g - C::kBufs : 0; i < g; ++i)
+      drain_wait(bar(kKFull + 4 * h + i % C::kBufs), (i / C::kBufs) & 1);
+  };
+
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------ units and copies
     if (lane == 0) {
@@ -268,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int uc = 0;        // units published
     uint32_t g = 0;    // tiles copied
-    bool half = false; // ... and the first part of one more
     bool ok = !*abort;
     auto publish = [&](const Unit& u) {
       const int slot = uc & 1;
@@ -281,13 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     auto run = [&](const Unit& u) {
-      const int32_t* table = p.block_tables + static_cast<long long>(u.r) * p.max_blocks_per_seq;
-      // table entries of the pages of 8 tiles, one a lane: of group g, -1 past the request's keys
-      auto entries = [&](int g) {
-        const int b = g * 32 + lane;
-        return b * kBlockSize < u.seq ? __ldg(table + b) : -1;
-      };
-      int now = entries(u.t0 / 8), then = entries(u.t0 / 8 + 1);
+      int now = entries(u, u.t0 / 8), then = entries(u, u.t0 / 8 + 1);
       if (!publish(u)) return false;
       const int qs = uc % C::kQs;
       if (uc >= C::kQs && !wait_bar(bar(kQEmpty + qs), (uc / C::kQs - 1) & 1, abort, p.status)) return false;
@@ -306,35 +328,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int end = u.t0 + u.n;
       int fetched = u.t0 + 1;  // tiles before it are copied or on their way to L2
       for (int t = u.t0; t < end; ++t, ++g) {
-        const int b = g % C::kBufs;
         if ((t & 7) == 0 && t > u.t0) {
           now = then;
-          then = entries(t / 8 + 1);
+          then = entries(u, t / 8 + 1);
         }
         for (; fetched <= t + kAhead && fetched < end; ++fetched) {
           const int ph = block_of(fetched, t >> 3);
           if (lane < kPages && ph >= 0 && ph < p.num_blocks) tma_prefetch_5d(&maps.page, 0, 0, 0, 0, ph);
         }
-        // 8 lanes a part, one for every 8 keys; a page past the keys or with a bad table entry is
-        // read out of bounds: zeros
-        const int page = (lane & 7) >> 1, part = lane >> 3;
-        const int src = (t & 7) * kPages + page;
-        int cur = __shfl_sync(0xffffffffu, now, src);
-        if (cur < 0 || cur >= p.num_blocks) {
-          if (lane < 8 && (t * kPages + page) * kBlockSize < u.seq) flag_error(p.status, PA_DEV_BLOCK_RANGE);
-          cur = p.num_blocks;
-        }
-        const uint32_t dst = sbase + b * C::kTileBytes + (lane & 7) * C::kGroupBytes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (g >= C::kBufs && !wait_bar(bar(kKEmpty + 4 * h + b), (g / C::kBufs - 1) & 1, abort, p.status)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + 4 * h + b), C::part_bytes(h));
-          __syncwarp();
-          if (part == h)
-            tma_load_5d(dst + h * C::kHalf * 1024, &maps.part[h], 0, 0, h * C::kHalf, lane & 1, cur,
-                        bar(kKFull + 4 * h + b));
-          half = h == 0;
-        }
+        if (!copy_part(u, 0, t, g, now)) return false;
       }
       return true;
     };
@@ -390,14 +392,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit end{};
     end.r = -1;
     if (ok) publish(end);
-    if (*abort) {  // let every copy issued land before the CTA ends
-      for (uint32_t i = g > C::kBufs ? g - C::kBufs : 0; i < g; ++i)
-        for (int h = 0; h < 2; ++h) drain_wait(bar(kKFull + 4 * h + i % C::kBufs), (i / C::kBufs) & 1);
-      // (the first part of a tile whose second was not waited for any more)
-      if (half) drain_wait(bar(kKFull + g % C::kBufs), (g / C::kBufs) & 1);
+    if (*abort) {
+      drain_part(0, g);
       for (int i = uc > C::kQs ? uc - C::kQs : 0; i < uc; ++i)
         drain_wait(bar(kQFull + i % C::kQs), (i / C::kQs) & 1);
     }
+    __syncwarp();
+  } else if (warp == kCopy2Warp) {
+    // ------------------------------------------------------------ copies of the second parts
+    uint32_t g = 0;
+    bool ok = !*abort;
+    for (int uc = 0; ok; ++uc) {
+      if (!wait_bar(bar(kUnitFull + (uc & 1)), (uc >> 1) & 1, abort, p.status)) break;
+      const Unit u = sm.units[uc & 1];
+      warp_arrive(bar(kUnitEmpty + (uc & 1)));
+      if (u.r < 0) break;
+      int now = entries(u, u.t0 / 8), then = entries(u, u.t0 / 8 + 1);
+      for (int t = u.t0; t < u.t0 + u.n; ++t, ++g) {
+        if ((t & 7) == 0 && t > u.t0) {
+          now = then;
+          then = entries(u, t / 8 + 1);
+        }
+        ok = copy_part(u, 1, t, g, now);
+        if (!ok) break;
+      }
+    }
+    if (*abort) drain_part(1, g);
     __syncwarp();
   } else if (warp >= kSWarp) {
     // ------------------------------------------------------------ MMA issue, one thread each
@@ -531,44 +551,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // column maxima: over the warp's 16 keys, then the four warps
-        float mx[F][2];
+        // column maxima over the warp's 16 keys: the 8 lanes that share the columns halve them among
+        // themselves, so each ends with one column's; then over the four warps
+        float v[2 * F];
 #pragma unroll
         for (int i = 0; i < F; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float y = fmaxf(x[i][j], x[i][j + 2]);
+          for (int j = 0; j < 2; ++j) v[2 * i + j] = fmaxf(x[i][j], x[i][j + 2]);
+        int own = 0;  // index of this lane's column among its 2 F
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-            mx[i][j] = y;
+        for (int n = 2 * F, o = 16; o >= 4; o >>= 1) {
+          if (n > 1) {
+            n /= 2;
+            const bool up = (lane & o) != 0;
+            if (up) own += n;
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+              const float send = up ? v[k] : v[k + n];
+              v[k] = fmaxf(up ? v[k + n] : v[k], __shfl_xor_sync(0xffffffffu, send, o));
+            }
+          } else {
+            v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
           }
-        if (lane < 4) {
+        }
+        const int col = c0 + 8 * (own >> 1) + (own & 1);
+        sm.mx[g & 1][quarter][col] = v[0];  // (lanes that hold the same column write the same)
+        if (!meet()) { ok = false; break; }
+        v[0] = fmaxf(fmaxf(sm.mx[g & 1][0][col], sm.mx[g & 1][1][col]), fmaxf(sm.mx[g & 1][2][col], sm.mx[g & 1][3][col]));
+        // ... and back to all of them
+#pragma unroll
+        for (int n = 1, o = 64 / (2 * F) / 2 > 16 ? 16 : 64 / (2 * F) / 2; n < 2 * F; n *= 2, o <<= 1) {
+          const bool up = (lane & o) != 0;
+#pragma unroll
+          for (int k = n - 1; k >= 0; --k) {
+            const float other = __shfl_xor_sync(0xffffffffu, v[k], o);
+            const float mine = v[k];
+            v[k] = up ? other : mine;
+            v[k + n] = up ? mine : other;
+          }
+        }
+        bool moved = false;
+#pragma unroll
+        for (int i = 0; i < F; ++i) moved |= v[2 * i] > m[i][0] + kGrowth || v[2 * i + 1] > m[i][1] + kGrowth;
+        moved = __any_sync(0xffffffffu, moved);
+        float f[F][2];
+        if (moved) {
 #pragma unroll
           for (int i = 0; i < F; ++i)
-            *reinterpret_cast<float2*>(&sm.mx[g & 1][quarter][8 * i + c0]) = make_float2(mx[i][0], mx[i][1]);
-        }
-        if (!meet()) { ok = false; break; }
-        bool moved = false;
-        float f[F][2];
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
-          float2 y[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) y[w] = *reinterpret_cast<const float2*>(&sm.mx[g & 1][w][8 * i + c0]);
-          mx[i][0] = fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x));
-          mx[i][1] = fmaxf(fmaxf(y[0].y, y[1].y), fmaxf(y[2].y, y[3].y));
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            f[i][j] = 1.f;
-            if (mx[i][j] > m[i][j] + kGrowth) {  // (also the first finite maximum: m = -inf)
-              f[i][j] = ex2(m[i][j] - mx[i][j]);
-              m[i][j] = mx[i][j];
+            for (int j = 0; j < 2; ++j) {
+              const bool up = v[2 * i + j] > m[i][j] + kGrowth;  // (also the first finite maximum: m = -inf)
+              f[i][j] = up ? ex2(m[i][j] - v[2 * i + j]) : 1.f;
+              if (up) m[i][j] = v[2 * i + j];
               l[i][j] *= f[i][j];
-              moved = true;
             }
-          }
         }
-        moved = __any_sync(0xffffffffu, moved);
         // P and this lane's sums
 #pragma unroll
         for (int i = 0; i < F; ++i)
