@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t nk = 0;               // K tiles copied
       uint32_t nq[2] = {0, 0};       // Q tiles copied
       bool ok = !*abort;
-      if (lane == 0 && p.recs) p.recs[blockIdx.x * kLatentRecWords + 3] = 0;
+      if (lane < 2 && p.recs) p.recs[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
+      __syncwarp();
       auto publish = [&](const EUnit& u) {
         const int s = uc & 1;
         if (uc >= 2 && !wait_bar(bar(eUnitEmpty + s), ((uc >> 1) - 1) & 1, abort, p.status)) return false;
@@ -395,15 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (u.n[1]) u.n[1] = t1 - u.t0;
               const bool whole = c0 == 0 && c1 == len;
               u.slot = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (c0 == 0);
-              if (!whole && c0 == 0 && lane == 0) {
-                int pieces = 2;  // and one for every later border inside
-                for (int c = blockIdx.x + 2; c < sm.ctas; ++c, ++pieces)
-                  if (cut(sm.total * c / sm.ctas) == len) break;
-                int* rec = p.recs + blockIdx.x * kLatentRecWords;
-                rec[0] = u.row0;
-                rec[1] = u.rows;
-                rec[2] = h;
-                rec[3] = pieces;
+              if (!whole) {  // borders inside the unit, before this piece and behind it
+                int piece = 0, pieces = 1;
+                for (int c = blockIdx.x; c > 0 && cut(sm.total * c / sm.ctas) > 0; --c) ++piece;
+                for (int c = blockIdx.x + 1; c < sm.ctas && cut(sm.total * c / sm.ctas) < len; ++c) ++pieces;
+                if (lane == 0) p.recs[u.slot] = make_int4(u.row0, u.rows, h, piece | (piece + pieces) << 16);
               }
               ok = run(u);
             }
@@ -702,44 +699,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of cut units, in the order of their keys: 8 CTAs a record of 32 rows each, a lane
-// a row, a warp D / 8 of its numbers.
+// Joins the pieces of cut units, in the order of their keys.  Every piece has left a record {first row,
+// rows, head, piece and pieces}, and 8 CTAs a piece take part; a lane a row, a warp 8 of its numbers,
+// 4 pieces' loads at once.
 template <int D>
 __global__ void __launch_bounds__(256) expanded_join_kernel(const ExpandedParams p) {
-  constexpr int kVec = D / 32;  // float4 of a thread
+  constexpr int kAtOnce = 4;
   wait_prior_grid();
-  const int* rec = p.recs + blockIdx.x * kLatentRecWords;
-  const int pieces = rec[3], row = blockIdx.y * 32 + (threadIdx.x & 31), chunk = (threadIdx.x >> 5) * kVec;
-  if (pieces == 0 || row >= rec[1]) return;
-  float m = -CUDART_INF_F, l = 0.f;
-  float4 acc[kVec];
+  const int4 recs[2] = {p.recs[blockIdx.x * 2], p.recs[blockIdx.x * 2 + 1]};
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int k = 0; k < pieces; ++k) {
-    // the first CTA's slot 1, then slot 0 of the following ones
-    const long long base = (static_cast<long long>(blockIdx.x + k) * 2 + (k == 0)) * kUnitRows;
-    const float2 ml = p.part_ml[base + row];
-    if (ml.y == 0.f) continue;  // no key of the piece is seen
-    const float nm = fmaxf(m, ml.x);
-    const float fa = m == nm ? 1.f : ex2(m - nm), fb = ml.x == nm ? 1.f : ex2(ml.x - nm);
-    m = nm;
-    l = l * fa + ml.y * fb;
+  for (int which = 0; which < 2; ++which) {
+    const int piece = recs[which].w & 0xffff, pieces = recs[which].w >> 16;
+    const int first = blockIdx.x - piece;  // CTA of the first piece
+    if (pieces == 0) continue;
+    for (int item = (piece * 8 + blockIdx.y) * 8 + (threadIdx.x >> 5); item < kUnitRows / 32 * (D / 8);
+         item += pieces * 64) {
+      const int row = item / (D / 8) * 32 + (threadIdx.x & 31), chunk = item % (D / 8) * 2;
+      if (row >= recs[which].y) break;
+      float m = -CUDART_INF_F, l = 0.f;
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < pieces; k += kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 x[kAtOnce][2];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float4 x = p.part_acc[base * (D / 4) + (chunk + i) * kUnitRows + row];
-      acc[i].x = acc[i].x * fa + x.x * fb;
-      acc[i].y = acc[i].y * fa + x.y * fb;
-      acc[i].z = acc[i].z * fa + x.z * fb;
-      acc[i].w = acc[i].w * fa + x.w * fb;
+        for (int j = 0; j < kAtOnce; ++j) {
+          ml[j].y = 0.f;
+          if (k + j < pieces) {  // the first CTA's slot 1, then slot 0 of the following ones
+            const long long base = (static_cast<long long>(first + k + j) * 2 + (k + j == 0)) * kUnitRows;
+            ml[j] = p.part_ml[base + row];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) x[j][i] = p.part_acc[base * (D / 4) + (chunk + i) * kUnitRows + row];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          if (ml[j].y == 0.f) continue;  // no key of the piece is seen
+          const float nm = fmaxf(m, ml[j].x);
+          const float fa = m == nm ? 1.f : ex2(m - nm), fb = ml[j].x == nm ? 1.f : ex2(ml[j].x - nm);
+          m = nm;
+          l = l * fa + ml[j].y * fb;
+          const float y[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = acc[i] * fa + y[i] * fb;
+        }
+      }
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] *= inv;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
+                           (static_cast<long long>(recs[which].x + row) * p.num_heads + recs[which].z) * D;
+      *reinterpret_cast<uint4*>(out + chunk * 4) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
+                                                             pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
     }
   }
-  const float inv = 1.f / l;
-  uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
-                                        (static_cast<long long>(rec[0] + row) * p.num_heads + rec[2]) * D) + chunk;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i)
-    out[i] = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
 }
 
 namespace {
@@ -789,7 +801,7 @@ cudaError_t launch_expanded(const ExpandedParams& args, int num_sms, cudaStream_
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, expanded_tc_kernel<D>, p, maps);
   if (e != cudaSuccess || !p.part_acc) return e;
-  cfg.gridDim = dim3(ctas, kUnitRows / 32);
+  cfg.gridDim = dim3(ctas, 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, expanded_join_kernel<D>, p);

@@ -8,7 +8,6 @@ namespace pa {
 constexpr int kLatentRope = 64;       // numbers of the shared key part
 constexpr int kLatentMaxHeads = 256;
 constexpr int kLatentMaxCtas = 152;  // of the bf16 kernel: workspaces are sized for them
-constexpr int kLatentRecWords = 8;   // of a CTA's record
 
 struct LatentWriteArgs {
   const void *c, *k;
@@ -43,7 +42,7 @@ struct LatentParams {
   int splits;        // fp32: pieces of every request's keys
   float* part_acc;   // partial sums, and per row {maximum, sum}
   float* part_ml;
-  int* recs;  // bf16: per CTA, the unit whose pieces start in it
+  int4* recs;  // bf16: per CTA and slot, what piece it holds
   int32_t* status;
 };
 
@@ -60,7 +59,7 @@ struct ExpandedParams {
   // bf16: partial states of units cut in pieces, and per CTA a record; null: units are not cut
   float4* part_acc;   // [slot][D / 4][rows of a unit]
   float2* part_ml;    // [slot][rows]: maximum, sum
-  int* recs;
+  int4* recs;
 };
 
 // fp32: CUDA cores.

@@ -74,7 +74,7 @@ LatentWs latent_ws(const pa_latent_layout* L, int num_tokens, int max_query_len,
   }
   w.acc = take(rows * L->latent_size * sizeof(float));
   w.ml = take(rows * 2 * sizeof(float));
-  w.recs = take(kLatentMaxCtas * kLatentRecWords * sizeof(int));
+  w.recs = take(2 * kLatentMaxCtas * sizeof(int4));
   w.total = off;
   return w;
 }
@@ -206,7 +206,7 @@ int pa_latent_forward(const void* q, const void* cache, const int32_t* block_tab
   p.scale_log2 = scale * 1.4426950408889634f;
   p.part_acc = reinterpret_cast<float*>(ws + w.acc);
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
-  p.recs = reinterpret_cast<int*>(ws + w.recs);
+  p.recs = reinterpret_cast<int4*>(ws + w.recs);
   p.status = status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (layout->dtype == PA_F32) {
@@ -223,7 +223,7 @@ static LatentWs expanded_ws(const pa_expanded_layout* L, int num_tokens, int max
   if (rows == 0) return w;
   w.ml = align256(rows * L->head_size * sizeof(float));
   w.recs = align256(w.ml + rows * 2 * sizeof(float));
-  w.total = align256(w.recs + kLatentMaxCtas * kLatentRecWords * sizeof(int));
+  w.total = align256(w.recs + 2 * kLatentMaxCtas * sizeof(int4));
   return w;
 }
 
@@ -290,7 +290,7 @@ int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, c
     char* ws = static_cast<char*>(workspace);
     p.part_acc = reinterpret_cast<float4*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-    p.recs = reinterpret_cast<int*>(ws + w.recs);
+    p.recs = reinterpret_cast<int4*>(ws + w.recs);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return done(L->dtype == PA_F32 ? launch_expanded_cc(p, L->head_size, st)

@@ -291,10 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------ units and copies
-    if (lane == 0) {
-      p.recs[blockIdx.x * kLatentRecWords + 3] = 0;
-      p.recs[blockIdx.x * kLatentRecWords + 4] = 0;
-    }
+    if (lane < 2) p.recs[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
+    __syncwarp();
     int uc = 0;        // units published
     uint32_t g = 0;    // tiles copied
     bool ok = !*abort;
@@ -374,16 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (u.t0 >= t1) continue;
           u.n = t1 - u.t0;
           u.slot = u.n == nk ? -1 : static_cast<int>(blockIdx.x) * 2 + (u.t0 == 0);
-          if (u.slot >= 0 && u.t0 == 0 && lane == 0) {
-            int* rec = p.recs + blockIdx.x * kLatentRecWords;
-            rec[0] = u.row0;
-            rec[1] = u.rows;
-            rec[2] = ways;
-            rec[3] = group_of(f + nk - 1, total, sh.groups) - sh.group + 1;
+          if (u.slot >= 0 && lane == 0) {
+            const int first = group_of(f, total, sh.groups);
+            p.recs[u.slot] = make_int4(u.row0, u.rows, sh.group - first, group_of(f + nk - 1, total, sh.groups) - first + 1);
           }
-          // (a CTA of a later piece helps joining: how many CTAs before it the first piece lies)
-          if (u.t0 > 0 && lane == 0)
-            p.recs[blockIdx.x * kLatentRecWords + 4] = (sh.group - group_of(f, total, sh.groups)) * ways;
           ok = run(u);
         }
         pos += static_cast<long long>(s.units) * s.len;
@@ -733,31 +725,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of units that a border cut, in the order of their keys.  The CTA that held a unit's
-// first piece has left a record; 8 CTAs a record.  Where there are few pieces, a warp of these
-// joins a row's one after the other; else the 8 CTAs of every piece take a row each, and
-// their warps every eighth piece of it.
+// Joins the pieces of units that a border cut, in the order of their keys.  Every piece has left a record
+// {first row, rows, piece, pieces}, and 8 CTAs a piece take part: a warp a row, or of many
+// pieces a CTA a row and a warp of it every eighth piece.  16 float4 a lane are loaded at once, as
+// the time is that of a few loads that wait for one another.
 template <int R, int N>
-__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) {
+__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, int ways) {
   constexpr int kVec = R / 128;  // float4 of a lane
-  constexpr int kFew = 8;
+  constexpr int kAtOnce = 16 / kVec, kFew = 8;
   __shared__ float4 acc_s[8][R / 4];
   __shared__ float2 ml_s[8];
   wait_prior_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int back = p.recs[blockIdx.x * kLatentRecWords + 4];
-  // the unit that begins in this CTA's stretch, then the one that goes on in it
-  for (int own = 1; own >= 0; --own) {
-    if (!own && back == 0) break;
-    const int first = blockIdx.x - (own ? 0 : back);  // CTA of the first piece
-    const int* rec = p.recs + first * kLatentRecWords;
-    const int row0 = rec[0], rows = rec[1], ways = rec[2], pieces = rec[3];
+  const int4 recs[2] = {p.recs[blockIdx.x * 2], p.recs[blockIdx.x * 2 + 1]};
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int4 rec = which ? recs[1] : recs[0];
+    const int rows = rec.y, piece = rec.z, pieces = rec.w;
+    if (pieces == 0) continue;
+    const int first = blockIdx.x - piece * ways;  // CTA of the first piece
     const bool few = pieces <= kFew;
-    if (pieces == 0 || (few && !own)) continue;
-    // piece k: the first CTA's slot 1, then slot 0 of the following ones
-    auto slot = [&](int k) { return (static_cast<long long>(first + k * ways) * 2 + (k == 0)) * N; };
-    const int n = few ? blockIdx.y * 8 + warp : (own ? 0 : back / ways) * 8 + blockIdx.y;
-    if (n >= rows) continue;  // (a whole CTA where its warps share a row)
+    const int k0 = few ? 0 : warp, dk = few ? 1 : 8;
+    const int n = few ? (piece * 8 + blockIdx.y) * 8 + warp : piece * 8 + blockIdx.y;
+    if (n >= rows) continue;  // (a whole CTA where its warps share a row; 8 pieces are CTAs enough for 64)
     float m = -CUDART_INF_F, l = 0.f;
     float4 acc[kVec];
 #pragma unroll
@@ -776,22 +766,23 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) 
         acc[i].w = acc[i].w * fa + x[i].w * fb;
       }
     };
-    const int k0 = few ? 0 : warp, dk = few ? 1 : 8;
-    for (int k = k0; k < pieces; k += 2 * dk) {  // two pieces' loads at once
-      float2 ml[2];
-      float4 x[2][kVec];
+    for (int k = k0; k < pieces; k += kAtOnce * dk) {
+      float2 ml[kAtOnce];
+      float4 x[kAtOnce][kVec];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool is = k + j * dk < pieces;
-        const long long row = slot(is ? k + j * dk : k) + n;
-        ml[j] = reinterpret_cast<const float2*>(p.part_ml)[row];
-        if (!is) ml[j].y = 0.f;
-        const float4* src = reinterpret_cast<const float4*>(p.part_acc + row * R);
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = k + j * dk;
+        ml[j].y = 0.f;
+        if (i < pieces) {  // piece i: the first CTA's slot 1, then slot 0 of the following ones
+          const long long row = (static_cast<long long>(first + i * ways) * 2 + (i == 0)) * N + n;
+          ml[j] = reinterpret_cast<const float2*>(p.part_ml)[row];
+          const float4* src = reinterpret_cast<const float4*>(p.part_acc + row * R);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) x[j][i] = src[i * 32 + lane];
+          for (int c = 0; c < kVec; ++c) x[j][c] = src[c * 32 + lane];
+        }
       }
-      add(ml[0], x[0]);
-      add(ml[1], x[1]);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) add(ml[j], x[j]);
     }
     if (!few) {
       __syncthreads();  // (the row before is read)
@@ -808,7 +799,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) 
       }
     }
     const float inv = 1.f / l;
-    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(row0 + n) * R);
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(rec.x + n) * R);
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
       out[i * 32 + lane] = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
@@ -872,7 +863,7 @@ cudaError_t launch_latent(const LatentParams& p, int num_sms, cudaStream_t strea
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, latent_join_kernel<R, N>, p);
+  return cudaLaunchKernelEx(&cfg, latent_join_kernel<R, N>, p, ways);
 }
 
 }  // namespace
