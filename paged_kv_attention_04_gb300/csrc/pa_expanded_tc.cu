@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool dealt = !p.part_acc && p.num_seqs <= 32;
   ESpan mine{};
   int err = 0;
-  if (dealt && warp == kCopyWarp && lane < p.num_seqs) err = span_of(p, lane, mine);
   if (tid == 0) {
     for (int i = 0; i < eNumBars; ++i) {
       uint32_t n = 1;
@@ -195,6 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_fence_init();
   }
   if (warp == 0) tmem_alloc(smem_u32(&sm.tmem), 512);
+  wait_prior_grid();  // (the lengths, like everything else, may be the kernel's before)
+  launch_dependents();  // (the joining kernel's launch; it waits for this grid)
+  if (dealt && warp == kCopyWarp && lane < p.num_seqs) err = span_of(p, lane, mine);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -258,8 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  wait_prior_grid();
-  launch_dependents();  // (the joining kernel's launch; it waits for this grid)
 
   if (warp >= kCopyWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
@@ -706,6 +706,7 @@ template <int D>
 __global__ void __launch_bounds__(256) expanded_join_kernel(const ExpandedParams p) {
   constexpr int kAtOnce = 4;
   wait_prior_grid();
+  launch_dependents();
   const int4 recs[2] = {p.recs[blockIdx.x * 2], p.recs[blockIdx.x * 2 + 1]};
 #pragma unroll
   for (int which = 0; which < 2; ++which) {

@@ -49,7 +49,7 @@ constexpr int kAhead = 2;           // tiles that are prefetched to L2 behind th
 constexpr float kGrowth = 8.f;      // base-2 growth of a maximum that moves the reference
 constexpr int kUnitCost = 2;        // what a unit costs beside its tiles, in tiles
 constexpr int kMinStretch = kUnitCost + 1;  // shortest stretch of the line for a CTA: a unit of one tile
-constexpr int kWholeTiles = 6;      // units of up to so many tiles are not cut: joining costs 5 us
+constexpr int kWholeTiles = 6;      // units of up to so many tiles are not cut: a join costs 3.5 us
 
 template <int R, int N>
 struct Cfg {
@@ -165,8 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sm.abort;
   auto bar = [&](int i) { return smem_u32(&sm.bars[i]); };
 
-  // ---- this CTA's place, and this thread's requests of the step (the first one's loads are on
-  // their way while the barriers are set up)
+  // ---- this CTA's place, and this thread's requests of the step
   Shape sh;
   sh.ways = ways;
   sh.way = blockIdx.x % ways;
@@ -174,8 +173,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   sh.groups = gridDim.x / ways;
   const int per = (p.num_seqs + kThreads - 1) / kThreads;
   const int ra = min(tid * per, p.num_seqs), rb = min(ra + per, p.num_seqs);
-  Span s0{};
-  int err = ra < rb ? span_of<N>(p, sh, ra, s0) : 0;
 
   if (tid == kCopyWarp * 32) {
     prefetch_map(&maps.q);
@@ -199,6 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_fence_init();
   }
   if (warp == 0) tmem_alloc(smem_u32(&sm.tmem), 512);
+  wait_prior_grid();  // (the lengths, like everything else, may be the kernel's before)
+  launch_dependents();  // (the joining kernel's launch; it waits for this grid)
+  Span s0{};
+  int err = ra < rb ? span_of<N>(p, sh, ra, s0) : 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -257,8 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  wait_prior_grid();
-  launch_dependents();  // (the joining kernel's launch; it waits for this grid)
 
   // ---- what both copy warps do: part h of the tiles of a unit
   // table entries of the pages of 8 tiles, one a lane: of group i of unit u, -1 past the request's keys
@@ -736,6 +735,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, 
   __shared__ float4 acc_s[8][R / 4];
   __shared__ float2 ml_s[8];
   wait_prior_grid();
+  launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 recs[2] = {p.recs[blockIdx.x * 2], p.recs[blockIdx.x * 2 + 1]};
 #pragma unroll 1

@@ -205,6 +205,31 @@ def test_repeats_streams_and_graph():
     assert torch.equal(ds[0]["out"], first[1])
 
 
+@pytest.mark.parametrize("q_lens,seq_lens", [([3, 150], [40, 150]), ([200], [2500])])
+def test_starts_of_the_kernel_before(q_lens, seq_lens):
+    """Captured calls whose starts the kernel right before each writes."""
+    step = Prompts(2, 64, q_lens, seq_lens, seed=13)
+    d = step.gpu()
+    want = step.run()["out"]
+    zero, outs = torch.zeros_like(d["qsl"]), [torch.empty_like(d["out"]) for _ in range(4)]
+    q0, k0 = d["qsl"].clone(), d["kvsl"].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for out in outs:
+            torch.add(k0, zero, out=d["kvsl"])
+            torch.add(q0, zero, out=d["qsl"])
+            step.run({**d, "out": out})
+            d["qsl"].zero_()
+            d["kvsl"].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    step.check({"out": want})
+    assert int(d["status"].item()) == 0
+    for out in outs:
+        assert torch.equal(out, want)
+
+
 def test_cut_units_on_another_stream():
     """The workspace that the call takes itself belongs to the stream it runs on: memory that work on the current
     stream still reads is not given to it."""

@@ -320,6 +320,28 @@ def test_streams_and_graph():
     check(d["out"], want, mag, BF16, steps[0].logit_size(), 576)
 
 
+@pytest.mark.parametrize("seq_lens", [[40, 7, 130], [900, 130, 2000]])
+def test_lengths_of_the_kernel_before(seq_lens):
+    """A captured loop of steps whose lengths the kernel right before each call moves on."""
+    step = Step(16, 256, [1] * 3, seq_lens, seed=40)
+    d = step.gpu()
+    outs = [torch.empty_like(d["out"]) for _ in range(6)]
+    step.run(d)  # (takes the workspace)
+    d["seq"] -= len(outs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for out in outs:
+            d["seq"].add_(1)
+            step.run({**d, "out": out}, max_q=1, max_s=max(seq_lens))
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        step.seq_lens = np.asarray(seq_lens) - len(outs) + 1 + i
+        want, mag = step.want()
+        check(out, want, mag, BF16, step.logit_size(), 320)
+
+
 def test_cache_past_4_gib():
     """Slots whose bytes lie past 32 bits: written, read back and attended over."""
     heads, r, n = 4, 512, 300
