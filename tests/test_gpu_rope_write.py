@@ -89,6 +89,29 @@ def test_bits(tokens, hq, hkv, d, n, dtype, cache, pairs):
     assert (np.abs(q_out.double().cpu().numpy() - exact) <= eps * np.abs(exact) * (1 + 2 ** -7) + 4 * 2.0 ** -24 * 2 * big).all()
 
 
+@pytest.mark.parametrize("tokens,hq,hkv,d,cache", [(60000, 3, 3, 64, None), (45000, 4, 1, 128, None), (30000, 3, 3, 128, None),
+                                                   (33000, 8, 1, 128, P.PA_INT4)])
+def test_many_tokens(tokens, hq, hkv, d, cache):
+    """Steps whose rows are taken two at a time (odd numbers of them too), with skipped tokens: as in parts."""
+    lay, qkv, q, k, v, pos, tab, slots, kc, vc = case(tokens, hq, hkv, d, 32, BF16, cache, seed=7)
+    slots[::97] = -1
+    gq, gk, gv = on_gpu(qkv, hq, hkv, d)
+    gpos, gtab, gslots = pos.cuda(), tab.cuda(), slots.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    whole, parts = (kc.cuda(), vc.cuda()), (kc.cuda(), vc.cuda())
+    q_out, q_parts = (torch.zeros(tokens, hq, d, dtype=BF16, device="cuda") for _ in range(2))
+    P.pa_rope_cache_write(gq, gk, gv, gpos, gtab, gslots, q_out, *whole, lay, status=status)
+    for i in range(0, tokens, 5000):
+        at = slice(i, i + 5000)
+        P.pa_rope_cache_write(gq[at], gk[at], gv[at], gpos[at], gtab, gslots[at], q_parts[at], *parts, lay, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(bits(q_out), bits(q_parts))
+    assert torch.equal(bits(q_out[-3000:]), bits(rotated(q[-3000:], tab, pos[-3000:], False)))
+    for a, b in zip(whole, parts):
+        assert torch.equal(bits(a), bits(b))
+
+
 def test_in_place_and_keys_alone():
     lay, qkv, q, k, v, pos, tab, slots, kc, vc = case(33, 8, 2, 128, 128, seed=5)
     gq = q.contiguous().cuda()
