@@ -10,17 +10,18 @@
 // O' += L' P' (M = 128 numbers of the latent, R / 128 of them, N rows, K = 64 keys).  N is
 // 16, 32 or 64 query rows, a row being a (token, head) of a request.  O' takes R / 128 x N
 // columns of tensor memory: 64 rows of 512 are half of it.
-// The 64-key tile lies in shared memory as four 16-token pages, each one TMA box:
+// The 64-key tile lies in shared memory as four 16-token pages (a TMA box per 8 keys and part):
 //   [8-key group][64-number slice][8 keys][128 bytes], 128-byte swizzle.
 // Read with the keys as rows (K-major) it is A of the first product, with the numbers
 // as rows (MN-major) A of the second, so there is one copy of it.
 //
-// Roles: warps 0-3 and 4-7 softmax and output of half of the query rows each, warp 8 units and copies (of
-// Q and of the first part of every tile, warp 11 of the second), warps 9 and 10 the issue of S and of O.  Two 64-key tiles of R = 512 fill shared memory, and a tile stays for its
-// copy (2 us from HBM), S, softmax and O, so this chain is kept short: the copies of the tiles
-// after them are begun as prefetches to L2; a tile comes and goes in two parts (half of the latent
-// each, the second with the key part), S beginning on the first and O freeing it; P takes the
-// place of the key part, which only S reads; O does not wait for the issue of the next S.
+// Roles: warps 0-3 and 4-7 softmax and output of half of the query rows each, warp 8 units and copies
+// (of Q and of the first part of every tile, warp 11 of the second), warps 9 and 10 the issue of S and of
+// O.  Two 64-key tiles of R = 512 fill shared memory, and a tile stays for its copy (2 us from HBM),
+// S, softmax and O, so this chain is kept short: the copies of the tiles after them are begun as
+// prefetches to L2; a tile comes and goes in two parts (half of the latent each, the second with the key
+// part), S beginning on the first and O freeing it; P takes the place of the key part, which only
+// S reads; O does not wait for the issue of the next S.
 // S' has a key per TMEM lane (16 of every 32) and is read as matrix fragments: column maxima by
 // shuffles over lanes and a trade between the four warps in shared memory.  The reference
 // of a column moves only when its maximum grows by more than 2^8; P is written transposed
@@ -29,6 +30,10 @@
 // Work: units (request, N rows) lie on a line, each as long as its keys' tiles plus a
 // constant; every CTA takes an equal stretch, computed by itself from the lengths.  Units
 // cut by a border leave partial states (at most two a CTA) that a second kernel joins in order.
+//
+// Measured (R = 512): 256 decodes of 32 heads over a median of 1024 keys 82 us (383 MB, 57 us at the copy
+// bandwidth), 16 of 16 heads over 32768 to 131072 keys 250 us (228), 48 requests of 2 to 8 tokens of 32
+// heads after 256 to 4096 keys 75 us (bound by the chain above).
 #include <math_constants.h>
 
 #include "pa_latent.h"
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, 
   __shared__ float4 acc_s[8][R / 4];
   __shared__ float2 ml_s[8];
   wait_prior_grid();
-  launch_dependents();
+  launch_dependents();  // a following kernel may set up; it waits for this grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 recs[2] = {p.recs[blockIdx.x * 2], p.recs[blockIdx.x * 2 + 1]};
 #pragma unroll 1
