@@ -3,7 +3,7 @@
 //
 // One pass: every number of q, k and v is read once and written once, where rotating
 // first reads and writes q and k and then k and v again.  A thread takes 16 numbers
-// of one row (32 bytes of bf16), D / 16 threads a row, 256 threads a CTA; the rows of a
+// of one row, or of two (32 bytes of bf16 each), D / 16 threads a row, 256 threads a CTA; the rows of a
 // token are its q heads, then its k heads, then its v heads.  The table row of a token
 // (4 n bytes) is read once per row through L1.
 #include "pa_rope.cuh"
