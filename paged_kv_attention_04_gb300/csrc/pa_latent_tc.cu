@@ -64,6 +64,10 @@ struct Cfg {
   static constexpr int kTileBytes = kPages * kPageBytes;
   static constexpr int kQBytes = N * (R + kLatentRope) * 2;  // [slice][N rows][128 bytes]
   static constexpr int kBufs = R == 512 ? 2 : 4;   // tiles
+  // P's barriers, one a tile buffer: P of tile g + kBufs waits for the buffer, so for O of tile g, whose issue
+  // has then seen this phase.  (Of two in turn with four buffers, P of tile g + 2 could complete the barrier again
+  // before the issue of O looked for P of tile g.)
+  static constexpr int kPBars = kBufs;
   static constexpr int kQs = N == 64 ? 1 : 2;
   static constexpr int kQOff = kBufs * kTileBytes;
   static constexpr int kSmallOff = kQOff + kQs * kQBytes;
@@ -76,6 +80,7 @@ struct Cfg {
   static constexpr int kBlocks = R / 128;          // of 128 latent numbers
   static constexpr int kTmemS = 256;               // S of even and odd tiles behind O
   static_assert(kBlocks * N <= 256, "O fits beside S");
+  static_assert(kPBars <= 4 && (kPBars & (kPBars - 1)) == 0, "P's barriers; tile numbers wrap");
   static_assert(N <= kKeys, "P fits the key part");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds 227 KB");
 };
@@ -99,10 +104,10 @@ enum Bar : int {
   kKFull = 8,      // [4] TMA, the tile's first part; [4] its second
   kKEmpty = 16,    // [4] O += of the first part done: frees it; [4] the second's, and P
   kSFull = 24,     // [2] S done
-  kPFull = 26,     // [2] S read, P written, O rescaled (8 warps)
-  kTrade = 28,     // [2] the softmax warps of a half meet (4 warps)
-  kDrain = 30,     // [2]
-  kNumBars = 32
+  kPFull = 26,     // [4] S read, P written, O rescaled (8 warps), by buffer
+  kTrade = 30,     // [2] the softmax warps of a half meet (4 warps)
+  kDrain = 32,     // [2]
+  kNumBars = 34
 };
 
 // The line: what request r (rows a .. a + L - 1 of the step, S keys) takes of it.
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
       if (i == kUnitEmpty || i == kUnitEmpty + 1) n = 11;
-      if (i == kPFull || i == kPFull + 1) n = 8;
+      if (i >= kPFull && i < kTrade) n = 8;
       if (i == kTrade || i == kTrade + 1) n = 4;
       mbar_init(bar(i), n);
     }
@@ -436,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < n; ++t, ++g) {
           if (warp == kSWarp) {
             // S of tile g - 2 is read (phase -1 of a barrier counts as complete)
-            ok = wait_both(bar(kKFull + b), phase, bar(kPFull + (g & 1)), ((g >> 1) - 1) & 1, abort, p.status);
+            ok = wait_both(bar(kKFull + b), phase, bar(kPFull + (g - 2) % C::kPBars), ((g - 2) / C::kPBars) & 1, abort,
+                           p.status);
             if (!ok) break;
             tc_fence_after();
             constexpr uint32_t kId = idesc_bf16(kKeys, N, 0);
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(bar(kSFull + (g & 1)));
             if (t == n - 1) tc_commit(bar(kQEmpty + qs));
           } else {
-            ok = wait(kPFull + (g & 1), (g >> 1) & 1);
+            ok = wait(kPFull + b, phase);
             if (!ok) break;
             tc_fence_after();
             constexpr uint32_t kId = idesc_bf16(128, N, 0) | (1u << 15);  // A MN-major
@@ -655,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        warp_arrive(bar(kPFull + (g & 1)));
+        warp_arrive(bar(kPFull + g % C::kPBars));
       }
       if (!ok) break;
 
