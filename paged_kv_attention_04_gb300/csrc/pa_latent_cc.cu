@@ -47,9 +47,10 @@ __device__ bool starts_ok(const int32_t* starts, int n, int end) {
 // one key's logit x (base 2) into a running softmax; returns the key's weight,
 // `old` the factor of what was summed before
 __device__ __forceinline__ float softmax_step(float x, float& m, float& l, float& old) {
-  const float nm = fmaxf(m, x);
+  const float nm = fmaxf(m, x);  // (a NaN leaves the maximum as it is)
   old = m == nm ? 1.f : exp2f(m - nm);
-  const float w = nm == -CUDART_INF_F ? 0.f : exp2f(x - nm);  // (logits of -inf alone: 0 / 0 at the end)
+  // no finite logit yet: against 0, so that -inf weighs 0 (such logits alone: 0 / 0 at the end) and NaN is kept
+  const float w = exp2f(x - (nm == -CUDART_INF_F ? 0.f : nm));
   m = nm;
   l = l * old + w;
   return w;
