@@ -49,13 +49,24 @@ int check_latent(const pa_latent_layout* L) {
   return PA_OK;
 }
 
-// fp32: pieces of a request's keys, so that few rows fill the GPU.
+// fp32: pieces of a request's keys, so that few rows fill the GPU: as many as bring the CTAs to kCcCtas, of
+// 16 blocks at least.
+constexpr int kCcCtas = 4 * 152;
+long long cc_most_splits(int max_seq_len) { return cdiv(max_seq_len, 16 * kBlockSize); }
 int cc_splits(const pa_latent_layout* L, int num_tokens, int max_seq_len) {
   const long long rows = static_cast<long long>(num_tokens) * cdiv(L->num_heads, 8);
-  long long s = rows > 0 ? cdiv(4 * 152, rows) : 1;
-  const long long most = cdiv(max_seq_len, 16 * kBlockSize);
-  if (s > most) s = most;
-  return static_cast<int>(s < 1 ? 1 : s);
+  const long long s = rows > 0 ? cdiv(kCcCtas, rows) : 1, most = cc_most_splits(max_seq_len);
+  return static_cast<int>(s > most ? (most < 1 ? 1 : most) : s);
+}
+// Rows of partial states that a step of up to num_tokens tokens may leave: fewer tokens are cut into more
+// pieces, so this is a bound over all of them.  With A = ceil(kCcCtas / groups of heads), t tokens are cut where
+// t < A, into min(ceil(A / t), most) pieces, and t ceil(A / t) <= A + t - 1.
+size_t cc_partial_rows(const pa_latent_layout* L, int num_tokens, int max_seq_len) {
+  const long long most = cc_most_splits(max_seq_len), a = cdiv(kCcCtas, cdiv(L->num_heads, 8));
+  const long long t = num_tokens < a ? num_tokens : a - 1;
+  if (most <= 1 || t < 1) return 0;
+  const long long pieces = t * most < a + t - 1 ? t * most : a + t - 1;
+  return static_cast<size_t>(pieces) * L->num_heads;
 }
 
 struct LatentWs {
@@ -65,13 +76,8 @@ LatentWs latent_ws(const pa_latent_layout* L, int num_tokens, int max_query_len,
   LatentWs w{};
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
-  size_t rows;
-  if (L->dtype == PA_F32) {
-    const int s = cc_splits(L, num_tokens, max_seq_len);
-    rows = s == 1 ? 0 : static_cast<size_t>(num_tokens) * L->num_heads * s;
-  } else {
-    rows = latent_tc_partial_rows(L->num_heads, max_query_len);
-  }
+  const size_t rows = L->dtype == PA_F32 ? cc_partial_rows(L, num_tokens, max_seq_len)
+                                         : latent_tc_partial_rows(L->num_heads, max_query_len);
   w.acc = take(rows * L->latent_size * sizeof(float));
   w.ml = take(rows * 2 * sizeof(float));
   w.recs = take(2 * kLatentMaxCtas * sizeof(int4));
