@@ -439,7 +439,7 @@ typedef struct {
  * as for pa_latent_forward.
  *   workspace  device scratch of pa_expanded_workspace_size bytes, 256-byte aligned, with which the work
  *              of a few long requests is cut over the GPU's SMs (its contents need no initialisation);
- *              NULL: it is not (results differ in rounding alone)
+ *              NULL, or of 0 bytes: it is not (results differ in rounding alone)
  * Calls whose work overlaps on the GPU need workspaces of their own.
  */
 int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, const void* v,
@@ -448,8 +448,10 @@ int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, c
                         float scale, void* out, void* workspace, size_t workspace_bytes,
                         const pa_expanded_layout* layout, int32_t* status, void* stream);
 
-/* Bytes of workspace that are of use to pa_expanded_forward with these bounds (the layout's strides
- * do not matter): 0 where none is, or on bad arguments (see pa_last_error). */
+/* Bytes of workspace that are of use to a pa_expanded_forward of num_tokens tokens over up to max_kv_len
+ * keys a request (the layout's strides do not matter): 0 where none is, or on bad arguments (see
+ * pa_last_error).  Many tokens need none, so the size falls to 0 as num_tokens grows: for steps of
+ * several sizes take that of num_tokens 1, which no other exceeds. */
 size_t pa_expanded_workspace_size(const pa_expanded_layout* layout, int num_tokens, int max_kv_len);
 
 /* Message of the last failing call on this thread ("" if none). */

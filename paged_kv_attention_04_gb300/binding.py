@@ -616,7 +616,8 @@ def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max
 
 def pa_expanded_workspace_size(num_heads: int, head_size: int, num_tokens: int, max_kv_len: int,
                                dtype=torch.bfloat16, rope_size: int = 64) -> int:
-    """Bytes of workspace that are of use to pa_expanded_forward (0: none)."""
+    """Bytes of workspace that are of use to a pa_expanded_forward of num_tokens tokens (0: none); that of one
+    token serves steps of any number."""
     layout = pa_expanded_layout(num_heads, head_size, rope_size, _DTYPES[dtype])
     n = lib().pa_expanded_workspace_size(layout, num_tokens, max_kv_len)
     if n == 0 and last_error():

@@ -284,6 +284,7 @@ int pa_expanded_forward(const void* q, const void* k_nope, const void* k_rope, c
     return fail(PA_ERR_INVALID, "step too large for one call");
   if (workspace && !aligned(workspace, 256)) return fail(PA_ERR_INVALID, "workspace must be 256-byte aligned");
   const LatentWs w = expanded_ws(L, num_tokens, max_kv_len);
+  if (workspace_bytes == 0) workspace = nullptr;  // (sized for a larger step, whose units are not cut)
   if (workspace && workspace_bytes < w.total)
     return fail(PA_ERR_INVALID, "workspace of %zu bytes < %zu needed", workspace_bytes, w.total);
   int num_sms = 0;
