@@ -206,10 +206,11 @@ size_t pa_forward_workspace_size(const pa_layout* layout, int num_seqs, int num_
  *
  * The call's first kernel reads seq_lens and query_start_loc as soon as it
  * starts, which may be while the kernel before it in `stream` still runs, if
- * that kernel lets dependent launches start early (pa_cache_write does;
- * ordinary kernels, copies and event waits do not).  Such a kernel must not
- * write them.  Everything else pa_forward reads is read only after the
- * previous kernel has finished.
+ * that kernel lets dependent launches start early (those of pa_cache_write,
+ * pa_rope_cache_write, pa_latent_write and pa_latent_read do, and the bf16 ones
+ * of pa_latent_forward and pa_expanded_forward; ordinary kernels, copies and
+ * event waits do not).  Such a kernel must not write them.  Everything else
+ * pa_forward reads is read only after the previous kernel has finished.
  *
  * Streams: everything is ordered on `stream`.  When the step can hold bf16
  * chunks of at least 16 tokens (max_query_len >= 16), their tensor-core
@@ -387,8 +388,8 @@ size_t pa_latent_workspace_size(const pa_latent_layout* layout, int num_seqs, in
 /*
  * Attention over a latent cache, absorbed form.  Steps are described as for
  * pa_forward (query_start_loc, seq_lens, block_tables, bounds, workspace, status, skipped
- * requests, early reading of seq_lens and query_start_loc).  With L_p and K_p the latent and
- * the key part of position p,
+ * requests), but everything is read after the kernel before it in `stream` has finished, so
+ * that one may write the lengths.  With L_p and K_p the latent and the key part of position p,
  *   out[t][h] = sum_p softmax_p(scale * q[t][h] . [L_p, K_p]) L_p
  *   q    device [num_tokens][num_heads][latent_size + rope_size], contiguous, 16-byte aligned
  *   out  device [num_tokens][num_heads][latent_size], contiguous, 16-byte aligned
@@ -435,8 +436,8 @@ typedef struct {
  *   max_query_len, max_kv_len  host upper bounds of L and S
  * Pointers are 16-byte aligned, strides multiples of 16 bytes.  Requests with L < 1,
  * L > S or above a bound set PA_DEV_LENGTHS and their rows are left unwritten; bad start arrays
- * set PA_DEV_QSL and nothing is written.  Rounding, NaN and early reads (of both start arrays)
- * as for pa_latent_forward.
+ * set PA_DEV_QSL and nothing is written.  Rounding, NaN and when things are read as for
+ * pa_latent_forward.
  *   workspace  device scratch of pa_expanded_workspace_size bytes, 256-byte aligned, with which the work
  *              of a few long requests is cut over the GPU's SMs (its contents need no initialisation);
  *              NULL, or of 0 bytes: it is not (results differ in rounding alone)
