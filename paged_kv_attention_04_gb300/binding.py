@@ -549,6 +549,9 @@ def alloc_latent_workspace(layout: pa_latent_layout, num_seqs: int, num_tokens: 
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+_CUT_KEYS = 1024  # pa_expanded_forward cuts no shorter requests
+
+
 def _workspace(workspace, dev: int) -> tuple:
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _explain("workspace", workspace, dev, workspace.dtype, workspace.shape, None)
@@ -598,7 +601,7 @@ def pa_expanded_forward(q, k_nope, k_rope, v, query_start_loc, kv_start_loc, max
     ws, nbytes = None, 0
     if workspace is not None:
         ws, nbytes = _workspace(workspace, dev)
-    elif max_kv_len >= 1024:  # (shorter requests are never cut)
+    elif max_kv_len >= _CUT_KEYS:
         nbytes = lib().pa_expanded_workspace_size(layout, n, max_kv_len)
         if nbytes:
             if stream is None:

@@ -47,9 +47,17 @@ constexpr int kQSlice = kRows * 128, kKSlice = kKeys * 128;  // bytes of 64 numb
 constexpr float kGrowth = 8.f;
 constexpr int kUnitCost = 0;       // what a unit costs beside its key tiles (measured: nothing, its start
                                    // and output run beside other units' products)
-constexpr int kMinPiece = 6;       // fewest key tiles of a piece
-constexpr int kCutKeys = 1024;     // units are cut where a request may be this long ...
-constexpr int kCutUnits = 5;       // ... and a CTA gets fewer units than this
+// Fewest key tiles of a piece.  32 heads, 2048 rows over 8192 keys: 220 us with 3, 221 with 6, 226 with 12, 247 with
+// 24; few short units (4 heads, 300 rows over 3000 keys) 20, 24, 37 and 55.
+constexpr int kMinPiece = 6;
+// Units are cut where a request may be this long and a CTA would get fewer units than kCutUnits if the step's rows
+// were one request's (requests of few rows are more units than that).  Measured in us, cut and whole, D = 128, 32 heads
+// unless said: rows over 8192 keys: 32: 37 and 78, 256: 51 and 134, 1024: 128 and 136, 2048: 221 and 233, 4096 (3.4
+// units a CTA): 360 and 380, 8192 (6.7): 494 and 490; 96 heads, 2048 rows (5.1): 630 and 750.  256 rows over 512 keys:
+// 18 and 14, over 1024: 27 and 22, over 2048: 28 and 38.  What the rule does not look at, and cuts at a loss: prompts
+// with few earlier tokens (2048 rows over 2048 keys 55 and 41, 4096 over 4096 150 and 131) and many short
+// chunks (64 of 32 rows over 4128 keys 783 and 720).
+constexpr int kCutKeys = 1024, kCutUnits = 5;
 
 template <int D>
 struct ECfg {
@@ -704,8 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of cut units, in the order of their keys.  Every piece has left a record {first row,
-// rows, head, piece and pieces}, and 8 CTAs a piece take part; a lane a row, a warp 8 of its numbers,
-// 4 pieces' loads at once.
+// rows, head, piece and pieces}, and has 8 CTAs; a lane a row, a warp 8 of its numbers, 4 pieces' loads at
+// once.  The unit's D warps of work go to the pieces in order, 64 a piece: those of the first piece take
+// all of D = 64, those of the first two all of D = 128.
 template <int D>
 __global__ void __launch_bounds__(256) expanded_join_kernel(const ExpandedParams p) {
   constexpr int kAtOnce = 4;

@@ -6,8 +6,12 @@
 // (R + 64 products, five shuffles) and an update of R sums, held by the lanes.  The running
 // maximum and sum of the softmax move with every block, so the keys are read once.  A request's
 // keys are cut into `splits` pieces so that few requests fill the GPU; a second kernel
-// joins the pieces in order.  Bound by instruction issue.
+// joins the pieces in order.  Bound by instruction issue: a key costs five shuffles that wait for one another.
 // Expanded: the same with a warp per (token, head) and that head's own keys.
+//
+// Measured: absorbed (R = 512) 32 decodes of 16 heads over 1024 keys 116 us, 256 of 32 heads 1290 us (14 TFLOP/s),
+// 2 of 16 heads over 32768 keys 244 us; expanded (D = 128) 512 tokens of 16 heads 268 us, 2048 of 32
+// heads 6.0 ms (7 TFLOP/s).
 #include <math_constants.h>
 
 #include "pa_device.cuh"

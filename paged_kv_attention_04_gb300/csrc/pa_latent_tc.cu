@@ -33,7 +33,8 @@
 //
 // Measured (R = 512): 256 decodes of 32 heads over a median of 1024 keys 82 us (383 MB, 57 us at the copy
 // bandwidth), 16 of 16 heads over 32768 to 131072 keys 250 us (228), 48 requests of 2 to 8 tokens of 32
-// heads after 256 to 4096 keys 75 us (bound by the chain above).
+// heads after 256 to 4096 keys 75 us (bound by the chain above).  So are decodes of more heads: 256 of 64
+// heads over that median 94 us (60), of 128 heads 134 us (65), 16 of 128 heads over 8192 to 32768 keys 126 us (58).
 #include <math_constants.h>
 
 #include "pa_latent.h"
@@ -736,9 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of units that a border cut, in the order of their keys.  Every piece has left a record
-// {first row, rows, piece, pieces}, and 8 CTAs a piece take part: a warp a row, or of many
-// pieces a CTA a row and a warp of it every eighth piece.  16 float4 a lane are loaded at once, as
-// the time is that of a few loads that wait for one another.
+// {first row, rows, piece, pieces}, and has 8 CTAs.  Of up to 8 pieces those of the first one join, a warp a row
+// (64 rows at most); of more, all pieces' CTAs, each a row in turn and a warp of it every eighth piece.
+// 16 float4 a lane are loaded at once, as the time is that of a few loads that wait for one another.
 template <int R, int N>
 __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, int ways) {
   constexpr int kVec = R / 128;  // float4 of a lane

@@ -7,7 +7,8 @@
 // A warp takes either a token's cache row (a lane R / 32 numbers of the latent in chunks of
 // 16 bytes that lie side by side over the warp; four lanes the key part) or the
 // parts of 16 of its heads (four lanes a head, eight heads at once, their loads ahead of the position:
-// 34.3 us for 16384 tokens of 32 heads, 75 % of the copy bandwidth; with 8 heads a warp 40.9, with 32 37.0).
+// 34.3 us for 16384 tokens of 32 heads, 75 % of the copy bandwidth; with 8 heads a warp 40.9, with 32 37.0;
+// fp32 69 us, 75 % too).
 #include "pa_latent.h"
 #include "pa_rope.cuh"
 

@@ -141,7 +141,7 @@ cudaError_t launch_rope_write(const RopeWriteArgs& a, const pa_layout& L, cudaSt
   const bool d64 = L.head_size == 64;
   if (L.cache_dtype == PA_INT4) {
     // k and v by the 4-bit slot write's kernel, which quantises whole groups of a
-    // row; q by the kernel above
+    // row; q by the kernel above (32768 tokens of 32 / 8 heads, D 128: 170-180 us, 109 at the copy bandwidth; 2048: 18)
     p.kv_rows = 0;
     const cudaError_t e = d64 ? launch<__nv_bfloat16, 64, false>(p, stream)
                               : launch<__nv_bfloat16, 128, false>(p, stream);

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import paged_kv_attention_04_gb300 as P
+from paged_kv_attention_04_gb300 import binding
 from latent_cases import Step, check
 from test_gpu_expanded import Prompts
 
@@ -59,6 +60,7 @@ def test_expanded_size_of_one_token_is_the_largest():
         for n in (1000, 1024, 8192, 100000):
             assert max(size(heads, head_size, t, n) for t in range(1, 50000, 777)) <= size(heads, head_size, 1, n)
         sizes = [size(heads, head_size, 1, n) for n in (1, 1000, 1024, 8192, 1 << 20)]
+        assert size(heads, head_size, 1, binding._CUT_KEYS - 1) == 0 < size(heads, head_size, 1, binding._CUT_KEYS)
         assert sizes == sorted(sizes)
 
 
